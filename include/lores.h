@@ -362,6 +362,135 @@ int lores_dequant_state(const lores_state *st, float *out, void *stream);
 int lores_quant_state(lores_state *st, const float *X, uint64_t seed, int64_t seq_base,
                       int64_t head_base, void *stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Sequence operators: the same recurrence over whole sequences at full
+ * precision (prompts, training), and the norm next to it.
+ * ------------------------------------------------------------------------
+ */
+
+/* Shapes of a scan.  Strides are in elements, between sequences, tokens and
+ * heads; the last dimension is contiguous.  Any stride >= 0 will do (0
+ * broadcasts); 16-byte aligned q and k rows are read faster. */
+typedef struct {
+    int32_t B, T;              /* sequences (1 .. 65535), tokens (0 .. 2^28)            */
+    int32_t H, H_k;            /* value heads (as lores_state_alloc), and query / key
+                                  heads: H_k divides H, and value head h reads
+                                  query / key head h / (H / H_k)                       */
+    int32_t d_k, d_v;          /* as lores_state_alloc                                  */
+    int32_t in_bf16;           /* q, k, v, o and their gradients: bf16 (1) or fp32 (0)  */
+    int32_t delta;             /* 0 or 1 (delta rule)                                   */
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+} lores_scan_dims;
+
+/* Bytes of device workspace a lores_scan (backward = 0) or a
+ * lores_scan_backward (1) of these shapes needs (host out; may be 0). */
+int lores_scan_workspace(const lores_scan_dims *dims, int32_t backward, size_t *bytes);
+
+/*
+ * lores_scan - the general recurrence over T tokens without quantization,
+ *   S_t = S_{t-1} alpha_t (I - delta beta_t k_t k_t^T) + beta_t v_t k_t^T,
+ *   o_t = S_t q_t
+ * ("Introduction and Theoretical Foundation", scalar decay per head): the
+ * prompt of a layer whose decoding lores_decode_step runs.  S_last has the
+ * layout that lores_quant_state takes.
+ *   q, k       device [B][T][H_k][d_k] by strides
+ *   v          device [B][T][H][d_v] by strides
+ *   alpha      device [B][T][H] fp32 decay in [0, 1] (0 forgets everything)
+ *   beta       device [B][T][H] fp32 write gate
+ *   lengths    device [B] int32, or NULL: sequence b has lengths[b] tokens
+ *              (values outside [0, T] are taken as 0 and T); nothing behind
+ *              them is read, and o is 0 there
+ *   S_first    device [B][H][d_v][d_k] fp32, 16-byte aligned, or NULL: zero
+ *   o          device out [B][T][H][d_v] contiguous, the inputs' type
+ *   S_last     device out [B][H][d_v][d_k] fp32, 16-byte aligned, or NULL;
+ *              may be S_first
+ *   work       device workspace, 256-byte aligned, of at least
+ *              lores_scan_workspace bytes (NULL if that is 0); its contents
+ *              do not matter before or after
+ * The state and every sum are held to fp32 accuracy for either input type;
+ * bf16 outputs are rounded once.  Caller preconditions not checked: finite
+ * inputs, and for delta = 1 |k| = 1 and beta in (0, 2).  Nothing is launched
+ * on an error.
+ */
+int lores_scan(const lores_scan_dims *dims, const void *q, const void *k, const void *v,
+               const float *alpha, const float *beta, const int32_t *lengths,
+               const float *S_first, void *o, float *S_last, void *work, size_t work_bytes,
+               void *stream);
+
+/*
+ * lores_scan_backward - gradients of lores_scan's inputs from those of its
+ * outputs; the forward pass is recomputed from the inputs, nothing is kept
+ * between the calls.
+ *   q .. S_first  as given to lores_scan
+ *   dout       device [B][T][H][d_v] contiguous, the inputs' type
+ *   dS_last    device [B][H][d_v][d_k] fp32, 16-byte aligned, or NULL: zero
+ *   dq, dk     device out [B][T][H_k][d_k] contiguous, the inputs' type
+ *              (summed over the value heads that share them, in head order)
+ *   dv         device out [B][T][H][d_v] contiguous, the inputs' type
+ *   dalpha, dbeta  device out [B][T][H] fp32 (also where alpha is 0)
+ *   dS_first   device out [B][H][d_v][d_k] fp32, 16-byte aligned, or NULL
+ *   work       as for lores_scan, of lores_scan_workspace(dims, 1) bytes
+ * Gradients of tokens behind lengths[b] are 0.  Results do not depend on
+ * scheduling: the same call gives the same bits.
+ */
+int lores_scan_backward(const lores_scan_dims *dims, const void *q, const void *k, const void *v,
+                        const float *alpha, const float *beta, const int32_t *lengths,
+                        const float *S_first, const void *dout, const float *dS_last, void *dq,
+                        void *dk, void *dv, float *dalpha, float *dbeta, float *dS_first,
+                        void *work, size_t work_bytes, void *stream);
+
+#define LORES_MAX_NORM 16384 /* columns of a normed row */
+
+/*
+ * lores_rmsnorm - root-mean-square norm of rows, with the residual's addition
+ * and an output in 8 bits with one scale per row:
+ *   h = rnd(x + residual) in the inputs' type (x itself without a residual),
+ *   z_j = fl(h_j w_j),  r = (mean_j h_j^2 + eps)^(-1/2),  y_j = rnd(z_j r)
+ *   out_prec LORES_INT8: m = max_j |z_j|, code_j = z_j fl(127 fl(1 / m)) rounded to
+ *     nearest (ties to even), scale = fl(fl(m / 127) r): y_j ~ scale code_j
+ *   out_prec LORES_FP8: the same with 448 and E4M3 values
+ * A row of zeros has the scale 0.  A row with an infinity or NaN has the
+ * scale NaN.
+ *   x          device [rows][n], in_bf16 ? bf16 : fp32, rows x_stride elements
+ *              apart; 1 <= n <= LORES_MAX_NORM, 0 <= rows < 2^31
+ *   residual   device [rows][n] of x's type, rows res_stride apart, or NULL
+ *   weight     device [n], w_bf16 ? bf16 : fp32
+ *   out_prec   LORES_FP32, LORES_BF16, LORES_INT8 or LORES_FP8
+ *   y          device out [rows][n] contiguous (int8 codes, E4M3 bytes)
+ *   scales     device out [rows] fp32 (8-bit outputs; else unused)
+ *   h          device out [rows][n] contiguous, x's type (with a residual;
+ *              else unused); may be x or residual if that is contiguous
+ */
+int lores_rmsnorm(const void *x, int64_t x_stride, const void *residual, int64_t res_stride,
+                  const void *weight, int32_t w_bf16, int64_t rows, int32_t n, int32_t in_bf16,
+                  float eps, int32_t out_prec, void *y, float *scales, void *h, void *stream);
+
+/* Bytes of device workspace of a lores_rmsnorm_backward (host out). */
+int lores_rmsnorm_workspace(int64_t rows, int32_t n, size_t *bytes);
+
+/*
+ * lores_rmsnorm_backward - gradients of y = h r w (LORES_FP32 / LORES_BF16
+ * output, before its rounding):
+ *   dx_j = r (w_j dy_j - h_j r^2 mean_i(w_i dy_i h_i)) + dresidual_j
+ *   dw_j = sum over rows of dy_j h_j r
+ *   h          device [rows][n] of in_bf16's type, rows h_stride apart: the
+ *              sum that lores_rmsnorm stored (x without a residual)
+ *   dy         device [rows][n] contiguous, h's type
+ *   dresidual  device [rows][n] contiguous, h's type: the gradient that
+ *              reaches h by other ways, or NULL
+ *   dx         device out [rows][n] contiguous, h's type: the gradient of x
+ *              and of the residual alike; may be dy or dresidual
+ *   dw         device out [n] fp32
+ *   work       device workspace of lores_rmsnorm_workspace bytes, 16-byte
+ *              aligned
+ * Results do not depend on scheduling.
+ */
+int lores_rmsnorm_backward(const void *h, int64_t h_stride, const void *weight, int32_t w_bf16,
+                           const void *dy, const void *dresidual, int64_t rows, int32_t n,
+                           int32_t in_bf16, float eps, void *dx, float *dw, void *work,
+                           size_t work_bytes, void *stream);
+
 /* Thread-local description of the last error (empty string if none). */
 const char *lores_last_error(void);
 

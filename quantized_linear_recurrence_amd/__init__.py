@@ -15,7 +15,7 @@ import numpy as np
 
 from . import _lib
 from ._lib import (LORES_BF16, LORES_FP8, LORES_FP32, LORES_INT4, LORES_INT6, LORES_INT8,
-                   LORES_MAX_WINDOW, LORES_ROUND_NEAREST, LORES_ROUND_STOCHASTIC, LORES_SCALE_KEY,
+                   LORES_MAX_NORM, LORES_MAX_WINDOW, LORES_ROUND_NEAREST, LORES_ROUND_STOCHASTIC, LORES_SCALE_KEY,
                    LORES_SCALE_VALUE, LoresLayout, LoresLibraryMissing)
 
 __all__ = ["LORES_FP32", "LORES_BF16", "LORES_INT8", "LORES_INT4", "LORES_INT6", "LORES_FP8",
@@ -26,6 +26,8 @@ __all__ = ["LORES_FP32", "LORES_BF16", "LORES_INT8", "LORES_INT4", "LORES_INT6",
            "lores_state_layout",
            "lores_state_head_map", "lores_decay_stat", "lores_assign_precision",
            "lores_decode_step", "lores_step_launches", "lores_quant_state", "lores_dequant_state",
+           "lores_scan", "lores_scan_backward", "lores_rmsnorm", "lores_rmsnorm_backward",
+           "LORES_MAX_NORM",
            "lores_last_error", "lores_spec_version"]
 
 
@@ -252,3 +254,220 @@ def lores_dequant_state(state, out=None, stream=None):
     _check(_lib.lib().lores_dequant_state(ctypes.c_void_p(state.handle), ptr,
                                           _stream_ptr(stream, state.device)))
     return out
+
+
+# ---------------------------------------------------------------- sequences
+
+def _on(stream, device):
+    """Allocations inside belong to `stream`, where the kernels that use them run."""
+    import contextlib
+
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _opt_ptr(t, name, dtype, numel, device):
+    return None if t is None else _dev_ptr(t, name, dtype, numel, device)
+
+
+def _rows4(t, name, dtype, shape, device):
+    """A [B, T, heads, width] tensor with a contiguous last dimension: its
+    pointer and its other strides."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, q is on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.stride(3) != 1 and shape[3] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.stride()[:3]
+
+
+def _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths):
+    import torch
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [B, T, heads, width], got {list(t.shape)}")
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError(f"q must be on the GPU, got {dev}")
+    if dt not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"q must be torch.bfloat16 or torch.float32, got {dt}")
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2:]
+    d = _lib.LoresScanDims(B, T, H, Hk, dk, dv, int(dt == torch.bfloat16), int(delta))
+    qp, d.q_stride[:] = _rows4(q, "q", dt, (B, T, Hk, dk), dev)
+    kp, d.k_stride[:] = _rows4(k, "k", dt, (B, T, Hk, dk), dev)
+    vp, d.v_stride[:] = _rows4(v, "v", dt, (B, T, H, dv), dev)
+    f32 = torch.float32
+    args = (qp, kp, vp, _dev_ptr(alpha, "alpha", f32, B * T * H, dev),
+            _dev_ptr(beta, "beta", f32, B * T * H, dev),
+            _opt_ptr(lengths, "lengths", torch.int32, B, dev),
+            _opt_ptr(S0, "S0", f32, B * H * dv * dk, dev))
+    return d, args, dev, dt
+
+
+def _scan_work(d, backward, workspace, dev):
+    import torch
+    n = ctypes.c_size_t(0)
+    _check(_lib.lib().lores_scan_workspace(ctypes.byref(d), backward, ctypes.byref(n)))
+    if workspace is None:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace, ctypes.c_void_p(workspace.data_ptr() if n.value else None), \
+        workspace.numel() * workspace.element_size()
+
+
+def lores_scan(q, k, v, alpha, beta, delta, S0=None, lengths=None, o=None, S=None, workspace=None,
+               stream=None):
+    """The recurrence over whole sequences, unquantized: a prompt, or a
+    training step's forward pass.
+
+    q, k [B, T, H_k, d_k] and v [B, T, H, d_v] (bf16 or fp32, any strides with
+    a contiguous last dimension; H_k divides H), alpha, beta [B, T, H] fp32,
+    S0 [B, H, d_v, d_k] fp32 or None (zero), lengths [B] int32 on the device
+    or None.  Returns (o [B, T, H, d_v] of q's type, S [B, H, d_v, d_k] fp32);
+    S is what lores_quant_state takes.  workspace: a device tensor of at least
+    the bytes that lores_scan_workspace says, or None to allocate it.
+    """
+    import torch
+    d, args, dev, dt = _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths)
+    with _on(stream, dev):
+        if o is None:
+            o = torch.empty((d.B, d.T, d.H, d.d_v), dtype=dt, device=dev)
+        if S is None:
+            S = torch.empty((d.B, d.H, d.d_v, d.d_k), dtype=torch.float32, device=dev)
+        work, wp, wn = _scan_work(d, 0, workspace, dev)
+    _check(_lib.lib().lores_scan(
+        ctypes.byref(d), *args, _dev_ptr(o, "o", dt, d.B * d.T * d.H * d.d_v, dev),
+        _dev_ptr(S, "S", torch.float32, d.B * d.H * d.d_v * d.d_k, dev), wp, wn,
+        _stream_ptr(stream, dev)))
+    return o, S
+
+
+def lores_scan_backward(q, k, v, alpha, beta, delta, do, dS=None, S0=None, lengths=None,
+                        workspace=None, stream=None):
+    """Gradients of lores_scan's inputs from do (and dS) of its outputs.
+
+    The forward pass is recomputed; do [B, T, H, d_v] has q's type, dS
+    [B, H, d_v, d_k] is fp32 or None (zero).  Returns (dq, dk, dv, dalpha,
+    dbeta, dS0), each of its input's type and shape, contiguous.
+    """
+    import torch
+    d, args, dev, dt = _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths)
+    n, f32 = d.B * d.H * d.d_v * d.d_k, torch.float32
+    dop = _dev_ptr(do, "do", dt, d.B * d.T * d.H * d.d_v, dev)
+    dSp = _opt_ptr(dS, "dS", f32, n, dev)
+    with _on(stream, dev):
+        dq = torch.empty((d.B, d.T, d.H_k, d.d_k), dtype=dt, device=dev)
+        dk = torch.empty_like(dq)
+        dv = torch.empty((d.B, d.T, d.H, d.d_v), dtype=dt, device=dev)
+        da = torch.empty((d.B, d.T, d.H), dtype=f32, device=dev)
+        db = torch.empty_like(da)
+        dS0 = torch.empty((d.B, d.H, d.d_v, d.d_k), dtype=f32, device=dev)
+        work, wp, wn = _scan_work(d, 1, workspace, dev)
+    out = (dq, dk, dv, da, db, dS0)
+    _check(_lib.lib().lores_scan_backward(
+        ctypes.byref(d), *args, dop, dSp, *(ctypes.c_void_p(t.data_ptr()) for t in out), wp, wn,
+        _stream_ptr(stream, dev)))
+    return out
+
+
+def _norm_rows(t, name, dtype, shape, device):
+    """A tensor of rows [..., n]: its pointer and the elements between rows."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the rows are on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    n = shape[-1]
+    if t.is_contiguous():
+        return ctypes.c_void_p(t.data_ptr()), n
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < n:
+        raise ValueError(f"{name} must be contiguous, or [rows, n] with contiguous rows")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0)
+
+
+def _norm_shape(x, weight):
+    import torch
+    if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
+        raise TypeError("the rows and weight must be torch tensors")
+    if x.device.type != "cuda":
+        raise ValueError(f"the rows must be on the GPU, got {x.device}")
+    for t, name in ((x, "the rows"), (weight, "weight")):
+        if t.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"rows must be [..., n] with n >= 1, got {list(x.shape)}")
+    n = x.shape[-1]
+    wp = _dev_ptr(weight, "weight", weight.dtype, n, x.device)
+    bf = torch.bfloat16
+    return x.numel() // n, n, wp, int(weight.dtype == bf), int(x.dtype == bf)
+
+
+def lores_rmsnorm(x, weight, eps, residual=None, out_prec=None, stream=None):
+    """Root-mean-square norm of the rows of x [..., n], of x + residual if given.
+
+    Returns (y, scales, h).  out_prec None, LORES_FP32 or LORES_BF16: y in x's
+    type, fp32 or bf16, scales None.  LORES_INT8 / LORES_FP8: y holds int8
+    codes / torch.float8_e4m3fn values and scales [...] fp32 one factor per
+    row.  h is the sum x + residual in x's type (x itself without a residual).
+    """
+    import torch
+    rows, n, wp, w_bf16, in_bf16 = _norm_shape(x, weight)
+    dev = x.device
+    xp, xs = _norm_rows(x, "x", x.dtype, x.shape, dev)
+    rp, rs = (None, 0) if residual is None else _norm_rows(residual, "residual", x.dtype, x.shape,
+                                                           dev)
+    if out_prec is None:
+        out_prec = LORES_BF16 if in_bf16 else LORES_FP32
+    types = {LORES_FP32: torch.float32, LORES_BF16: torch.bfloat16, LORES_INT8: torch.int8,
+             LORES_FP8: torch.float8_e4m3fn}
+    if out_prec not in types:
+        raise ValueError("out_prec must be LORES_FP32, LORES_BF16, LORES_INT8 or LORES_FP8")
+    with _on(stream, dev):
+        y = torch.empty(x.shape, dtype=types[out_prec], device=dev)
+        scales = None
+        if out_prec in (LORES_INT8, LORES_FP8):
+            scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        h = x if residual is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    _check(_lib.lib().lores_rmsnorm(
+        xp, xs, rp, rs, wp, w_bf16, rows, n, in_bf16, float(eps), int(out_prec),
+        ctypes.c_void_p(y.data_ptr()),
+        None if scales is None else ctypes.c_void_p(scales.data_ptr()),
+        None if residual is None else ctypes.c_void_p(h.data_ptr()), _stream_ptr(stream, dev)))
+    return y, scales, h
+
+
+def lores_rmsnorm_backward(h, weight, dy, eps, dresidual=None, stream=None):
+    """Gradients (dx, dw) of lores_rmsnorm's unquantized output: dx [..., n] of
+    h's type, for x and the residual alike, with the gradient dresidual that
+    reaches h otherwise added; dw [n] fp32."""
+    import torch
+    rows, n, wp, w_bf16, in_bf16 = _norm_shape(h, weight)
+    dev = h.device
+    hp, hs = _norm_rows(h, "h", h.dtype, h.shape, dev)
+    dyp = _dev_ptr(dy, "dy", h.dtype, rows * n, dev)
+    drp = _opt_ptr(dresidual, "dresidual", h.dtype, rows * n, dev)
+    size = ctypes.c_size_t(0)
+    _check(_lib.lib().lores_rmsnorm_workspace(rows, n, ctypes.byref(size)))
+    with _on(stream, dev):
+        dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+        dw = torch.empty(n, dtype=torch.float32, device=dev)
+        work = torch.empty(size.value, dtype=torch.uint8, device=dev)
+    _check(_lib.lib().lores_rmsnorm_backward(
+        hp, hs, wp, w_bf16, dyp, drp, rows, n, in_bf16, float(eps),
+        ctypes.c_void_p(dx.data_ptr()), ctypes.c_void_p(dw.data_ptr()),
+        ctypes.c_void_p(work.data_ptr()), size.value, _stream_ptr(stream, dev)))
+    return dx, dw

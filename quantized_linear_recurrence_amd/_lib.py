@@ -14,6 +14,7 @@ NUM_PREC = 6
 LORES_ROUND_STOCHASTIC, LORES_ROUND_NEAREST = 0, 1
 LORES_SCALE_VALUE, LORES_SCALE_KEY = 0, 1
 LORES_MAX_WINDOW = 16
+LORES_MAX_NORM = 16384
 LORES_OK, LORES_EINVAL, LORES_EUNSUPPORTED, LORES_ESIZE, LORES_EHIP, LORES_ENOMEM = 0, -1, -2, -3, -4, -5
 STATUS_NAMES = {0: "LORES_OK", -1: "LORES_EINVAL", -2: "LORES_EUNSUPPORTED", -3: "LORES_ESIZE",
                 -4: "LORES_EHIP", -5: "LORES_ENOMEM"}
@@ -24,6 +25,8 @@ EXPORTS = ("lores_state_alloc", "lores_state_alloc_axis", "lores_state_alloc_win
            "lores_decay_stat", "lores_assign_precision", "lores_decode_step",
            "lores_step_launches", "lores_state_set_rounding", "lores_quant_state",
            "lores_dequant_state",
+           "lores_scan_workspace", "lores_scan", "lores_scan_backward",
+           "lores_rmsnorm", "lores_rmsnorm_workspace", "lores_rmsnorm_backward",
            "lores_last_error", "lores_spec_version")
 
 
@@ -42,6 +45,14 @@ class LoresLayout(ctypes.Structure):
                 ("window", ctypes.c_int32), ("window_fill", ctypes.c_int32),
                 ("window_offset", ctypes.c_int64 * NUM_PREC),
                 ("unit_window_bytes", ctypes.c_int64 * NUM_PREC)]
+
+
+class LoresScanDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("H_k", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32),
+                ("in_bf16", ctypes.c_int32), ("delta", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3)]
 
 
 _lib = None
@@ -87,6 +98,18 @@ def lib():
     L.lores_quant_state.restype = ctypes.c_int
     L.lores_dequant_state.argtypes = [vp, vp, vp]
     L.lores_dequant_state.restype = ctypes.c_int
+    sz, dims = ctypes.c_size_t, ctypes.POINTER(LoresScanDims)
+    L.lores_scan_workspace.argtypes = [dims, i32, ctypes.POINTER(sz)]
+    L.lores_scan.argtypes = [dims] + [vp] * 10 + [sz, vp]
+    L.lores_scan_backward.argtypes = [dims] + [vp] * 16 + [sz, vp]
+    L.lores_rmsnorm.argtypes = [vp, i64, vp, i64, vp, i32, i64, i32, i32, ctypes.c_float, i32, vp,
+                                vp, vp, vp]
+    L.lores_rmsnorm_workspace.argtypes = [i64, i32, ctypes.POINTER(sz)]
+    L.lores_rmsnorm_backward.argtypes = [vp, i64, vp, i32, vp, vp, i64, i32, i32, ctypes.c_float,
+                                         vp, vp, vp, sz, vp]
+    for f in (L.lores_scan_workspace, L.lores_scan, L.lores_scan_backward, L.lores_rmsnorm,
+              L.lores_rmsnorm_workspace, L.lores_rmsnorm_backward):
+        f.restype = ctypes.c_int
     L.lores_last_error.argtypes = []
     L.lores_last_error.restype = ctypes.c_char_p
     L.lores_spec_version.argtypes = []

@@ -18,13 +18,14 @@ BUILD = os.path.join(os.path.dirname(PKG), "_build")
 LIB = os.path.join(PKG, "liblores.so")
 ARCH = "gfx950"
 
-SOURCES = ["lores_api.cpp", "lores_aux.hip", "lores_step_int8.hip", "lores_step_int4.hip",
+SOURCES = ["lores_api.cpp", "lores_seq_api.cpp", "lores_aux.hip", "lores_step_int8.hip", "lores_step_int4.hip",
            "lores_step_int6.hip", "lores_step_fp8.hip", "lores_step_bf16.hip", "lores_step_fp32.hip",
            "lores_step_int8_int4.hip", "lores_step_int4_int6.hip", "lores_step_bf16_int8.hip",
            "lores_step_bf16_int4.hip", "lores_step_key_int8.hip", "lores_step_key_int4.hip",
            "lores_step_key_int6.hip", "lores_step_key_fp8.hip", "lores_window.hip",
            "lores_window_int8.hip", "lores_window_int4.hip", "lores_window_int6.hip",
-           "lores_window_fp8.hip"]
+           "lores_window_fp8.hip", "lores_norm.hip", "lores_scan_rows.hip", "lores_scan_prep.hip",
+           "lores_scan_state.hip", "lores_scan_back.hip", "lores_scan_grad.hip"]
 
 COMMON = [
     "-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",

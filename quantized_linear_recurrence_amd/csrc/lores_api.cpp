@@ -217,6 +217,12 @@ hipError_t launch_step(int dk, bool pc, bool delta, bool bf16, int p0, int p1, c
 // the launch's.
 static void consume_stale_hip_error() { (void)hipGetLastError(); }
 
+namespace lores {
+// the same thread-local text for the entry points of the other host files
+int set_error(int code, const char *msg) { return fail(code, "%s", msg); }
+int set_ok() { return ok(); }
+}  // namespace lores
+
 extern "C" {
 
 const char *lores_last_error(void) { return g_err.c_str(); }
