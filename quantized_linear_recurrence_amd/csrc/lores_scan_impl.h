@@ -54,19 +54,31 @@ __device__ __forceinline__ void store4(float *p, f32x4 x) {
     *(f32x4 *)p = x;
 }
 
+// Two values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, b16x2));
+}
+
 // x = p[0] + p[1] + ... up to the last plane's rounding
 template <int NP>
 __device__ __forceinline__ void split8(const float (&x)[8], b16x8 (&p)[NP]) {
-    float r[8];
+    u32x4 w[NP];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = x[e];
+    for (int e = 0; e < 4; ++e) {
+        float a = x[2 * e], b = x[2 * e + 1];
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            p[i][e] = (__bf16)r[e];
-            if (i + 1 < NP) r[e] -= (float)p[i][e];
+        for (int i = 0; i < NP; ++i) {
+            w[i][e] = pack2(a, b);
+            if (i + 1 < NP) {
+                a -= __uint_as_float(w[i][e] << 16);
+                b -= __uint_as_float(w[i][e] & 0xffff0000u);
+            }
         }
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) p[i] = __builtin_bit_cast(b16x8, w[i]);
 }
 
 // 8 neighbours of a row at p, the first `n` of which exist (vec: 16-byte
@@ -112,17 +124,81 @@ __device__ __forceinline__ f32x4 mma(const b16x8 (&a)[NA], const b16x8 (&b)[NB],
     return c;
 }
 
-// An LDS matrix of bf16 planes, [NP][R][LD]; rows are 16-byte aligned and
-// start in different banks.
+// The same for MT results at once: products of planes outermost, so that
+// neighbouring instructions add to different results.
+template <int ORD, int MT, int NA, int NB>
+__device__ __forceinline__ void mma_all(const b16x8 (*a)[NA], const b16x8 (&b)[NB], f32x4 *c) {
+#pragma unroll
+    for (int o = ORD - 1; o >= 0; --o)
+#pragma unroll
+        for (int i = 0; i <= o; ++i)
+            if (i < NA && o - i < NB) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) c[t] = mfma(a[t][i], b[o - i], c[t]);
+            }
+}
+
+// Nothing is scheduled across: LDS reads written before it are in flight
+// while what stands behind it runs.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// Order of what stands before it back to the last fence: N times a matrix
+// instruction, then V vector instructions.  A wavefront issues in order and a
+// matrix instruction occupies its unit for 16 cycles, the time of four vector
+// instructions: the splitting of one operand hides behind the products of
+// another.
+template <int N, int V>
+__device__ __forceinline__ void mix() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
+    }
+}
+
+// Two neighbouring result tiles as one operand's 8 values.
+__device__ __forceinline__ void pair8(const f32x4 &a, const f32x4 &b, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x[i] = a[i]; x[4 + i] = b[i]; }
+}
+
+// The order of a row's 16-byte pieces in LDS: piece j lies at j ^ turn(row),
+// so that the 16 rows a matrix operand reads at one piece (rows 8 a + 4 p + b of
+// a block of 32, p fixed) hit different banks, without padding: 64 lanes'
+// 16-byte direct loads land in LDS one behind the other.  Rows r and r + 4 of
+// an aligned 8 turn alike.
+template <int W>
+__device__ __forceinline__ constexpr int turn(int r) {
+    return W >= 128 ? 4 * ((r >> 3) & 3) + (r & 3)
+           : W == 64 ? 2 * ((r >> 3) & 3) + ((r >> 1) & 1) : (r >> 3) & 3;
+}
+
+// Sum over the 16 lanes of a row, in all of them.
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int v = __float_as_int(x);
+        const int r = i == 0 ? __builtin_amdgcn_update_dpp(0, v, 0x128, 0xf, 0xf, true)     // row_ror:8
+                      : i == 1 ? __builtin_amdgcn_update_dpp(0, v, 0x124, 0xf, 0xf, true)
+                      : i == 2 ? __builtin_amdgcn_update_dpp(0, v, 0x122, 0xf, 0xf, true)
+                               : __builtin_amdgcn_update_dpp(0, v, 0x121, 0xf, 0xf, true);
+        x += __int_as_float(r);
+    }
+    return x;
+}
+
+// An LDS matrix of bf16 planes, R rows of W.
 template <int NP, int R, int W>
 struct Planes {
-    static constexpr int LD = W + 8;
-    uint16_t x[NP][R][LD];
+    uint16_t x[NP][R * W];
+    static __device__ __forceinline__ int at_(int row, int c) {
+        return row * W + (((c >> 3) ^ turn<W>(row)) << 3) + (c & 7);
+    }
     // operand whose lane holds row `row`, columns c .. c + 7
     template <int N>
     __device__ __forceinline__ void rows(int row, int c, b16x8 (&o)[N]) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = *(const b16x8 *)&x[i][row][c];
+        for (int i = 0; i < N; ++i) o[i] = *(const b16x8 *)&x[i][at_(row, c)];
     }
     // operand whose lane holds 8 rows r0 + 8 g .. + 7 (g = lane / 16) of one
     // column: the transposing read hands lane i of 16 the column i of the
@@ -131,11 +207,12 @@ struct Planes {
     template <int STEP, int N>
     __device__ __forceinline__ void cols(int r0, int c0, int lane, b16x8 (&o)[N]) const {
         const int i = lane & 15, r = r0 + 8 * (lane >> 4) + (i >> 2), c = c0 + STEP * (i & 3);
+        const int at = at_(r, c);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             typedef __attribute__((address_space(3))) s16x4 lds4;
-            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)&x[k][r][c]);
-            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)&x[k][r + 4][c]);
+            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)&x[k][at]);
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)&x[k][at + 4 * W]);
             const s16x8 w = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
             o[k] = __builtin_bit_cast(b16x8, w);
         }
@@ -143,19 +220,27 @@ struct Planes {
     template <int N>
     __device__ __forceinline__ void put8(int row, int c, const b16x8 (&o)[N]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) *(b16x8 *)&x[i][row][c] = o[i];
+        for (int i = 0; i < N; ++i) *(b16x8 *)&x[i][at_(row, c)] = o[i];
     }
-    __device__ __forceinline__ float at(int row, int c) const {
-        float s = bf2f(x[0][row][c]);
+    // rows r0 + 4 g + r of column c0 + (lane & 15): a result tile's layout
+    __device__ __forceinline__ f32x4 tile(int r0, int c0, int lane) const {
+        typedef __attribute__((address_space(3))) s16x4 lds4;
+        const int i = lane & 15, at = at_(r0 + 4 * (lane >> 4) + (i >> 2), c0 + 4 * (i & 3));
+        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 1; i < NP; ++i) s += bf2f(x[i][row][c]);
+        for (int k = 0; k < NP; ++k) {
+            const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)&x[k][at]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r] += bf2f((uint16_t)v[r]);
+        }
         return s;
     }
     __device__ __forceinline__ void put(int row, int c, float v) {
+        const int p = at_(row, c);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            x[i][row][c] = f2bf(v);
-            if (i + 1 < NP) v -= bf2f(x[i][row][c]);
+            x[i][p] = f2bf(v);
+            if (i + 1 < NP) v -= bf2f(x[i][p]);
         }
     }
 };
@@ -169,7 +254,8 @@ __device__ __forceinline__ int token_of(int mt, int m) {
     return 32 * (mt >> 1) + 8 * (m >> 2) + 4 * (mt & 1) + (m & 3);
 }
 
-// Decays of one chunk, computed by one wavefront's first C lanes.
+// Gates of one chunk, computed by one wavefront's first C lanes of the prep
+// kernel, which keeps them in the workspace for the others.
 template <int C>
 struct Gates {
     float al[C];     // alpha (1 behind the sequence's end)
@@ -229,14 +315,204 @@ __device__ __forceinline__ void stage_rows(Planes<NP, R, W> &dst, const IN *src,
     }
 }
 
-// A [NP][R][W] block of planes in memory, rows of W elements without padding.
-template <int NP, int R, int W>
-__device__ __forceinline__ void stage_planes(Planes<NP, R, W> &dst, const uint16_t *src, int tid,
-                                             int threads) {
-    for (int x = tid; x < NP * R * (W / 8); x += threads) {
-        const int pl = x / (R * (W / 8)), y = x % (R * (W / 8)), row = y / (W / 8), c = (y % (W / 8)) * 8;
-        *(u32x4 *)&dst.x[pl][row][c] = *(const u32x4 *)(src + (int64_t)(pl * R + row) * W + c);
+// The lower triangle of a C x C matrix of bf16 planes in blocks of 32 x 32,
+// block (I, J <= I) at I (I + 1) / 2 + J: what X and P are in memory and in LDS.
+// The operand reads of a block take whole 256-byte groups of its 64-byte rows,
+// so they need no padding.
+__host__ __device__ constexpr int tri_blocks(int C) { return (C / 32) * (C / 32 + 1) / 2; }
+__device__ __forceinline__ constexpr int tri_block(int I, int J) { return I * (I + 1) / 2 + J; }
+
+template <int NP, int C>
+struct Tri {
+    static constexpr int NB = tri_blocks(C);
+    uint16_t x[NP][NB][32][32];
+    // rows `row` of block (I, J), columns 8 g .. 8 g + 7
+    template <int N>
+    __device__ __forceinline__ void rows(int I, int J, int row, int g, b16x8 (&o)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = *(const b16x8 *)&x[i][tri_block(I, J)][row][8 * g];
     }
+    // the transpose's: 8 rows 8 g .. + 7 of one column of block (I, J) (see Planes::cols)
+    template <int STEP, int N>
+    __device__ __forceinline__ void cols(int I, int J, int c0, int lane, b16x8 (&o)[N]) const {
+        const int i = lane & 15, r = 8 * (lane >> 4) + (i >> 2), c = c0 + STEP * (i & 3);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            typedef __attribute__((address_space(3))) s16x4 lds4;
+            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)&x[k][tri_block(I, J)][r][c]);
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)&x[k][tri_block(I, J)][r + 4][c]);
+            const s16x8 w = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            o[k] = __builtin_bit_cast(b16x8, w);
+        }
+    }
+};
+
+// 16 bytes per lane from memory (`src`, the same in all lanes, plus the lane's
+// offset in bytes) straight to LDS, lane i's to `lds` + 16 i (`lds` the same in
+// all lanes).  The compiler does not count these loads: arrived() waits for
+// all of the wavefront's, and a barrier behind it makes them the
+// work-group's.  (Written as the instruction because the builtin's wait
+// before every LDS read that might alias would undo the prefetch; there is
+// no output register to be overwritten in flight.)
+__device__ __forceinline__ void direct16(const void *src, uint32_t lane_at, void *lds) {
+    // the low half of a generic LDS address is its offset; nothing else in these
+    // kernels uses m0
+    const uint32_t at = (uint32_t)(uintptr_t)lds;
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(lane_at), "s"(src), "s"(at) : "memory");
+}
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Contiguous bytes (a multiple of 16) to LDS, by the work-group's NW wavefronts.
+template <int BYTES, int NW>
+__device__ __forceinline__ void direct_block(const void *src, void *lds, int wv, int lane) {
+#pragma unroll
+    for (int i = 0; i < (BYTES + 1023) / 1024; i += NW) {
+        const int k = (i + wv) * 1024;
+        // whole pieces of 1 KiB but for the end
+        if (BYTES % 1024 == 0 ? k < BYTES : k + lane * 16 < BYTES)
+            direct16((const uint8_t *)src + k, (uint32_t)lane * 16, (uint8_t *)lds + k);
+    }
+}
+
+// bf16 rows to LDS (q, k, dO, or a plane of what the passes keep): R rows,
+// zeros from row n and column dk on.  For rows that can be read 16 bytes at a
+// time (a.vec also bounds the stride: a chunk's offsets fit 32 bits).
+template <int R, int W, int NW>
+__device__ __forceinline__ void direct_rows(uint16_t *dst, const uint16_t *src, int64_t stride, int n,
+                                            int dk, int wv, int lane) {
+    constexpr int PPR = W / 8, RPI = 64 / PPR;       // pieces of a row, rows of an instruction
+    const uint32_t bytes = (uint32_t)stride * 2;
+    const bool whole = n == R && dk == W;
+    // the lane's piece of the wavefront's first rows; its later rows are whole
+    // 8s further on, where all lanes' turns change alike
+    const int row0 = wv * RPI + lane / PPR;
+    const uint32_t piece0 = (uint32_t)((lane % PPR) ^ turn<W>(row0)) * 16, row_at = (uint32_t)(lane / PPR) * bytes;
+#pragma unroll
+    for (int i = 0; i < R / RPI; i += NW) {
+        const int blk = i + wv;
+        if (R / RPI % NW != 0 && blk >= R / RPI) break;
+        const uint32_t piece = piece0 ^ (uint32_t)(turn<W>(blk * RPI) ^ turn<W>(wv * RPI)) * 16;
+        uint16_t *to = dst + blk * RPI * W;
+        if (whole || (row0 + i * RPI < n && (int)piece < dk * 2))
+            direct16((const uint8_t *)src + (int64_t)(blk * RPI) * bytes, piece + row_at, to);
+        else
+            *(u32x4 *)(to + lane * 8) = u32x4{0, 0, 0, 0};
+    }
+}
+
+// A wavefront's 16 value columns of C tokens in LDS, [C][16] of the inputs'
+// type: v or dO on the way in (directly, 16 bytes per lane), o on the way out.
+// For rows of 16-byte pieces (a.vec_v: aligned, and d_v a whole number of
+// pieces); columns from d_v on are not written.
+template <typename IN, int C>
+struct Tile {
+    static constexpr int PPR = sizeof(IN), RPI = 64 / PPR;   // 16-byte pieces of a row, rows of an instruction
+    IN x[C * 16];
+    // n tokens from src (the tile's first column), rows `stride` apart
+    __device__ __forceinline__ void fetch(const IN *src, int64_t stride, int n, int cols, int lane) {
+        const uint32_t bytes = (uint32_t)stride * sizeof(IN);
+        const int piece = lane % PPR, row = lane / PPR;
+#pragma unroll
+        for (int i = 0; i < C / RPI; ++i)
+            if (i * RPI + row < n && piece * (16 / (int)sizeof(IN)) < cols)
+                direct16((const uint8_t *)src + (int64_t)(i * RPI) * bytes, (uint32_t)row * bytes + piece * 16,
+                         &x[i * RPI * 16]);
+    }
+    // the lane's column m = lane & 15 at tokens token_of(mt, 4 g + r)
+    __device__ __forceinline__ void get(int mt, int lane, float (&v)[4]) const {
+        const int g = lane >> 4, t0 = 32 * (mt >> 1) + 8 * g + 4 * (mt & 1);
+        if constexpr (sizeof(IN) == 2) {
+            typedef __attribute__((address_space(3))) s16x4 lds4;
+            const int i = lane & 15;
+            const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)&x[(t0 + (i >> 2)) * 16 + 4 * (i & 3)]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = bf2f((uint16_t)w[r]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = x[(t0 + r) * 16 + (lane & 15)];
+        }
+    }
+    __device__ __forceinline__ void put(int mt, int lane, const f32x4 &v) {
+        const int g = lane >> 4, t0 = 32 * (mt >> 1) + 8 * g + 4 * (mt & 1);
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+            if constexpr (sizeof(IN) == 2) {
+                const uint32_t w = pack2(v[r], v[r + 1]);
+                x[(t0 + r) * 16 + (lane & 15)] = (IN)(w & 0xffff);
+                x[(t0 + r + 1) * 16 + (lane & 15)] = (IN)(w >> 16);
+            } else {
+                x[(t0 + r) * 16 + (lane & 15)] = v[r];
+                x[(t0 + r + 1) * 16 + (lane & 15)] = v[r + 1];
+            }
+        }
+    }
+    // the tile's n first rows to dst
+    __device__ __forceinline__ void store(IN *dst, int64_t stride, int n, int cols, int lane) const {
+        const uint32_t bytes = (uint32_t)stride * sizeof(IN);
+        const int piece = lane % PPR, row = lane / PPR;
+#pragma unroll
+        for (int i = 0; i < C / RPI; ++i) {
+            f32x4 w = *(const f32x4 *)((const uint8_t *)&x[i * RPI * 16] + lane * 16);
+            if (i * RPI + row < n && piece * (16 / (int)sizeof(IN)) < cols)
+                store4((float *)((uint8_t *)dst + (int64_t)(i * RPI) * bytes + ((uint32_t)row * bytes + piece * 16)), w);
+        }
+    }
+};
+
+// fp32 rows on their way to LDS, where they become planes: held in registers
+// while the chunk before is worked on.  Every thread reads inside the rows,
+// what is not there is blanked on the way to LDS, so no branch and no wait
+// stands between the loads.
+template <int R, int W, int TH>
+struct RowFetch {
+    static constexpr int N = (R * (W / 8) + TH - 1) / TH;
+    f32x4 w[N][2];
+    __device__ __forceinline__ void load(const float *src, int64_t stride, int n, int dk, int tid) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int x = tid + i * TH, row = x / (W / 8), c = (x % (W / 8)) * 8;
+            const uint32_t at = (uint32_t)min(row, n - 1) * (uint32_t)stride + (uint32_t)(c < dk ? c : 0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) w[i][j] = ((const f32x4 *)(src + at))[j];
+        }
+    }
+    __device__ __forceinline__ void store(Planes<3, R, W> &dst, int n, int dk, int tid) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int x = tid + i * TH, row = x / (W / 8), c = (x % (W / 8)) * 8;
+            if (R * (W / 8) % TH != 0 && x >= R * (W / 8)) continue;
+            float f[8];
+            pair8(w[i][0], w[i][1], f);
+            if (row >= n || c >= dk) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+            }
+            b16x8 p[3];
+            split8(f, p);
+            dst.put8(row, c, p);
+        }
+    }
+};
+
+// Wavefronts of a work-group in the passes over the chunks (16 value rows
+// each).  Eight share a chunk's rows in LDS and fill a compute unit's SIMDs
+// twice, which pays where that still leaves a work-group for each of the 256
+// compute units; with fewer units the rows are spread over more of them.
+// Measured at d_k = d_v = 128: 256 units x 4096 tokens 1517 us by eight, 1705
+// by four; 32 units 478 and 424; 128 units (training step) 1978 and 1743.
+inline int scan_waves(const ScanArgs &a) {
+    return (int64_t)a.B * a.H * ((a.dv + 127) / 128) >= 256 ? 8 : 4;
+}
+
+// The units' order along the grid: work-groups go round the 8 XCDs, so the
+// `groups` work-groups of a unit, which read the same rows, are 8 apart and
+// share an L2.
+__device__ __forceinline__ bool unit_of(int block, int groups, int units, int *unit, int *grp) {
+    const int x = block & 7, y = block >> 3;
+    *grp = y % groups;
+    *unit = y / groups * 8 + x;
+    return *unit < units;
 }
 
 }  // namespace scan

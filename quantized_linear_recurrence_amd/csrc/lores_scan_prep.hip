@@ -17,7 +17,7 @@ namespace {
 
 template <typename IN>
 __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const ScanArgs a, const ScanWork w) {
-    constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16;
+    constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, NB = tri_blocks(C);
     __shared__ Gates<C> gt;
     __shared__ __attribute__((aligned(16))) float nm[C][C + 4];      // N, rows of 16-byte multiples
     __shared__ __attribute__((aligned(16))) float xd[NT][16][20];    // inverses of the diagonal blocks
@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
         if (gi) __syncthreads();                     // the last head's arrays have been read
         if (mt == 0) gt.load(a.alpha + gate, a.beta + gate, a.H, n, lane);
         __syncthreads();
-        uint16_t *Pp = w.P + unit * w.p_planes * C * C;
+        w.G[unit * 4 * C + threadIdx.x] = (&gt.al[0])[threadIdx.x];
+        uint16_t *Pp = w.P + unit * w.p_planes * NB * 1024;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if (nt > (mt | 1)) continue;             // blocks of 32 tokens above the diagonal are not read
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
                 float x = qk[nt][r] * d[r];
                 for (int pl = 0; pl < w.p_planes; ++pl) {
                     const uint16_t bits = f2bf(x);
-                    Pp[(pl * C + row) * C + col] = bits;
+                    Pp[((pl * NB + tri_block(mt >> 1, nt >> 1)) * 32 + (row & 31)) * 32 + (col & 31)] = bits;
                     x -= bf2f(bits);
                 }
                 if (a.delta) nm[row][col] = row > col ? gt.be[row] * (kk[nt][r] * d[r]) : 0.0f;
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
             }
         }
         __syncthreads();
-        uint16_t *Xp = w.X + unit * 3 * C * C;
+        uint16_t *Xp = w.X + unit * 3 * NB * 1024;
         f32x4 x[NT];                                 // block column J = mt, rows 4 g + r of block I
 #pragma unroll
         for (int I = 0; I < NT; ++I) {
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
 #pragma unroll
                 for (int pl = 0; pl < 3; ++pl) {
                     const uint16_t bits = f2bf(v);
-                    Xp[(pl * C + 16 * I + 4 * g + r) * C + 16 * mt + m] = bits;
+                    Xp[((pl * NB + tri_block(I >> 1, mt >> 1)) * 32 + 16 * (I & 1) + 4 * g + r) * 32 + 16 * (mt & 1) + m] = bits;
                     v -= bf2f(bits);
                 }
             }
@@ -154,14 +155,16 @@ uint64_t plan_scan_work(bool in_bf16, bool backward, const ScanArgs &a, void *ba
         off += (bytes + 255) / 256 * 256;
         return p;
     };
-    w->X = (uint16_t *)(a.delta ? cut(units * 3 * C * C * 2) : nullptr);
-    w->P = (uint16_t *)cut(units * w->p_planes * C * C * 2);
+    const uint64_t tri = scan::tri_blocks((int)C) * 2048;       // bytes of a plane
+    w->X = (uint16_t *)(a.delta ? cut(units * 3 * tri) : nullptr);
+    w->P = (uint16_t *)cut(units * w->p_planes * tri);
+    w->G = (float *)cut(units * 4 * C * 4);
     w->S = w->dS = w->U = w->Hm = nullptr;
     if (backward) {
-        w->S = (float *)cut(units * a.dk * w->dvp * 4);
-        w->dS = (float *)cut(units * a.dk * w->dvp * 4);
-        w->U = (float *)cut(units * C * w->dvp * 4);
-        w->Hm = (float *)cut(units * C * w->dvp * 4);
+        w->S = (uint16_t *)cut(units * 3 * a.dk * w->dvp * 2);
+        w->dS = (uint16_t *)cut(units * 3 * a.dk * w->dvp * 2);
+        w->U = (uint16_t *)cut(units * 3 * C * w->dvp * 2);
+        w->Hm = (uint16_t *)cut(units * 3 * C * w->dvp * 2);
     }
     return off;
 }

@@ -16,31 +16,40 @@ namespace lores {
 namespace scan {
 namespace {
 
-constexpr int NW = 4;                                // wavefronts of a work-group
-
-template <typename IN, int DKP, bool BACK>
+template <typename IN, int DKP, bool BACK, int NW>
 struct StateLds {
-    static constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NP = BACK ? 1 : sizeof(IN) == 2 ? 2 : 3;
+    static constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NP = sizeof(IN) == 2 ? 2 : 3;
     Planes<NIN, C, DKP> k;
     Planes<NIN, BACK ? 1 : C, DKP> q;
-    Planes<3, C, C> x;
-    Planes<NP, BACK ? 1 : C, C> p;
+    Tri<3, C> x;
+    Tri<BACK ? 1 : NP, BACK ? 32 : C> p;
     Gates<C> g;
+    Tile<IN, C> v[NW];
 };
 
-// BACK: store every chunk's first state and U instead of outputs.
-template <typename IN, int DKP, bool DELTA, bool BACK>
+// Two chunks' rows where they fit: the next chunk's arrive while one is
+// worked on.
+template <typename L> __host__ __device__ constexpr int stages() { return 2 * sizeof(L) <= 160 * 1024 ? 2 : 1; }
+
+// BACK: store every chunk's first state and U instead of outputs.  FAST: q and
+// k rows that can be read 16 bytes at a time (a.vec); VEC: v and o rows (a.vec_v).
+// Others take the same steps with narrower loads.  NW: wavefronts of a
+// work-group.
+template <typename IN, int DKP, bool DELTA, bool BACK, bool FAST, bool VEC, int NW>
 __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArgs a, const ScanWork w, const int groups) {
-    constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, MT = C / 16, SB = C / 32, KS = DKP / 32;
+    constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, MT = C / 16, SB = C / 32, KS = DKP / 32, TH = 64 * NW;
     constexpr bool OUT16 = sizeof(IN) == 2;          // outputs end in bf16: two planes carry them
     constexpr int NO = OUT16 ? 2 : 3;
-    __shared__ __attribute__((aligned(16))) StateLds<IN, DKP, BACK> sm;
+    typedef StateLds<IN, DKP, BACK, NW> Lds;
+    constexpr int NS = stages<Lds>();
+    __shared__ __attribute__((aligned(16))) Lds lds[NS];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
-    const int unit = blockIdx.x / groups, grp = blockIdx.x - unit * groups;
+    int unit, grp;
+    if (!unit_of(blockIdx.x, groups, a.B * a.H, &unit, &grp)) return;
     const int b = unit / a.H, h = unit - b * a.H, hk = h / (a.H / a.Hk);
-    const int col = (grp * NW + wv) * 16 + m;        // the lane's value row of S
-    const bool mine = (grp * NW + wv) * 16 < a.dv, ok = col < a.dv;
+    const int col0 = (grp * NW + wv) * 16, col = col0 + m;   // the wavefront's value rows of S, the lane's
+    const bool mine = col0 < a.dv, ok = col < a.dv;
     int len = a.T;
     if (a.lengths) len = min(max(a.lengths[b], 0), a.T);
     f32x4 st[2 * KS];
@@ -53,162 +62,302 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
     }
     const IN *kb = (const IN *)a.k + b * a.ks[0] + hk * a.ks[2];
     const IN *qb = (const IN *)a.q + b * a.qs[0] + hk * a.qs[2];
-    const IN *vb = (const IN *)a.v + b * a.vs[0] + h * a.vs[2] + col;
+    const IN *vb = (const IN *)a.v + b * a.vs[0] + h * a.vs[2] + (mine ? col0 : 0);
+    const int64_t os = (int64_t)a.H * a.dv;
+    IN *ob = (IN *)a.o + ((int64_t)b * a.T * a.H + h) * a.dv + col0;
     const int chunks = (len + C - 1) / C;
+    RowFetch<C, OUT16 ? 8 : DKP, TH> kf, qf;         // fp32 only
+    IN vf[VEC ? 1 : MT][4];
+    // A chunk's rows to stage `to`, in parts that the compute steps below are
+    // interleaved with: part 0 k, 1 q, 2 what the tokens do to one another,
+    // 3 the values.
+    auto fetch = [&](int part, int ch, Lds &to) {
+        const int t0 = ch * C, n = min(len - t0, C);
+        const int64_t cu = (int64_t)unit * w.chunks + ch;
+        if (part == 0) {
+            if constexpr (FAST && OUT16) direct_rows<C, DKP, NW>(to.k.x[0], kb + t0 * a.ks[1], a.ks[1], n, a.dk, wv, lane);
+            else if constexpr (FAST) kf.load(kb + t0 * a.ks[1], a.ks[1], n, a.dk, tid);
+        } else if (part == 1) {
+            if constexpr (!BACK && FAST && OUT16) direct_rows<C, DKP, NW>(to.q.x[0], qb + t0 * a.qs[1], a.qs[1], n, a.dk, wv, lane);
+            else if constexpr (!BACK && FAST) qf.load(qb + t0 * a.qs[1], a.qs[1], n, a.dk, tid);
+        } else if (part == 2) {
+            if constexpr (!BACK) direct_block<sizeof(to.p), NW>(w.P + cu * (NO * Tri<1, C>::NB * 1024), &to.p, wv, lane);
+            if constexpr (DELTA) direct_block<sizeof(to.x), NW>(w.X + cu * (3 * Tri<1, C>::NB * 1024), &to.x, wv, lane);
+            direct_block<sizeof(to.g), NW>(w.G + cu * (4 * C), &to.g, wv, lane);
+        } else if (mine) {
+            if constexpr (VEC) {
+                to.v[wv].fetch(vb + t0 * a.vs[1], a.vs[1], n, a.dv - col0, lane);
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        vf[mt][r] = vb[(t0 + token_of(mt, r) + min(8 * g, n - 1 - token_of(mt, r))) * a.vs[1] + (ok ? m : 0)];
+            }
+        }
+    };
+    // fp32 rows, and rows at odd addresses, through registers
+    auto place = [&](int ch, Lds &to) {
+        const int t0 = ch * C, n = min(len - t0, C);
+        if constexpr (!FAST) {
+            stage_rows(to.k, kb + t0 * a.ks[1], a.ks[1], n, a.dk, false, tid, TH);
+            if constexpr (!BACK) stage_rows(to.q, qb + t0 * a.qs[1], a.qs[1], n, a.dk, false, tid, TH);
+        } else if constexpr (!OUT16) {
+            kf.store(to.k, n, a.dk, tid);
+            if constexpr (!BACK) qf.store(to.q, n, a.dk, tid);
+        }
+    };
+    if (chunks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fetch(i, 0, lds[0]);
+        place(0, lds[0]);
+        arrived();
+    }
     for (int ch = 0; ch < chunks; ++ch) {
         const int t0 = ch * C, n = min(len - t0, C);
         const int64_t cu = (int64_t)unit * w.chunks + ch;
-        __syncthreads();                             // the last chunk's rows have been read
-        stage_rows(sm.k, kb + t0 * a.ks[1], a.ks[1], n, a.dk, a.vec, tid, 64 * NW);
-        if constexpr (!BACK) {
-            stage_rows(sm.q, qb + t0 * a.qs[1], a.qs[1], n, a.dk, a.vec, tid, 64 * NW);
-            stage_planes(sm.p, w.P + cu * w.p_planes * C * C, tid, 64 * NW);
-        }
-        if constexpr (DELTA) stage_planes(sm.x, w.X + cu * 3 * C * C, tid, 64 * NW);
-        if (wv == 0) {
-            const int64_t gate = ((int64_t)b * a.T + t0) * a.H + h;
-            sm.g.load(a.alpha + gate, a.beta + gate, a.H, n, lane);
-        }
-        float u[MT][4];                              // V, then E, then U: tokens token_of(mt, 4 g + r)
+        Lds &sm = lds[NS == 2 ? ch & 1 : 0];
+        Lds &next = lds[NS == 2 ? (ch & 1) ^ 1 : 0];
+        const bool more = NS == 2 && ch + 1 < chunks;
+        f32x4 u[MT];                                 // V, then beta E, then U: tokens token_of(mt, 4 g + r)
+        if constexpr (!VEC) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int tk = token_of(mt, 4 * g + r);
-                u[mt][r] = ok && tk < n ? get1(vb + (t0 + tk) * a.vs[1]) : 0.0f;
+                for (int r = 0; r < 4; ++r) u[mt][r] = get1(&vf[mt][r]);
+        }
+        __syncthreads();                             // this chunk is there, the other stage has been read
+        if (!mine) {                                 // a wavefront without value rows only helps to fetch
+            if (more) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fetch(i, ch + 1, next);
             }
-        __syncthreads();
-        if (!mine) continue;
-        if constexpr (BACK) {
-            float *sp = w.S + cu * a.dk * w.dvp + col;
-#pragma unroll
-            for (int t = 0; t < 2 * KS; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int key = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + r;
-                    if (key < a.dk) sp[(int64_t)key * w.dvp] = st[t][r];
-                }
-        }
-        f32x4 o[MT];
-        if constexpr (DELTA || !BACK) {
-            f32x4 e[MT];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) e[mt] = o[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = st[2 * ks + (i >> 2)][i & 3];
-                b16x8 sp[3];
-                split8(x, sp);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const int row = token_of(mt, m);
-                    b16x8 av[NIN];
-                    if constexpr (DELTA) {
-                        sm.k.rows(row, 32 * ks + 8 * g, av);
-                        e[mt] = mma<3>(av, sp, e[mt]);
-                    }
-                    if constexpr (!BACK) {
-                        sm.q.rows(row, 32 * ks + 8 * g, av);
-                        o[mt] = mma<OUT16 ? 2 : 3>(av, sp, o[mt]);
-                    }
-                }
-            }
+        } else {
+        if constexpr (VEC) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const f32x4 gm = *(const f32x4 *)&sm.g.gam[token_of(mt, 4 * g)];
+                float x[4];
+                sm.v[wv].get(mt, lane, x);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if constexpr (DELTA) u[mt][r] = fmaf(-gm[r], e[mt][r], u[mt][r]);
-                    o[mt][r] *= gm[r];
-                }
+                for (int r = 0; r < 4; ++r) u[mt][r] = x[r];
             }
         }
+        if (more) fetch(0, ch + 1, next);
+        f32x4 o[MT], e[MT], gm[MT], be[MT];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const f32x4 be = *(const f32x4 *)&sm.g.be[token_of(mt, 4 * g)];
+        for (int mt = 0; mt < MT; ++mt) e[mt] = o[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        b16x8 sp[KS][3], rv[2][MT][NIN], xv[MT][3];
+        auto split = [&](int ks) {
+            float x[8];
+            pair8(st[2 * ks], st[2 * ks + 1], x);
+            split8(x, sp[ks]);
+        };
+        auto gates = [&]() {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) u[mt][r] *= be[r];
-        }
+            for (int mt = 0; mt < MT; ++mt) {
+                gm[mt] = *(const f32x4 *)&sm.g.gam[token_of(mt, 4 * g)];
+                be[mt] = *(const f32x4 *)&sm.g.be[token_of(mt, 4 * g)];
+            }
+        };
+        auto x_first = [&]() {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) sm.x.rows(mt >> 1, 0, token_of(mt, m) & 31, g, xv[mt]);
+        };
+        // K S^T; S is split one block of 32 keys ahead
         if constexpr (DELTA) {
-            f32x4 y[MT];
+            auto rows = [&](int ks) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) y[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int mt = 0; mt < MT; ++mt) sm.k.rows(token_of(mt, m), 32 * ks + 8 * g, rv[ks & 1][mt]);
+            };
+            rows(0);
+            split(0);
 #pragma unroll
-            for (int sb = 0; sb < SB; ++sb) {
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = u[2 * sb + (i >> 2)][i & 3];
-                b16x8 ep[3];
-                split8(x, ep);
-#pragma unroll
-                for (int mt = 2 * sb; mt < MT; ++mt) {
-                    b16x8 xv[3];
-                    sm.x.rows(token_of(mt, m), 32 * sb + 8 * g, xv);
-                    y[mt] = mma<3>(xv, ep, y[mt]);
-                }
+            for (int ks = 0; ks < KS; ++ks) {
+                fence();
+                if (ks + 1 < KS) rows(ks + 1);
+                else gates();
+                fence();
+                if (ks + 1 < KS) split(ks + 1);
+                mma_all<3, MT>(rv[ks & 1], sp[ks], e);
+                mix<(NIN == 1 ? 3 : 6) * MT, 4>();
             }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) u[mt][r] = y[mt][r];
+            fence();
+        } else {
+            gates();
         }
+        if (more) fetch(1, ch + 1, next);
         if constexpr (BACK) {
-            float *up = w.U + cu * C * w.dvp + col;
+            if constexpr (!DELTA) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) split(ks);
+            }
+            // the chunk's first state, as planes
+            uint16_t *sp0 = w.S + cu * 3 * w.dvp * a.dk;
+            const uint32_t at = (uint32_t)col * (uint32_t)a.dk + 8 * g;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                if (32 * ks < a.dk) {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        store4((float *)(sp0 + (uint32_t)(i * w.dvp * a.dk) + (at + 32 * ks)), __builtin_bit_cast(f32x4, sp[ks][i]));
+                }
+        }
+        // Q S^T, and beside it E and its planes
+        b16x8 ep[SB][3];
+        // nothing behind the sequence's end or d_v counts, whatever stands there
+        if (n < C || col0 + 16 > a.dv) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) u[mt][r] = ok && 8 * g < n - token_of(mt, r) ? u[mt][r] : 0.0f;
+        }
+        auto finish_e = [&](int sb) {
+#pragma unroll
+            for (int mt = 2 * sb; mt < 2 * sb + 2; ++mt)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    up[(int64_t)token_of(mt, 4 * g + r) * w.dvp] = u[mt][r];
-        } else {
-#pragma unroll
-            for (int sb = 0; sb < SB; ++sb) {
+                    u[mt][r] = be[mt][r] * (DELTA ? fmaf(-gm[mt][r], e[mt][r], u[mt][r]) : u[mt][r]);
+            if constexpr (DELTA) {
                 float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = u[2 * sb + (i >> 2)][i & 3];
-                b16x8 up[NO];
-                split8(x, up);
-#pragma unroll
-                for (int mt = 2 * sb; mt < MT; ++mt) {
-                    b16x8 pv[NO];
-                    sm.p.rows(token_of(mt, m), 32 * sb + 8 * g, pv);
-                    o[mt] = mma<NO>(pv, up, o[mt]);
-                }
+                pair8(u[2 * sb], u[2 * sb + 1], x);
+                split8(x, ep[sb]);
             }
-            IN *op = (IN *)a.o + ((int64_t)b * a.T + t0) * a.H * a.dv + (int64_t)h * a.dv + col;
+        };
+        if constexpr (!BACK) {
+            auto rows = [&](int ks) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+                for (int mt = 0; mt < MT; ++mt) sm.q.rows(token_of(mt, m), 32 * ks + 8 * g, rv[ks & 1][mt]);
+            };
+            rows(0);
+            if constexpr (!DELTA) split(0);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int tk = token_of(mt, 4 * g + r);
-                    if (ok && t0 + tk < a.T) put1(op + (int64_t)tk * a.H * a.dv, o[mt][r]);
+            for (int ks = 0; ks < KS; ++ks) {
+                fence();
+                if (ks + 1 < KS) rows(ks + 1);
+                else if constexpr (DELTA) x_first();
+                fence();
+                if constexpr (!DELTA) {
+                    if (ks + 1 < KS) split(ks + 1);
                 }
+                if (ks < SB) finish_e(ks);
+                mma_all<OUT16 ? 2 : 3, MT>(rv[ks & 1], sp[ks], o);
+                mix<(NIN == 1 ? 2 : 6) * MT, 6>();
+            }
+            fence();
+        } else {
+            if constexpr (DELTA) x_first();
+            fence();
+#pragma unroll
+            for (int sb = 0; sb < SB; ++sb) finish_e(sb);
         }
+        if (more) fetch(2, ch + 1, next);
+        // the last products' left operands come while U is made
+        b16x8 kt[2 * KS][NIN], pv[BACK ? 1 : MT][NO], ut[SB][3], up[SB][BACK ? 3 : NO];
+        f32x4 en[MT];
+        auto turned = [&](int sb) {
+#pragma unroll
+            for (int t = 0; t < 2 * KS; ++t)
+                sm.k.template cols<8>(32 * sb, 32 * (t >> 1) + 4 * (t & 1), lane, kt[t]);
+            if constexpr (!BACK) {
+#pragma unroll
+                for (int mt = 2 * sb; mt < MT; ++mt) sm.p.rows(mt >> 1, sb, token_of(mt, m) & 31, g, pv[mt]);
+            }
+        };
+        // U = X beta E, one block of 32 tokens after the other
+        if constexpr (DELTA) {
+            b16x8 xn[MT][3];
+            if constexpr (SB > 1) {
+#pragma unroll
+                for (int mt = 2; mt < MT; ++mt) sm.x.rows(mt >> 1, 1, token_of(mt, m) & 31, g, xn[mt]);
+            }
+            fence();
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) e[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            mma_all<3, MT>(xv, ep[0], e);
+            if constexpr (!BACK) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) o[mt] *= gm[mt];
+            }
+            fence();
+            turned(0);
+            fence();
+            if constexpr (SB > 1) mma_all<3, MT - 2>(xn + 2, ep[SB - 1], e + 2);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) u[mt] = e[mt];
+        } else {
+            turned(0);
+            if constexpr (!BACK) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) o[mt] *= gm[mt];
+            }
+        }
+        // S_C = gamma_C S + K^T (D_C U), and O += P U beside it
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) en[mt] = *(const f32x4 *)&sm.g.end[token_of(mt, 4 * g)];
         const float ge = sm.g.gam[C - 1];
+        auto split_u = [&](int sb) {
+            float x[8];
+            pair8(u[2 * sb], u[2 * sb + 1], x);
+            split8(x, up[sb]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= i < 4 ? en[2 * sb][i] : en[2 * sb + 1][i - 4];
+            split8(x, ut[sb]);
+        };
 #pragma unroll
         for (int t = 0; t < 2 * KS; ++t) st[t] *= ge;
+        split_u(0);
+        fence();
+        if (more) fetch(3, ch + 1, next);
+        if constexpr (SB > 1) split_u(SB - 1);
+        mma_all<3, 2 * KS>(kt, ut[0], st);
+        if constexpr (!BACK) mma_all<NO, MT>(pv, up[0], o);
+        mix<(NIN == 1 ? 3 : 6) * 2 * KS + (BACK ? 0 : (OUT16 ? 3 : 6) * MT), 3>();
+        fence();
+        if constexpr (SB > 1) {
+            turned(1);
+            fence();
+            if constexpr (!BACK) mma_all<NO, MT - 2>(pv + 2, up[SB - 1], o + 2);
+            mma_all<3, 2 * KS>(kt, ut[SB - 1], st);
+        }
+        if constexpr (BACK) {
+            uint16_t *u0 = w.U + cu * 3 * w.dvp * C;
 #pragma unroll
-        for (int sb = 0; sb < SB; ++sb) {
-            float x[8];
+            for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = u[2 * sb + (i >> 2)][i & 3] * sm.g.end[32 * sb + 8 * g + i];
-            b16x8 up[3];
-            split8(x, up);
+                for (int i = 0; i < 3; ++i)
+                    store4((float *)(u0 + (uint32_t)(i * w.dvp * C) + (uint32_t)(col * C + 32 * sb + 8 * g)),
+                           __builtin_bit_cast(f32x4, up[sb][i]));
+        } else {
+            const int nT = min(a.T - t0, C);
+            IN *oc = ob + t0 * os;
+            if constexpr (VEC) {
 #pragma unroll
-            for (int t = 0; t < 2 * KS; ++t) {
-                b16x8 kv[NIN];
-                sm.k.template cols<8>(32 * sb, 32 * (t >> 1) + 4 * (t & 1), lane, kv);
-                st[t] = mma<3>(kv, up, st[t]);
+                for (int mt = 0; mt < MT; ++mt) sm.v[wv].put(mt, lane, o[mt]);
+                sm.v[wv].store(oc, os, nT, a.dv - col0, lane);
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (ok && 8 * g < nT - token_of(mt, r))
+                            put1(oc + (token_of(mt, r) + 8 * g) * os + m, o[mt][r]);
             }
+        }
+        }
+        if (ch + 1 < chunks) {
+            if constexpr (NS == 1) {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fetch(i, ch + 1, lds[0]);
+            }
+            place(ch + 1, next);
+            arrived();
         }
     }
     if constexpr (!BACK) {
         // whole chunks behind the sequence's end
         if (ok)
-            for (int t = chunks * C + g; t < a.T; t += 4)
-                put1((IN *)a.o + (((int64_t)b * a.T + t) * a.H + h) * a.dv + col, 0.0f);
+            for (int t = chunks * C + g; t < a.T; t += 4) put1(ob + t * os + m, 0.0f);
         if (a.S && ok) {
 #pragma unroll
             for (int t = 0; t < 2 * KS; ++t) {
@@ -219,25 +368,33 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
     }
 }
 
-template <typename IN, int DKP>
+template <typename IN, int DKP, bool FAST, bool VEC, int NW>
 hipError_t go(bool backward, const ScanArgs &a, const ScanWork &w, hipStream_t s) {
     const int groups = (a.dv + 16 * NW - 1) / (16 * NW);
-    const dim3 grid((unsigned)((int64_t)a.B * a.H * groups));
+    const dim3 grid((unsigned)(((int64_t)a.B * a.H + 7) / 8 * 8 * groups));
     if (backward) {
-        if (a.delta) lores_scan_state_kernel<IN, DKP, true, true><<<grid, 64 * NW, 0, s>>>(a, w, groups);
-        else lores_scan_state_kernel<IN, DKP, false, true><<<grid, 64 * NW, 0, s>>>(a, w, groups);
+        if (a.delta) lores_scan_state_kernel<IN, DKP, true, true, FAST, VEC, NW><<<grid, 64 * NW, 0, s>>>(a, w, groups);
+        else lores_scan_state_kernel<IN, DKP, false, true, FAST, VEC, NW><<<grid, 64 * NW, 0, s>>>(a, w, groups);
     } else {
-        if (a.delta) lores_scan_state_kernel<IN, DKP, true, false><<<grid, 64 * NW, 0, s>>>(a, w, groups);
-        else lores_scan_state_kernel<IN, DKP, false, false><<<grid, 64 * NW, 0, s>>>(a, w, groups);
+        if (a.delta) lores_scan_state_kernel<IN, DKP, true, false, FAST, VEC, NW><<<grid, 64 * NW, 0, s>>>(a, w, groups);
+        else lores_scan_state_kernel<IN, DKP, false, false, FAST, VEC, NW><<<grid, 64 * NW, 0, s>>>(a, w, groups);
     }
     return hipGetLastError();
 }
 
+template <typename IN, int DKP>
+hipError_t by_rows(bool backward, const ScanArgs &a, const ScanWork &w, hipStream_t s) {
+    if (!a.vec) return go<IN, DKP, false, false, 4>(backward, a, w, s);
+    if (!a.vec_v) return go<IN, DKP, true, false, 4>(backward, a, w, s);
+    if (scan_waves(a) == 8) return go<IN, DKP, true, true, 8>(backward, a, w, s);
+    return go<IN, DKP, true, true, 4>(backward, a, w, s);
+}
+
 template <typename IN>
 hipError_t by_width(bool backward, const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    if (a.dk <= 64) return go<IN, 64>(backward, a, w, s);
-    if (a.dk <= 128) return go<IN, 128>(backward, a, w, s);
-    return go<IN, 256>(backward, a, w, s);
+    if (a.dk <= 64) return by_rows<IN, 64>(backward, a, w, s);
+    if (a.dk <= 128) return by_rows<IN, 128>(backward, a, w, s);
+    return by_rows<IN, 256>(backward, a, w, s);
 }
 
 }  // namespace

@@ -41,7 +41,10 @@ hipError_t launch_norm_backward(bool in_bf16, bool vec, const NormArgs &a, hipSt
 
 struct ScanArgs {
     int32_t B, T, H, Hk, dk, dv, delta;
-    int32_t vec;                       // q and k rows can be read 16 bytes at a time
+    int32_t vec;                       // q and k rows can be read 16 bytes at a time, and
+                                       // tokens lie less than 2^24 elements apart
+    int32_t vec_v;                     // the same of v, with d_v a multiple of 16 bytes, and of
+                                       // o, dout and dv
     int64_t qs[3], ks[3], vs[3];       // elements between sequences, tokens, heads
     const void *q, *k, *v;
     const float *alpha, *beta;         // [B][T][H]
@@ -65,13 +68,15 @@ constexpr int kScanRowsTokens = 8;
 __host__ __device__ constexpr int scan_chunk(bool in_bf16) { return in_bf16 ? 64 : 32; }
 
 // Workspace of a chunked scan, cut from the caller's buffer.  Per (sequence,
-// head, chunk): the planes of X and P, and for the backward pass the state
-// and its gradient at the chunk's two ends ([d_k][dvp]) and U and H ([C][dvp]).
+// head, chunk): the planes of X and P, the gates, and for the backward pass the state
+// and its gradient at the chunk's two ends and U and H, as planes too, value
+// rows first.
 struct ScanWork {
-    uint16_t *X;                       // [B][H][chunks][3][C][C]
-    uint16_t *P;                       // [B][H][chunks][p_planes][C][C]
-    float *S, *dS;                     // [B][H][chunks][dk][dvp]
-    float *U, *Hm;                     // [B][H][chunks][C][dvp]
+    uint16_t *X;                       // [B][H][chunks][3][blocks][32][32]
+    uint16_t *P;                       // [B][H][chunks][p_planes][blocks][32][32]
+    float *G;                          // [B][H][chunks][4][C]: alpha, beta, gamma, D_Cj
+    uint16_t *S, *dS;                  // [B][H][chunks][3][dvp][dk]
+    uint16_t *U, *Hm;                  // [B][H][chunks][3][dvp][C]
     int32_t chunks, p_planes, dvp;
 };
 // Lays `w` out over `base` (which may be NULL) and returns the bytes.

@@ -98,6 +98,11 @@ int check_scan_inputs(const lores_scan_dims *d, const void *q, const void *k, co
     a->vec = aligned(q, 16) && aligned(k, 16);
     for (int i = 0; i < 3; ++i)
         if (a->qs[i] * (int64_t)el % 16 != 0 || a->ks[i] * (int64_t)el % 16 != 0) a->vec = 0;
+    // offsets within a chunk of 64 tokens then fit 32 bits
+    if (a->qs[1] >= (1 << 24) || a->ks[1] >= (1 << 24)) a->vec = 0;
+    a->vec_v = aligned(v, 16) && d->d_v * el % 16 == 0 && a->vs[1] < (1 << 24);
+    for (int i = 0; i < 3; ++i)
+        if (a->vs[i] * (int64_t)el % 16 != 0) a->vec_v = 0;
     return LORES_OK;
 }
 
@@ -151,6 +156,7 @@ int lores_scan(const lores_scan_dims *dims, const void *q, const void *k, const 
     if (!aligned(S_last, 16)) return fail(LORES_EINVAL, "S_last must be 16-byte aligned");
     a.o = o;
     a.S = S_last;
+    if (!aligned(o, 16)) a.vec_v = 0;
     lores::ScanWork w;
     const uint64_t need = scan_work(dims, 0, work, &w);
     if (const int rc = check_work(need, work, work_bytes)) return rc;
@@ -186,6 +192,7 @@ int lores_scan_backward(const lores_scan_dims *dims, const void *q, const void *
     a.dalpha = dalpha;
     a.dbeta = dbeta;
     a.dS0 = dS_first;
+    if (!aligned(dout, 16) || !aligned(dv, 16)) a.vec_v = 0;
     lores::ScanWork w;
     std::memset(&w, 0, sizeof w);
     const uint64_t need = scan_work(dims, 1, work, &w);
