@@ -254,33 +254,85 @@ __device__ __forceinline__ int token_of(int mt, int m) {
     return 32 * (mt >> 1) + 8 * (m >> 2) + 4 * (mt & 1) + (m & 3);
 }
 
-// Gates of one chunk, computed by one wavefront's first C lanes of the prep
-// kernel, which keeps them in the workspace for the others.
+// Gates of one chunk: the prep kernel makes them and keeps them in the
+// workspace for the others.
 template <int C>
 struct Gates {
     float al[C];     // alpha (1 behind the sequence's end)
     float be[C];     // beta (0 behind it)
     float gam[C];    // gamma_i = alpha_0 .. alpha_i of the chunk
     float end[C];    // D_Cj: alpha_{j+1} .. alpha_{C-1}
-    __device__ __forceinline__ void load(const float *alpha, const float *beta, int64_t stride,
-                                         int n, int lane) {
-        if (lane >= C) return;
-        const float a = lane < n ? alpha[lane * stride] : 1.0f;
-        const float b = lane < n ? beta[lane * stride] : 0.0f;
-        float g = a, e = a;
-#pragma unroll
-        for (int d = 1; d < C; d <<= 1) {
-            const float x = __shfl_up(g, d, C), y = __shfl_down(e, d, C);
-            if (lane >= d) g *= x;
-            if (lane + d < C) e *= y;
-        }
-        e = __shfl_down(e, 1, C);
-        al[lane] = a;
-        be[lane] = b;
-        gam[lane] = g;
-        end[lane] = lane == C - 1 ? 1.0f : e;
-    }
 };
+
+// Products of alpha within the 16-token strips, for D_ij between tokens of
+// different strips: pre_i (the strips between, multiplied up) suf_j.
+template <int C>
+struct Strips {
+    float pre[C];    // alpha from the strip's first token to i
+    float suf[C];    // alpha behind j to the strip's last token
+};
+
+// Inclusive products over the lanes before (UP) or behind, in groups of W.
+template <int W, bool UP>
+__device__ __forceinline__ float scan_product(float x, int lane) {
+#pragma unroll
+    for (int d = 1; d < W; d <<= 1) {
+        const float y = UP ? __shfl_up(x, d, W) : __shfl_down(x, d, W);
+        const int l = lane & (W - 1);
+        if (UP ? l >= d : l + d < W) x *= y;
+    }
+    return x;
+}
+
+// One wavefront's share `part` of 4 of a chunk's gates; n tokens are there.
+template <int C>
+__device__ __forceinline__ void make_gates(Gates<C> &g, Strips<C> &s, int part, const float *alpha,
+                                           const float *beta, int64_t stride, int n, int lane) {
+    const int l = lane & (C - 1);
+    const float a = l < n ? alpha[l * stride] : 1.0f;
+    if (part == 0) {
+        const float b = l < n ? beta[l * stride] : 0.0f;
+        const float x = scan_product<C, true>(a, lane);
+        if (lane < C) { g.al[l] = a; g.be[l] = b; g.gam[l] = x; }
+    } else if (part == 1) {
+        const float x = __shfl_down(scan_product<C, false>(a, lane), 1, C);
+        if (lane < C) g.end[l] = l == C - 1 ? 1.0f : x;
+    } else if (part == 2) {
+        const float x = scan_product<16, true>(a, lane);
+        if (lane < C) s.pre[l] = x;
+    } else {
+        const float x = __shfl_down(scan_product<16, false>(a, lane), 1, 16);
+        if (lane < C) s.suf[l] = (l & 15) == 15 ? 1.0f : x;
+    }
+}
+
+// D_ij of the tile (mt, nt <= mt) turned over: the lane's row i = 16 mt + (lane &
+// 15) and columns j = 16 nt + 4 (lane / 16) + r; zero where j > i.
+template <int C>
+__device__ __forceinline__ void decay_turned(const Gates<C> &g, const Strips<C> &s, int mt, int nt,
+                                             int lane, float (&d)[4]) {
+    const int m = lane & 15, q = lane >> 4, i = 16 * mt + m;
+    if (nt < mt) {
+        float x = s.pre[i];
+        for (int k = nt + 1; k < mt; ++k) x *= s.pre[16 * k + 15];
+        const f32x4 sj = *(const f32x4 *)&s.suf[16 * nt + 4 * q];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[r] = x * sj[r];
+    } else {
+        float x = 1.0f;
+#pragma unroll
+        for (int l = 4; l < 16; ++l) {
+            const float al = g.al[16 * mt + l];
+            if (l >= 4 * q + 4 && l <= m) x *= al;
+        }
+        const f32x4 al = *(const f32x4 *)&g.al[16 * mt + 4 * q];
+#pragma unroll
+        for (int r = 3; r >= 0; --r) {
+            d[r] = 4 * q + r <= m ? x : 0.0f;
+            if (4 * q + r <= m) x *= al[r];
+        }
+    }
+}
 
 // D_ij of the 16 x 16 tile (mt, nt <= mt) for the lane's column j = 16 nt +
 // (lane & 15) and rows i = 16 mt + 4 (lane / 16) + r; zero above the diagonal.
@@ -333,6 +385,21 @@ struct Tri {
         for (int i = 0; i < N; ++i) o[i] = *(const b16x8 *)&x[i][tri_block(I, J)][row][8 * g];
     }
     // the transpose's: 8 rows 8 g .. + 7 of one column of block (I, J) (see Planes::cols)
+    // four neighbours of one row, as planes
+    __device__ __forceinline__ void put4(int I, int J, int row, int c, const float (&v)[4]) {
+        float a[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            const u32x2 w = {pack2(a[0], a[1]), pack2(a[2], a[3])};
+            *(u32x2 *)&x[i][tri_block(I, J)][row][c] = w;
+            if (i + 1 < NP) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    a[e] -= __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+            }
+        }
+    }
     template <int STEP, int N>
     __device__ __forceinline__ void cols(int I, int J, int c0, int lane, b16x8 (&o)[N]) const {
         const int i = lane & 15, r = 8 * (lane >> 4) + (i >> 2), c = c0 + STEP * (i & 3);

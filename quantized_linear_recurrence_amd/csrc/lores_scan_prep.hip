@@ -4,24 +4,38 @@
 //
 // A work-group takes one chunk of one sequence and key head, a wavefront 16
 // rows of it.  q k^T and k k^T are formed once for all value heads that share
-// them.  X = (I + N)^-1 with N = diag(beta) M strictly lower: the 16 x 16
-// diagonal blocks by forward substitution (a lane per column), the blocks
-// below by X_IJ = -X_II sum_K N_IK X_KJ on the fp32 matrix instructions, one
-// wavefront per block column J.  Substitution follows the recurrence itself,
-// so X stays as bounded as the tokens' transition products are.
+// them.  All tiles are made turned over (operands exchanged), so that a lane
+// holds four neighbours of one row: planes then go to LDS 8 bytes at a time
+// and to memory 16 (2-byte stores of the tiles as they come out took three
+// quarters of this kernel's time).  X = (I + N)^-1 with N = diag(beta) M
+// strictly lower: the 16 x 16 diagonal blocks by forward substitution (a lane
+// per column), the blocks left of them by X_IJ = -(sum_{K>J} X_IK N_KJ) X_JJ
+// on the fp32 matrix instructions, a wavefront per block row.  Substitution
+// follows the recurrence itself, so X stays as bounded as the tokens'
+// transition products are.
 #include "lores_scan_impl.h"
 
 namespace lores {
 namespace scan {
 namespace {
 
-template <typename IN>
+template <typename IN, int NP>
+struct PrepLds {
+    static constexpr int C = Cfg<IN>::C, NT = C / 16;
+    Gates<C> g;
+    Strips<C> s;
+    float nt[NT * (NT - 1) / 2 + 1][16][20];         // N_KJ turned over (rows j), tile K (K - 1) / 2 + J
+    float nd[NT][16][20];                            // N_II, then X_II
+    Tri<3, C> x;
+    Tri<NP, C> p;
+};
+
+// NP: planes of P.
+template <typename IN, int NP, bool DELTA>
 __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const ScanArgs a, const ScanWork w) {
-    constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, NB = tri_blocks(C);
-    __shared__ Gates<C> gt;
-    __shared__ __attribute__((aligned(16))) float nm[C][C + 4];      // N, rows of 16-byte multiples
-    __shared__ __attribute__((aligned(16))) float xd[NT][16][20];    // inverses of the diagonal blocks
-    const int lane = threadIdx.x & 63, mt = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, NB = tri_blocks(C), NW = NT, TH = 64 * NW;
+    __shared__ __attribute__((aligned(16))) PrepLds<IN, NP> sm;
+    const int tid = threadIdx.x, lane = tid & 63, mt = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
     const int chunk = blockIdx.x % w.chunks;
     const int bk = blockIdx.x / w.chunks, b = bk / a.Hk, hk = bk - b * a.Hk, G = a.H / a.Hk;
@@ -31,113 +45,134 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
     if (n <= 0) return;
     const IN *kp = (const IN *)a.k + b * a.ks[0] + t0 * a.ks[1] + hk * a.ks[2];
     const IN *qp = (const IN *)a.q + b * a.qs[0] + t0 * a.qs[1] + hk * a.qs[2];
-    f32x4 qk[NT], kk[NT];
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 qk[NT], kk[NT];                            // rows j = 16 nt + 4 g + r of column i = 16 mt + m
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) qk[nt] = kk[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int ks = 0; ks < a.dk; ks += 32) {
-        const int row = 16 * mt + m, c = ks + 8 * g;
-        b16x8 qa[NIN], ka[NIN];
-        get_planes(qp + row * a.qs[1] + c, row < n ? 8 : 0, a.vec, qa);
-        get_planes(kp + row * a.ks[1] + c, row < n ? 8 : 0, a.vec, ka);
+    for (int t = 0; t < NT; ++t) qk[t] = kk[t] = zero;
+    {
+        const int row = 16 * mt + m;
+        const IN *qr = qp + (int64_t)min(row, n - 1) * a.qs[1];
+        for (int k0 = 0; k0 < a.dk; k0 += 64) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            if (nt <= mt) {
-                const int col = 16 * nt + m;
-                b16x8 kb[NIN];
-                get_planes(kp + col * a.ks[1] + c, col < n ? 8 : 0, a.vec, kb);
-                qk[nt] = mma<3>(qa, kb, qk[nt]);
-                if (a.delta) kk[nt] = mma<3>(ka, kb, kk[nt]);
+            for (int ks = 0; ks < 2; ++ks) {
+                const int c = k0 + 32 * ks + 8 * g;
+                if (k0 + 32 * ks >= a.dk) continue;
+                b16x8 qv[NIN], kv[NT][NIN];
+                get_planes(qr + c, row < n ? 8 : 0, a.vec, qv);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (t <= mt) get_planes(kp + (int64_t)min(16 * t + m, n - 1) * a.ks[1] + c, 16 * t + m < n ? 8 : 0, a.vec, kv[t]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (t <= mt) {
+                        qk[t] = mma<3>(kv[t], qv, qk[t]);
+                        if constexpr (DELTA) {
+#pragma unroll
+                            for (int u = 0; u < NT; ++u)
+                                if (u == mt) kk[t] = mma<3>(kv[t], kv[u], kk[t]);
+                        }
+                    }
             }
+        }
     }
     for (int gi = 0; gi < G; ++gi) {
         const int h = hk * G + gi;
         const int64_t gate = ((int64_t)b * a.T + t0) * a.H + h;
         const int64_t unit = ((int64_t)b * a.H + h) * w.chunks + chunk;
         if (gi) __syncthreads();                     // the last head's arrays have been read
-        if (mt == 0) gt.load(a.alpha + gate, a.beta + gate, a.H, n, lane);
+#pragma unroll
+        for (int q = 0; q < 4; q += NW) make_gates(sm.g, sm.s, q + mt, a.alpha + gate, a.beta + gate, a.H, n, lane);
         __syncthreads();
-        w.G[unit * 4 * C + threadIdx.x] = (&gt.al[0])[threadIdx.x];
-        uint16_t *Pp = w.P + unit * w.p_planes * NB * 1024;
+        const float be = sm.g.be[16 * mt + m];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (nt > (mt | 1)) continue;             // blocks of 32 tokens above the diagonal are not read
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (nt <= mt) decay_tile(gt, mt, nt, lane, d);
-            const int col = 16 * nt + m;
+        for (int t = 0; t < NT; ++t) {
+            if (t > (mt | 1)) continue;              // blocks of 32 tokens above the diagonal are not read
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4];
+            if (t <= mt) decay_turned(sm.g, sm.s, mt, t, lane, d);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * mt + 4 * g + r;
-                float x = qk[nt][r] * d[r];
-                for (int pl = 0; pl < w.p_planes; ++pl) {
-                    const uint16_t bits = f2bf(x);
-                    Pp[((pl * NB + tri_block(mt >> 1, nt >> 1)) * 32 + (row & 31)) * 32 + (col & 31)] = bits;
-                    x -= bf2f(bits);
+            for (int r = 0; r < 4; ++r) v[r] = qk[t][r] * d[r];
+            sm.p.put4(mt >> 1, t >> 1, 16 * (mt & 1) + m, 16 * (t & 1) + 4 * g, v);
+            if constexpr (DELTA) {
+                if (t > mt) continue;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = t < mt || 4 * g + r < m ? be * (kk[t][r] * d[r]) : 0.0f;
+                if (t < mt) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sm.nt[mt * (mt - 1) / 2 + t][4 * g + r][m] = v[r];
+                } else {
+                    *(f32x4 *)&sm.nd[mt][m][4 * g] = f32x4{v[0], v[1], v[2], v[3]};
                 }
-                if (a.delta) nm[row][col] = row > col ? gt.be[row] * (kk[nt][r] * d[r]) : 0.0f;
             }
         }
-        if (!a.delta) continue;
-        __syncthreads();
-        // the wavefront's diagonal block, column m by the lanes of every group
-        {
+        if constexpr (DELTA) {
+            // the wavefront's diagonal block, written and read by it alone:
+            // column m by the lanes of every group
             float x[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 float s = i == m ? 1.0f : 0.0f;
 #pragma unroll
-                for (int l = 0; l < i; ++l) s = fmaf(-nm[16 * mt + i][16 * mt + l], x[l], s);
+                for (int l = 0; l < i; l += 4) {
+                    const f32x4 nr = *(const f32x4 *)&sm.nd[mt][i][l];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (l + e < i) s = fmaf(-nr[e], x[l + e], s);
+                }
                 x[i] = s;
             }
             if (g == 0) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) xd[mt][i][m] = x[i];
+                for (int i = 0; i < 16; ++i) sm.nd[mt][i][m] = x[i];
             }
         }
         __syncthreads();
-        uint16_t *Xp = w.X + unit * 3 * NB * 1024;
-        f32x4 x[NT];                                 // block column J = mt, rows 4 g + r of block I
+        // what is done goes to memory while X is made
+        for (int i = tid; i < C; i += TH) ((f32x4 *)(w.G + unit * 4 * C))[i] = ((const f32x4 *)&sm.g.al[0])[i];
+        for (int i = tid; i < NP * NB * 128; i += TH)
+            ((u32x4 *)(w.P + unit * NP * NB * 1024))[i] = ((const u32x4 *)&sm.p.x[0])[i];
+        if constexpr (!DELTA) continue;
+        f32x4 xt[NT];                                // X_IJ of block row I = mt: rows j, column i
 #pragma unroll
-        for (int I = 0; I < NT; ++I) {
-            if (I < mt) {
-                x[I] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                continue;
-            }
-            if (I == mt) {
+        for (int J = NT - 1; J >= 0; --J) {
+            xt[J] = zero;
+            if (J > mt) continue;
+            if (J == mt) {
+                xt[J] = *(const f32x4 *)&sm.nd[mt][m][4 * g];
+            } else {
+                f32x4 s = zero;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[I][r] = xd[mt][4 * g + r][m];
-                continue;
-            }
-            f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int K = 0; K < NT; ++K)
+                    if (K > J && K <= mt) {
+                        const f32x4 nr = *(const f32x4 *)&sm.nt[K * (K - 1) / 2 + J][m][4 * g];
 #pragma unroll
-            for (int K = 0; K < I; ++K)
-                if (K >= mt) {
-                    const f32x4 nr = *(const f32x4 *)&nm[16 * I + m][16 * K + 4 * g];
+                        for (int r = 0; r < 4; ++r)
+                            s = __builtin_amdgcn_mfma_f32_16x16x4f32(nr[r], xt[K][r], s, 0, 0, 0);
+                    }
+                f32x4 y = zero;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        s = __builtin_amdgcn_mfma_f32_16x16x4f32(nr[r], x[K][r], s, 0, 0, 0);
-                }
-            const f32x4 xr = *(const f32x4 *)&xd[I][m][4 * g];
-            f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                y = __builtin_amdgcn_mfma_f32_16x16x4f32(xr[r], s[r], y, 0, 0, 0);
-            x[I] = -y;
-        }
-#pragma unroll
-        for (int I = 0; I < NT; ++I) {
-            if (mt > (I | 1)) continue;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float v = x[I][r];
-#pragma unroll
-                for (int pl = 0; pl < 3; ++pl) {
-                    const uint16_t bits = f2bf(v);
-                    Xp[((pl * NB + tri_block(I >> 1, mt >> 1)) * 32 + 16 * (I & 1) + 4 * g + r) * 32 + 16 * (mt & 1) + m] = bits;
-                    v -= bf2f(bits);
-                }
+                for (int r = 0; r < 4; ++r)
+                    y = __builtin_amdgcn_mfma_f32_16x16x4f32(sm.nd[J][4 * g + r][m], s[r], y, 0, 0, 0);
+                xt[J] = -y;
             }
         }
+#pragma unroll
+        for (int J = 0; J < NT; ++J) {
+            if (J > (mt | 1)) continue;
+            const float v[4] = {xt[J][0], xt[J][1], xt[J][2], xt[J][3]};
+            sm.x.put4(mt >> 1, J >> 1, 16 * (mt & 1) + m, 16 * (J & 1) + 4 * g, v);
+        }
+        __syncthreads();
+        for (int i = tid; i < 3 * NB * 128; i += TH)
+            ((u32x4 *)(w.X + unit * 3 * NB * 1024))[i] = ((const u32x4 *)&sm.x.x[0])[i];
     }
+}
+
+template <typename IN, int NP>
+hipError_t go(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
+    const dim3 grid((unsigned)((int64_t)a.B * a.Hk * w.chunks));
+    if (a.delta) lores_scan_prep_kernel<IN, NP, true><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
+    else lores_scan_prep_kernel<IN, NP, false><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -170,10 +205,8 @@ uint64_t plan_scan_work(bool in_bf16, bool backward, const ScanArgs &a, void *ba
 }
 
 hipError_t launch_scan_prep(bool in_bf16, const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)a.B * a.Hk * w.chunks));
-    if (in_bf16) scan::lores_scan_prep_kernel<uint16_t><<<grid, 256, 0, s>>>(a, w);
-    else scan::lores_scan_prep_kernel<float><<<grid, 128, 0, s>>>(a, w);
-    return hipGetLastError();
+    if (!in_bf16) return scan::go<float, 3>(a, w, s);
+    return w.p_planes == 2 ? scan::go<uint16_t, 2>(a, w, s) : scan::go<uint16_t, 3>(a, w, s);
 }
 
 }  // namespace lores
