@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_back_kernel(const ScanArgs
         } else if (part == 2) {
             direct_block<sizeof(to.p), NW>(w.P + cu * (3 * Tri<1, C>::NB * 1024), &to.p, wv, lane);
             if constexpr (DELTA) direct_block<sizeof(to.x), NW>(w.X + cu * (3 * Tri<1, C>::NB * 1024), &to.x, wv, lane);
-            direct_block<sizeof(to.g), NW>(w.G + cu * (4 * C), &to.g, wv, lane);
+            direct_block<sizeof(to.g), NW>(w.G + cu * (6 * C), &to.g, wv, lane);
         } else if (mine) {
             if constexpr (VEC) {
                 to.d[wv].fetch(ob + t0 * os, os, n, a.dv - col0, lane);
@@ -140,9 +140,14 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_back_kernel(const ScanArgs
                 for (int r = 0; r < 4; ++r) d[mt][r] = ok && 8 * g < n - token_of(mt, r) ? d[mt][r] : 0.0f;
         }
         if (more) fetch(0, ch - 1, next);
-        // the gradient at the chunk's end, as planes
-        uint16_t *sp0 = w.dS + cu * 3 * w.dvp * a.dk;
-        const uint32_t at0 = (uint32_t)col * (uint32_t)a.dk + 8 * g;
+        // the gradient at the chunk's end
+        {
+            float *sp0 = w.dS + cu * w.dvp * a.dk;
+            const uint32_t at = (uint32_t)col * (uint32_t)a.dk + 8 * g;
+#pragma unroll
+            for (int t = 0; t < 2 * KS; ++t)
+                if (32 * (t >> 1) < a.dk) store4(sp0 + (at + 32 * (t >> 1) + 4 * (t & 1)), st[t]);
+        }
         f32x4 y[MT], z[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) y[mt] = z[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -176,11 +181,6 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_back_kernel(const ScanArgs
                 }
                 fence();
                 if (ks + 1 < KS) split(ks + 1, (ks + 1) & 1);
-                if (32 * ks < a.dk) {
-#pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        store4((float *)(sp0 + (uint32_t)(i * w.dvp * a.dk) + (at0 + 32 * ks)), __builtin_bit_cast(f32x4, sp[ks & 1][i]));
-                }
                 mma_all<3, MT>(kv[ks & 1], sp[ks & 1], y);
                 if (ks >= 1 && ks - 1 < SB) {
                     if (ks == 1) mma_all<3, 2>(pv[0], dp[0], z);
@@ -237,18 +237,9 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_back_kernel(const ScanArgs
         turned(0);
         fence();
         {
-            uint16_t *h0 = w.Hm + cu * 3 * w.dvp * C;
+            float *h0 = w.Hm + cu * w.dvp * C;
 #pragma unroll
-            for (int sb = 0; sb < SB; ++sb) {
-                float x[8];
-                b16x8 hp[3];
-                pair8(hm[2 * sb], hm[2 * sb + 1], x);
-                split8(x, hp);
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    store4((float *)(h0 + (uint32_t)(i * w.dvp * C) + (uint32_t)(col * C + 32 * sb + 8 * g)),
-                           __builtin_bit_cast(f32x4, hp[i]));
-            }
+            for (int mt = 0; mt < MT; ++mt) store4(h0 + (uint32_t)(col * C + token_of(mt, 4 * g)), hm[mt]);
         }
         if (more) fetch(3, ch - 1, next);
         const float ge = sm.g.gam[C - 1];

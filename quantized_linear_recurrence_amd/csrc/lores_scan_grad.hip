@@ -17,12 +17,13 @@
 //
 // A work-group takes one chunk and key head and loops over the value heads
 // that share it, so dq and dk are summed in registers in head order.  The
-// value columns go by in blocks of 32: dO and the planes of S, dS, U and H, which
-// the passes over the chunks have left in operand form, come to LDS directly,
-// a block ahead where two fit.  A wavefront owns 16 tokens' rows of dP and Z and
-// its share of 16-key strips of the products with S and dS.  That part is
-// bound by the matrix instructions (of 16 cycles, one in five instructions
-// is another's); dv, the decays and the two recurrences take about a third.
+// value columns go by in blocks of 32: S, dS, U and H become planes in LDS on
+// the way from registers, where the next block's arrive while one is worked
+// on.  All results are made turned over (a lane holds four neighbours of one
+// token's row, see the prep kernel), which also leaves the sums over keys to
+// two lane exchanges.  A wavefront owns strips of 16 keys of the products with
+// S and dS, and a share of 16 tokens' rows of dP and Z.  Bound by reading S and dS
+// (8 d_k d_v bytes per chunk) about as much as by the matrix instructions.
 #include "lores_scan_impl.h"
 
 namespace lores {
@@ -47,30 +48,32 @@ struct GradRows {                                    // when they have all gone 
     float a[C + 1][C + 1];                           // A, row C and column 0 its borders
 };
 
-template <typename IN, int DKP>
+template <typename IN, int DKP, int NW>
 struct GradLds {
     static constexpr int C = Cfg<IN>::C;
-    static constexpr int NS = 2 * sizeof(GradBlock<IN, DKP>) <= 152 * 1024 ? 2 : 1;
     union {
-        GradBlock<IN, DKP> b[NS];
+        GradBlock<IN, DKP> b;
         GradRows<IN, DKP> r;
     };
-    float part[3][4][C];                             // per wavefront: q.S^T dO, k.S^T h, k.dS^T u
-    float hv[C], mz[C], ss[4];
+    float part[3][NW][C];                            // per wavefront: q.S^T dO, k.S^T h, k.dS^T u
+    float hv[2][C], mz[2][C], ss[NW];
     Gates<C> g;
 };
 
+// Wavefronts: a strip each where d_k has that many, two to a 16-token row.
+template <typename IN, int DKP>
+constexpr int grad_waves() { return Cfg<IN>::C / 16 * (DKP > 64 ? 2 : 1); }
+
 // GROUP: several value heads share the key head.
 template <typename IN, int DKP, bool DELTA, bool GROUP>
-__global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_grad_kernel(const ScanArgs a, const ScanWork w) {
-    constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, SB = C / 32, NW = C / 16, TH = 64 * NW;
-    constexpr int ST = DKP / 16 / NT;                // 16-key strips of a wavefront
+__global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_kernel(const ScanArgs a, const ScanWork w) {
+    constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, SB = C / 32, NW = grad_waves<IN, DKP>(), TH = 64 * NW;
+    constexpr int ST = DKP / 16 / NW, RW = NW / NT;  // strips of a wavefront, wavefronts of a row
     constexpr int NO = sizeof(IN) == 2 ? 2 : 3;      // planes of what ends in the inputs' type
-    typedef GradLds<IN, DKP> Lds;
-    constexpr int NS = Lds::NS;
-    __shared__ __attribute__((aligned(16))) Lds sm;
-    const int tid = threadIdx.x, lane = tid & 63, mt = __builtin_amdgcn_readfirstlane(tid >> 6);
+    __shared__ __attribute__((aligned(16))) GradLds<IN, DKP, NW> sm;
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
+    const int mt = wv / RW, half = wv % RW;          // the wavefront's row of tiles, its share of it
     const int chunk = blockIdx.x % w.chunks;
     const int bk = blockIdx.x / w.chunks, b = bk / a.Hk, hk = bk - b * a.Hk, G = GROUP ? a.H / a.Hk : 1;
     int len = a.T;
@@ -111,27 +114,85 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_grad_kernel(const S
         const int64_t tok = ((int64_t)b * a.T + t0) * a.H + h;   // of the chunk's first token
         const int64_t os = (int64_t)a.H * a.dv;
         const IN *dc = (const IN *)a.dout + tok * a.dv;
-        const uint16_t *Sp = w.S + cu * 3 * w.dvp * a.dk, *dSp = w.dS + cu * 3 * w.dvp * a.dk;
-        const uint16_t *Up = w.U + cu * 3 * w.dvp * C, *Hp = w.Hm + cu * 3 * w.dvp * C;
-        auto fetch = [&](int v0, GradBlock<IN, DKP> &to) {
-            const int rows = min(w.dvp - v0, VB);
+        // a block's pieces of 8: S and dS, U and H, dO
+        constexpr int NSP = (VB * (DKP / 8) + TH - 1) / TH, NUP = (2 * VB * (C / 8) + TH - 1) / TH;
+        constexpr int NDP = (C * (VB / 8) + TH - 1) / TH;
+        f32x4 fs[NSP][2], fe[NSP][2], fu[NUP][2];
+        b16x8 fd[NDP][NIN];
+        const float *Sp = w.S + cu * w.dvp * a.dk, *dSp = w.dS + cu * w.dvp * a.dk;
+        const float *Up = w.U + cu * w.dvp * C, *Hp = w.Hm + cu * w.dvp * C;
+        auto fetch = [&](int v0) {
+            const int last = w.dvp - v0 - 1;         // rows behind it are blanked in place()
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                direct_rows<VB, DKP, NW>(to.s.x[i], Sp + (i * w.dvp + v0) * a.dk, a.dk, rows, a.dk, mt, lane);
-                direct_rows<VB, DKP, NW>(to.ds.x[i], dSp + (i * w.dvp + v0) * a.dk, a.dk, rows, a.dk, mt, lane);
-                direct_rows<VB, C, NW>(to.u.x[i], Up + (i * w.dvp + v0) * C, C, rows, C, mt, lane);
-                direct_rows<VB, C, NW>(to.h.x[i], Hp + (i * w.dvp + v0) * C, C, rows, C, mt, lane);
+            for (int i = 0; i < NSP; ++i) {
+                const int x = tid + i * TH, r = min(x / (DKP / 8), last), c = (x % (DKP / 8)) * 8;
+                const uint32_t at = (uint32_t)((v0 + r) * a.dk + (c < a.dk ? c : 0));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    fs[i][j] = *(const f32x4 *)(Sp + at + 4 * j);
+                    fe[i][j] = *(const f32x4 *)(dSp + at + 4 * j);
+                }
             }
-            if constexpr (NIN == 1) {
-                if (a.vec_v) direct_rows<C, VB, NW>(to.d.x[0], (const uint16_t *)dc + v0, os, n, a.dv - v0, mt, lane);
+#pragma unroll
+            for (int i = 0; i < NUP; ++i) {
+                const int x = tid + i * TH, y = x % (VB * (C / 8)), r = min(y / (C / 8), last), c = (y % (C / 8)) * 8;
+                const float *p = (x < VB * (C / 8) ? Up : Hp) + (uint32_t)((v0 + r) * C + c);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) fu[i][j] = *(const f32x4 *)(p + 4 * j);
+            }
+#pragma unroll
+            for (int i = 0; i < NDP; ++i) {
+                const int x = tid + i * TH, r = x / (VB / 8), c = (x % (VB / 8)) * 8;
+                get_planes(dc + (int64_t)r * os + v0 + c, x < C * (VB / 8) && r < n ? a.dv - v0 - c : 0, a.vec_v, fd[i]);
             }
         };
-        // dO rows that do not come directly
-        auto place = [&](int v0, GradBlock<IN, DKP> &to) {
-            if (NIN == 3 || !a.vec_v) stage_rows(to.d, dc + v0, os, n, a.dv - v0, a.vec_v, tid, TH);
+        float ss = 0.0f, hv = 0.0f;                  // <S, dS>; h_i . v_i of token 16 mt + m
+        auto place = [&](int v0) {
+            const int rows = w.dvp - v0;
+#pragma unroll
+            for (int i = 0; i < NSP; ++i) {
+                const int x = tid + i * TH, r = x / (DKP / 8), c = (x % (DKP / 8)) * 8;
+                if (VB * (DKP / 8) % TH != 0 && x >= VB * (DKP / 8)) continue;
+                float s8[8], e8[8];
+                pair8(fs[i][0], fs[i][1], s8);
+                pair8(fe[i][0], fe[i][1], e8);
+                if (r >= rows || c >= a.dk) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s8[e] = e8[e] = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(s8[e], e8[e], ss);
+                b16x8 p[3];
+                split8(s8, p);
+                sm.b.s.put8(r, c, p);
+                split8(e8, p);
+                sm.b.ds.put8(r, c, p);
+            }
+#pragma unroll
+            for (int i = 0; i < NUP; ++i) {
+                const int x = tid + i * TH, y = x % (VB * (C / 8)), r = y / (C / 8), c = (y % (C / 8)) * 8;
+                if (2 * VB * (C / 8) % TH != 0 && x >= 2 * VB * (C / 8)) continue;
+                float u8[8];
+                pair8(fu[i][0], fu[i][1], u8);
+                if (r >= rows) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u8[e] = 0.0f;
+                }
+                b16x8 p[3];
+                split8(u8, p);
+                if (x < VB * (C / 8)) sm.b.u.put8(r, c, p);
+                else sm.b.h.put8(r, c, p);
+            }
+#pragma unroll
+            for (int i = 0; i < NDP; ++i) {
+                const int x = tid + i * TH;
+                if (x < C * (VB / 8)) sm.b.d.put8(x / (VB / 8), (x % (VB / 8)) * 8, fd[i]);
+            }
         };
+        fetch(0);
         __syncthreads();                             // the last head's arrays have been read
-        if (tid < 4 * C) (&sm.g.al[0])[tid] = w.G[cu * (4 * C) + tid];
+        for (int i = tid; i < 6 * C; i += TH) (&sm.g.al[0])[i] = w.G[cu * (6 * C) + i];
+        // turned over: the lane's token is the column, its rows four neighbours
         f32x4 dp[NT], z[NT], sdo[NT][ST], sh[NT][ST], dsu[NT][ST];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -139,110 +200,90 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_grad_kernel(const S
 #pragma unroll
             for (int s = 0; s < ST; ++s) sdo[t][s] = sh[t][s] = dsu[t][s] = zero;
         }
-        float ss = 0.0f, hv = 0.0f;                  // <S, dS>; h_i . v_i of token 16 mt + m
-        fetch(0, sm.b[0]);
-        place(0, sm.b[0]);
-        arrived();
         for (int v0 = 0; v0 < a.dv; v0 += VB) {
-            GradBlock<IN, DKP> &bl = sm.b[NS == 2 ? v0 / VB & 1 : 0];
-            __syncthreads();                         // this block is there, the other has been read
-            if (NS == 2 && v0 + VB < a.dv) fetch(v0 + VB, sm.b[(v0 / VB & 1) ^ 1]);
+            if (v0) __syncthreads();                 // the last block has been read
+            place(v0);
+            __syncthreads();
+            if (v0 + VB < a.dv) fetch(v0 + VB);
             const int row = 16 * mt + m, c = v0 + 8 * g;          // the lane's token and its 8 columns
-            // h of the wavefront's tokens: dv and h . v
-            b16x8 ha[3];
-            bl.h.template cols<4>(0, 16 * mt, lane, ha);
-            float h8[8], v8[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h8[e] = (float)ha[0][e] + (float)ha[1][e] + (float)ha[2][e];
-            const IN *vp = (const IN *)a.v + b * a.vs[0] + (t0 + min(row, n - 1)) * a.vs[1] + h * a.vs[2] + c;
-            if constexpr (NIN == 1) {
-                b16x8 t[1];
-                get_planes(vp, row < n ? a.dv - c : 0, a.vec_v, t);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v8[e] = (float)t[0][e];
-            } else {
-                get8(vp, row < n ? a.dv - c : 0, a.vec_v, v8);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) hv = fmaf(h8[e], v8[e], hv);
-            if (row < nT) {
-                IN *op = (IN *)a.dvalue + tok * a.dv + row * os + c;
-                const float be = sm.g.be[row];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h8[e] *= be;
-                if (a.vec_v && c + 8 <= a.dv) {
-                    if constexpr (NIN == 1) {
-                        b16x8 t[1];
-                        split8(h8, t);
-                        store4((float *)op, __builtin_bit_cast(f32x4, t[0]));
-                    } else {
-                        store4((float *)op, f32x4{h8[0], h8[1], h8[2], h8[3]});
-                        store4((float *)op + 4, f32x4{h8[4], h8[5], h8[6], h8[7]});
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (c + e < a.dv) put1(op + e, h8[e]);
-                }
-            }
-            // <S, dS>: every thread its share of the block
-            for (int x = tid; x < VB * (DKP / 8); x += TH) {
-                const int r8 = x / (DKP / 8), c8 = (x % (DKP / 8)) * 8;
-                b16x8 s3[3], d3[3];
-                bl.s.rows(r8, c8, s3);
-                bl.ds.rows(r8, c8, d3);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    ss = fmaf((float)s3[0][e] + (float)s3[1][e] + (float)s3[2][e],
-                              (float)d3[0][e] + (float)d3[1][e] + (float)d3[2][e], ss);
-            }
-            // dP and Z, the wavefront's rows
-            {
-                b16x8 da[NIN];
-                bl.d.rows(row, 8 * g, da);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    if (nt <= mt) {
-                        b16x8 ub[3];
-                        bl.u.template cols<4>(0, 16 * nt, lane, ub);
-                        dp[nt] = mma<3>(da, ub, dp[nt]);
-                        if constexpr (DELTA) z[nt] = mma<3>(ha, ub, z[nt]);
-                    }
-            }
             // S^T dO, S^T h and dS^T u, the wavefront's strips
             b16x8 sf[ST][3], ef[ST][3];
 #pragma unroll
             for (int s = 0; s < ST; ++s) {
-                bl.s.template cols<4>(0, 16 * (mt + NT * s), lane, sf[s]);
-                bl.ds.template cols<4>(0, 16 * (mt + NT * s), lane, ef[s]);
+                sm.b.s.template cols<4>(0, 16 * (wv + NW * s), lane, sf[s]);
+                sm.b.ds.template cols<4>(0, 16 * (wv + NW * s), lane, ef[s]);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 b16x8 x1[NIN], xh[3], xu[3];
-                bl.d.rows(16 * t + m, 8 * g, x1);
-                if constexpr (DELTA) bl.h.template cols<4>(0, 16 * t, lane, xh);
-                bl.u.template cols<4>(0, 16 * t, lane, xu);
+                sm.b.d.rows(16 * t + m, 8 * g, x1);
+                if constexpr (DELTA) sm.b.h.template cols<4>(0, 16 * t, lane, xh);
+                sm.b.u.template cols<4>(0, 16 * t, lane, xu);
 #pragma unroll
                 for (int s = 0; s < ST; ++s) {
-                    sdo[t][s] = mma<3>(x1, sf[s], sdo[t][s]);
-                    if constexpr (DELTA) sh[t][s] = mma<3>(xh, sf[s], sh[t][s]);
-                    dsu[t][s] = mma<3>(xu, ef[s], dsu[t][s]);
+                    sdo[t][s] = mma<3>(sf[s], x1, sdo[t][s]);
+                    if constexpr (DELTA) sh[t][s] = mma<3>(sf[s], xh, sh[t][s]);
+                    dsu[t][s] = mma<3>(ef[s], xu, dsu[t][s]);
                 }
             }
-            if (v0 + VB < a.dv) {
-                if constexpr (NS == 1) {
-                    __syncthreads();
-                    fetch(v0 + VB, sm.b[0]);
+            // dP and Z, the wavefront's tiles
+            b16x8 ha[3];
+            sm.b.h.template cols<4>(0, 16 * mt, lane, ha);
+            {
+                b16x8 da[NIN];
+                sm.b.d.rows(row, 8 * g, da);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (t <= mt && t % RW == half) {
+                        b16x8 ub[3];
+                        sm.b.u.template cols<4>(0, 16 * t, lane, ub);
+                        dp[t] = mma<3>(ub, da, dp[t]);
+                        if constexpr (DELTA) z[t] = mma<3>(ub, ha, z[t]);
+                    }
+            }
+            // h of the row's tokens: dv and h . v
+            if (v0 / VB % RW == half) {
+                float h8[8], v8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h8[e] = (float)ha[0][e] + (float)ha[1][e] + (float)ha[2][e];
+                const IN *vp = (const IN *)a.v + b * a.vs[0] + (t0 + min(row, n - 1)) * a.vs[1] + h * a.vs[2] + c;
+                if constexpr (NIN == 1) {
+                    b16x8 t[1];
+                    get_planes(vp, row < n ? a.dv - c : 0, a.vec_v, t);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v8[e] = (float)t[0][e];
+                } else {
+                    get8(vp, row < n ? a.dv - c : 0, a.vec_v, v8);
                 }
-                place(v0 + VB, sm.b[NS == 2 ? (v0 / VB & 1) ^ 1 : 0]);
-                arrived();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) hv = fmaf(h8[e], v8[e], hv);
+                if (row < nT) {
+                    IN *op = (IN *)a.dvalue + tok * a.dv + row * os + c;
+                    const float be = sm.g.be[row];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) h8[e] *= be;
+                    if (a.vec_v && c + 8 <= a.dv) {
+                        if constexpr (NIN == 1) {
+                            b16x8 t[1];
+                            split8(h8, t);
+                            store4((float *)op, __builtin_bit_cast(f32x4, t[0]));
+                        } else {
+                            store4((float *)op, f32x4{h8[0], h8[1], h8[2], h8[3]});
+                            store4((float *)op + 4, f32x4{h8[4], h8[5], h8[6], h8[7]});
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (c + e < a.dv) put1(op + e, h8[e]);
+                    }
+                }
             }
         }
         __syncthreads();                             // the blocks have been read: the rows take their place
         if constexpr (NIN == 1) {
             if (a.vec) {
-                direct_rows<C, DKP, NW>(sm.r.k.x[0], (const uint16_t *)kc, a.ks[1], n, a.dk, mt, lane);
-                direct_rows<C, DKP, NW>(sm.r.q.x[0], (const uint16_t *)qc, a.qs[1], n, a.dk, mt, lane);
+                direct_rows<C, DKP, NW>(sm.r.k.x[0], (const uint16_t *)kc, a.ks[1], n, a.dk, wv, lane);
+                direct_rows<C, DKP, NW>(sm.r.q.x[0], (const uint16_t *)qc, a.qs[1], n, a.dk, wv, lane);
             }
         }
         if (NIN == 3 || !a.vec) {
@@ -251,123 +292,122 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_grad_kernel(const S
         }
         hv += __shfl_xor(hv, 16);
         hv += __shfl_xor(hv, 32);
-        if (g == 0) sm.hv[16 * mt + m] = hv;
+        if (g == 0) sm.hv[half][16 * mt + m] = hv;
         ss = sum16(ss);
         ss += __shfl_xor(ss, 16);
         ss += __shfl_xor(ss, 32);
-        if (lane == 0) sm.ss[mt] = ss;
+        if (lane == 0) sm.ss[wv] = ss;
         arrived();
         __syncthreads();
         // dots with the rows of q and k over the wavefront's strips; then sdo
         // becomes dq, dsu dk
-        {
-            float x[NT][4], y[NT][4], e[NT][4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+            const int tk = 16 * t + m;
+            const float gm = sm.g.gam[tk], bg = sm.g.be[tk] * gm, en = sm.g.end[tk];
+            float x = 0.0f, y = 0.0f, e = 0.0f;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[t][r] = y[t][r] = e[t][r] = 0.0f;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const f32x4 gm = *(const f32x4 *)&sm.g.gam[16 * t + 4 * g], be = *(const f32x4 *)&sm.g.be[16 * t + 4 * g];
-                const f32x4 en = *(const f32x4 *)&sm.g.end[16 * t + 4 * g];
-#pragma unroll
-                for (int s = 0; s < ST; ++s) {
-                    const f32x4 kv = sm.r.k.tile(16 * t, 16 * (mt + NT * s), lane);
-                    const f32x4 qv = sm.r.q.tile(16 * t, 16 * (mt + NT * s), lane);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        x[t][r] = fmaf(qv[r], sdo[t][s][r], x[t][r]);
-                        if constexpr (DELTA) y[t][r] = fmaf(kv[r], sh[t][s][r], y[t][r]);
-                        e[t][r] = fmaf(kv[r], dsu[t][s][r], e[t][r]);
-                        sdo[t][s][r] *= gm[r];
-                        dsu[t][s][r] *= en[r];
-                        if constexpr (DELTA) dsu[t][s][r] = fmaf(-be[r] * gm[r], sh[t][s][r], dsu[t][s][r]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int s = 0; s < ST; ++s) {
+                const f32x4 kv = sm.r.k.get4(tk, 16 * (wv + NW * s) + 4 * g);
+                const f32x4 qv = sm.r.q.get4(tk, 16 * (wv + NW * s) + 4 * g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    x[t][r] = sum16(x[t][r]);
-                    if constexpr (DELTA) y[t][r] = sum16(y[t][r]);
-                    e[t][r] = sum16(e[t][r]);
-                    if (m == 0) {
-                        sm.part[0][mt][16 * t + 4 * g + r] = x[t][r];
-                        sm.part[1][mt][16 * t + 4 * g + r] = y[t][r];
-                        sm.part[2][mt][16 * t + 4 * g + r] = e[t][r];
-                    }
+                    x = fmaf(qv[r], sdo[t][s][r], x);
+                    if constexpr (DELTA) y = fmaf(kv[r], sh[t][s][r], y);
+                    e = fmaf(kv[r], dsu[t][s][r], e);
+                    sdo[t][s][r] *= gm;
+                    dsu[t][s][r] *= en;
+                    if constexpr (DELTA) dsu[t][s][r] = fmaf(-bg, sh[t][s][r], dsu[t][s][r]);
                 }
+            }
+            x += __shfl_xor(x, 16);
+            x += __shfl_xor(x, 32);
+            if constexpr (DELTA) {
+                y += __shfl_xor(y, 16);
+                y += __shfl_xor(y, 32);
+            }
+            e += __shfl_xor(e, 16);
+            e += __shfl_xor(e, 32);
+            if (g == 0) {
+                sm.part[0][wv][tk] = x;
+                sm.part[1][wv][tk] = y;
+                sm.part[2][wv][tk] = e;
+            }
         }
-        // A without its borders, dP.D and -beta Z.D
+        // A without its borders, dP.D and -beta Z.D: the wavefront's tiles
         {
-            f32x4 qk[NT], kk[NT];                    // the wavefront's rows of q k^T and k k^T
+            f32x4 qk[NT], kk[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) qk[nt] = kk[nt] = zero;
+            for (int t = 0; t < NT; ++t) qk[t] = kk[t] = zero;
 #pragma unroll
             for (int ks = 0; ks < DKP / 32; ++ks) {
                 b16x8 qa[NIN], ka[NIN];
                 sm.r.q.rows(16 * mt + m, 32 * ks + 8 * g, qa);
                 if constexpr (DELTA) sm.r.k.rows(16 * mt + m, 32 * ks + 8 * g, ka);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    if (nt <= mt) {
+                for (int t = 0; t < NT; ++t)
+                    if (t <= mt && t % RW == half) {
                         b16x8 kb[NIN];
-                        sm.r.k.rows(16 * nt + m, 32 * ks + 8 * g, kb);
-                        qk[nt] = mma<3>(qa, kb, qk[nt]);
-                        if constexpr (DELTA) kk[nt] = mma<3>(ka, kb, kk[nt]);
+                        sm.r.k.rows(16 * t + m, 32 * ks + 8 * g, kb);
+                        qk[t] = mma<3>(kb, qa, qk[t]);
+                        if constexpr (DELTA) kk[t] = mma<3>(kb, ka, kk[t]);
                     }
             }
-            float mz[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            const f32x4 be = *(const f32x4 *)&sm.g.be[16 * mt + 4 * g];
+            const int i = 16 * mt + m;               // the lane's row; its columns j = 16 t + 4 g + r
+            const float be = sm.g.be[i];
+            float mz = 0.0f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (nt > (mt | 1)) continue;
-                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (nt <= mt) decay_tile(sm.g, mt, nt, lane, d);
-                const int colj = 16 * nt + m;
+            for (int t = 0; t < NT; ++t) {
+                if (t > (mt | 1) || t % RW != half) continue;
+                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, pv[4], zv[4];
+                if (t <= mt) decay_turned(sm.g, mt, t, lane, d);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * mt + 4 * g + r;
+                    const int j = 16 * t + 4 * g + r;
                     float zr = 0.0f;
                     if constexpr (DELTA) {
-                        zr = row > colj ? z[nt][r] : 0.0f;
-                        mz[r] = fmaf(kk[nt][r] * d[r], zr, mz[r]);
-                        zr *= -be[r];
-                        sm.r.z.put(row, colj, zr * d[r]);
+                        zr = i > j ? z[t][r] : 0.0f;
+                        mz = fmaf(kk[t][r] * d[r], zr, mz);
+                        zr *= -be;
+                        zv[r] = zr * d[r];
                     }
-                    sm.r.p.put(row, colj, dp[nt][r] * d[r]);
-                    if (row >= colj) sm.r.a[row][colj + 1] = fmaf(dp[nt][r], qk[nt][r], zr * kk[nt][r]);
+                    pv[r] = dp[t][r] * d[r];
+                    if (i >= j) sm.r.a[i][j + 1] = fmaf(dp[t][r], qk[t][r], zr * kk[t][r]);
                 }
+                sm.r.p.put4(i, 16 * t + 4 * g, pv);
+                if constexpr (DELTA) sm.r.z.put4(i, 16 * t + 4 * g, zv);
             }
             if constexpr (DELTA) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    mz[r] = sum16(mz[r]);
-                    if (m == 0) sm.mz[16 * mt + 4 * g + r] = mz[r];
-                }
+                mz += __shfl_xor(mz, 16);
+                mz += __shfl_xor(mz, 32);
+                if (g == 0) sm.mz[half][i] = mz;
             }
         }
         __syncthreads();
         if (tid < C) {
-            float x = 0.0f, y = 0.0f, e = 0.0f;
+            float x = 0.0f, y = 0.0f, e = 0.0f, hvs = 0.0f, mzs = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
+            for (int i = 0; i < NW; ++i) {
                 x += sm.part[0][i][tid];
                 y += sm.part[1][i][tid];
                 e += sm.part[2][i][tid];
+            }
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                hvs += sm.hv[i][tid];
+                if constexpr (DELTA) mzs += sm.mz[i][tid];
             }
             sm.r.a[tid][0] = DELTA ? x - sm.g.be[tid] * y : x;
             sm.r.a[C][tid + 1] = e;
             if (tid == 0) {
                 float s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) s += sm.ss[i];
+                for (int i = 0; i < NW; ++i) s += sm.ss[i];
                 sm.r.a[C][0] = s;
             }
             if (tid < nT)
                 a.dbeta[tok + (int64_t)tid * a.H] =
-                    tid < n ? (DELTA ? sm.hv[tid] - sm.g.gam[tid] * y - sm.mz[tid] : sm.hv[tid]) : 0.0f;
+                    tid < n ? (DELTA ? hvs - sm.g.gam[tid] * y - mzs : hvs) : 0.0f;
         }
         __syncthreads();
         // along j: what row i has read of everything before token t, decayed to
@@ -412,8 +452,8 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_grad_kernel(const S
             b16x8 kv[ST][NIN], qv[ST][NIN];
 #pragma unroll
             for (int s = 0; s < ST; ++s) {
-                sm.r.k.template cols<4>(32 * sb, 16 * (mt + NT * s), lane, kv[s]);
-                sm.r.q.template cols<4>(32 * sb, 16 * (mt + NT * s), lane, qv[s]);
+                sm.r.k.template cols<4>(32 * sb, 16 * (wv + NW * s), lane, kv[s]);
+                sm.r.q.template cols<4>(32 * sb, 16 * (wv + NW * s), lane, qv[s]);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -423,8 +463,8 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_grad_kernel(const S
                     if constexpr (DELTA) sm.r.z.rows(16 * t + m, 32 * sb + 8 * g, y);
 #pragma unroll
                     for (int s = 0; s < ST; ++s) {
-                        sdo[t][s] = mma<NO>(x, kv[s], sdo[t][s]);
-                        if constexpr (DELTA) dsu[t][s] = mma<NO>(y, kv[s], dsu[t][s]);
+                        sdo[t][s] = mma<NO>(kv[s], x, sdo[t][s]);
+                        if constexpr (DELTA) dsu[t][s] = mma<NO>(kv[s], y, dsu[t][s]);
                     }
                 }
                 if (t < 2 * sb + 2) {                // tokens t are read by rows of block sb
@@ -432,8 +472,8 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_grad_kernel(const S
                     if constexpr (DELTA) sm.r.z.template cols<4>(32 * sb, 16 * t, lane, y);
 #pragma unroll
                     for (int s = 0; s < ST; ++s) {
-                        dsu[t][s] = mma<NO>(x, qv[s], dsu[t][s]);
-                        if constexpr (DELTA) dsu[t][s] = mma<NO>(y, kv[s], dsu[t][s]);
+                        dsu[t][s] = mma<NO>(qv[s], x, dsu[t][s]);
+                        if constexpr (DELTA) dsu[t][s] = mma<NO>(kv[s], y, dsu[t][s]);
                     }
                 }
             }
@@ -451,16 +491,14 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_grad_kernel(const S
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int s = 0; s < ST; ++s)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 16 * t + 4 * g + r, key = 16 * (mt + NT * s) + m;
-                        if (row < nT && key < a.dk) {
-                            const int64_t at = (int64_t)row * a.Hk * a.dk + key;
-                            put1(dqp + at, GROUP ? dqa[t][GROUP ? s : 0][r] : sdo[t][s][r]);
-                            put1(dkp + at, GROUP ? dka[t][GROUP ? s : 0][r] : dsu[t][s][r]);
-                        }
+                for (int s = 0; s < ST; ++s) {
+                    const int row = 16 * t + m, key = 16 * (wv + NW * s) + 4 * g;
+                    if (row < nT && key < a.dk) {
+                        const int64_t at = (int64_t)row * a.Hk * a.dk + key;
+                        put4(dqp + at, GROUP ? dqa[t][GROUP ? s : 0] : sdo[t][s], a.vec_g);
+                        put4(dkp + at, GROUP ? dka[t][GROUP ? s : 0] : dsu[t][s], a.vec_g);
                     }
+                }
         }
     }
 }
@@ -468,7 +506,7 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_grad_kernel(const S
 template <typename IN, int DKP>
 hipError_t go(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
     const dim3 grid((unsigned)((int64_t)a.B * a.Hk * w.chunks));
-    constexpr int TH = Cfg<IN>::C * 4;
+    constexpr int TH = 64 * grad_waves<IN, DKP>();
     if (a.H > a.Hk) {
         if (a.delta) lores_scan_grad_kernel<IN, DKP, true, true><<<grid, TH, 0, s>>>(a, w);
         else lores_scan_grad_kernel<IN, DKP, false, true><<<grid, TH, 0, s>>>(a, w);

@@ -27,6 +27,7 @@ namespace scan {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
@@ -61,6 +62,25 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, b16x2));
 }
 
+// Four neighbours of a row to memory (vec: a whole piece of 4 elements).
+__device__ __forceinline__ void put4(float *p, f32x4 v, bool vec) {
+    if (vec) {
+        store4(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = v[e];
+    }
+}
+__device__ __forceinline__ void put4(uint16_t *p, f32x4 v, bool vec) {
+    const u32x2 w = {pack2(v[0], v[1]), pack2(v[2], v[3])};
+    if (vec) {
+        *(u32x2 *)p = w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+
 // x = p[0] + p[1] + ... up to the last plane's rounding
 template <int NP>
 __device__ __forceinline__ void split8(const float (&x)[8], b16x8 (&p)[NP]) {
@@ -79,6 +99,22 @@ __device__ __forceinline__ void split8(const float (&x)[8], b16x8 (&p)[NP]) {
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i) p[i] = __builtin_bit_cast(b16x8, w[i]);
+}
+
+// The planes of four values, each handed to put(plane, bits).
+template <int NP, typename F>
+__device__ __forceinline__ void split4(const float (&v)[4], F put) {
+    float a[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const u32x2 w = {pack2(a[0], a[1]), pack2(a[2], a[3])};
+        put(i, w);
+        if (i + 1 < NP) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                a[e] -= __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+        }
+    }
 }
 
 // 8 neighbours of a row at p, the first `n` of which exist (vec: 16-byte
@@ -222,26 +258,21 @@ struct Planes {
 #pragma unroll
         for (int i = 0; i < N; ++i) *(b16x8 *)&x[i][at_(row, c)] = o[i];
     }
-    // rows r0 + 4 g + r of column c0 + (lane & 15): a result tile's layout
-    __device__ __forceinline__ f32x4 tile(int r0, int c0, int lane) const {
-        typedef __attribute__((address_space(3))) s16x4 lds4;
-        const int i = lane & 15, at = at_(r0 + 4 * (lane >> 4) + (i >> 2), c0 + 4 * (i & 3));
+    // four neighbours c .. c + 3 of a row (c a multiple of 4)
+    __device__ __forceinline__ f32x4 get4(int row, int c) const {
+        const int at = at_(row, c);
         f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)&x[k][at]);
+            const u32x2 w = *(const u32x2 *)&x[k][at];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s[r] += bf2f((uint16_t)v[r]);
+            for (int e = 0; e < 4; ++e)
+                s[e] += __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
         }
         return s;
     }
-    __device__ __forceinline__ void put(int row, int c, float v) {
-        const int p = at_(row, c);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            x[i][p] = f2bf(v);
-            if (i + 1 < NP) v -= bf2f(x[i][p]);
-        }
+    __device__ __forceinline__ void put4(int row, int c, const float (&v)[4]) {
+        split4<NP>(v, [&](int i, u32x2 w) { *(u32x2 *)&x[i][at_(row, c)] = w; });
     }
 };
 
@@ -262,12 +293,8 @@ struct Gates {
     float be[C];     // beta (0 behind it)
     float gam[C];    // gamma_i = alpha_0 .. alpha_i of the chunk
     float end[C];    // D_Cj: alpha_{j+1} .. alpha_{C-1}
-};
-
-// Products of alpha within the 16-token strips, for D_ij between tokens of
-// different strips: pre_i (the strips between, multiplied up) suf_j.
-template <int C>
-struct Strips {
+    // within the 16-token strips, for D_ij between tokens of different strips:
+    // pre_i (the strips between, multiplied up) suf_j
     float pre[C];    // alpha from the strip's first token to i
     float suf[C];    // alpha behind j to the strip's last token
 };
@@ -286,7 +313,7 @@ __device__ __forceinline__ float scan_product(float x, int lane) {
 
 // One wavefront's share `part` of 4 of a chunk's gates; n tokens are there.
 template <int C>
-__device__ __forceinline__ void make_gates(Gates<C> &g, Strips<C> &s, int part, const float *alpha,
+__device__ __forceinline__ void make_gates(Gates<C> &g, int part, const float *alpha,
                                            const float *beta, int64_t stride, int n, int lane) {
     const int l = lane & (C - 1);
     const float a = l < n ? alpha[l * stride] : 1.0f;
@@ -299,23 +326,22 @@ __device__ __forceinline__ void make_gates(Gates<C> &g, Strips<C> &s, int part, 
         if (lane < C) g.end[l] = l == C - 1 ? 1.0f : x;
     } else if (part == 2) {
         const float x = scan_product<16, true>(a, lane);
-        if (lane < C) s.pre[l] = x;
+        if (lane < C) g.pre[l] = x;
     } else {
         const float x = __shfl_down(scan_product<16, false>(a, lane), 1, 16);
-        if (lane < C) s.suf[l] = (l & 15) == 15 ? 1.0f : x;
+        if (lane < C) g.suf[l] = (l & 15) == 15 ? 1.0f : x;
     }
 }
 
 // D_ij of the tile (mt, nt <= mt) turned over: the lane's row i = 16 mt + (lane &
 // 15) and columns j = 16 nt + 4 (lane / 16) + r; zero where j > i.
 template <int C>
-__device__ __forceinline__ void decay_turned(const Gates<C> &g, const Strips<C> &s, int mt, int nt,
-                                             int lane, float (&d)[4]) {
+__device__ __forceinline__ void decay_turned(const Gates<C> &g, int mt, int nt, int lane, float (&d)[4]) {
     const int m = lane & 15, q = lane >> 4, i = 16 * mt + m;
     if (nt < mt) {
-        float x = s.pre[i];
-        for (int k = nt + 1; k < mt; ++k) x *= s.pre[16 * k + 15];
-        const f32x4 sj = *(const f32x4 *)&s.suf[16 * nt + 4 * q];
+        float x = g.pre[i];
+        for (int k = nt + 1; k < mt; ++k) x *= g.pre[16 * k + 15];
+        const f32x4 sj = *(const f32x4 *)&g.suf[16 * nt + 4 * q];
 #pragma unroll
         for (int r = 0; r < 4; ++r) d[r] = x * sj[r];
     } else {
@@ -331,27 +357,6 @@ __device__ __forceinline__ void decay_turned(const Gates<C> &g, const Strips<C> 
             d[r] = 4 * q + r <= m ? x : 0.0f;
             if (4 * q + r <= m) x *= al[r];
         }
-    }
-}
-
-// D_ij of the 16 x 16 tile (mt, nt <= mt) for the lane's column j = 16 nt +
-// (lane & 15) and rows i = 16 mt + 4 (lane / 16) + r; zero above the diagonal.
-// Each is a product of the alphas between, in an order that depends on the
-// tile alone.
-template <int C>
-__device__ __forceinline__ void decay_tile(const Gates<C> &g, int mt, int nt, int lane, float (&d)[4]) {
-    const int j = 16 * nt + (lane & 15), i0 = 16 * mt + 4 * (lane >> 4);
-    float x = 1.0f;
-    if (nt < mt) {
-        for (int l = 16 * nt + 1; l < 16 * mt; ++l) x *= l > j ? g.al[l] : 1.0f;
-        for (int l = 16 * mt; l < i0; ++l) x *= g.al[l];
-    } else {
-        for (int l = 16 * mt + 1; l < i0; ++l) x *= l > j ? g.al[l] : 1.0f;
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        if (i0 + r > j) x *= g.al[i0 + r];
-        d[r] = i0 + r >= j ? x : 0.0f;
     }
 }
 
@@ -387,18 +392,7 @@ struct Tri {
     // the transpose's: 8 rows 8 g .. + 7 of one column of block (I, J) (see Planes::cols)
     // four neighbours of one row, as planes
     __device__ __forceinline__ void put4(int I, int J, int row, int c, const float (&v)[4]) {
-        float a[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-            const u32x2 w = {pack2(a[0], a[1]), pack2(a[2], a[3])};
-            *(u32x2 *)&x[i][tri_block(I, J)][row][c] = w;
-            if (i + 1 < NP) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    a[e] -= __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-            }
-        }
+        split4<NP>(v, [&](int i, u32x2 w) { *(u32x2 *)&x[i][tri_block(I, J)][row][c] = w; });
     }
     template <int STEP, int N>
     __device__ __forceinline__ void cols(int I, int J, int c0, int lane, b16x8 (&o)[N]) const {

@@ -23,7 +23,6 @@ template <typename IN, int NP>
 struct PrepLds {
     static constexpr int C = Cfg<IN>::C, NT = C / 16;
     Gates<C> g;
-    Strips<C> s;
     float nt[NT * (NT - 1) / 2 + 1][16][20];         // N_KJ turned over (rows j), tile K (K - 1) / 2 + J
     float nd[NT][16][20];                            // N_II, then X_II
     Tri<3, C> x;
@@ -81,14 +80,14 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
         const int64_t unit = ((int64_t)b * a.H + h) * w.chunks + chunk;
         if (gi) __syncthreads();                     // the last head's arrays have been read
 #pragma unroll
-        for (int q = 0; q < 4; q += NW) make_gates(sm.g, sm.s, q + mt, a.alpha + gate, a.beta + gate, a.H, n, lane);
+        for (int q = 0; q < 4; q += NW) make_gates(sm.g, q + mt, a.alpha + gate, a.beta + gate, a.H, n, lane);
         __syncthreads();
         const float be = sm.g.be[16 * mt + m];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (t > (mt | 1)) continue;              // blocks of 32 tokens above the diagonal are not read
             float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4];
-            if (t <= mt) decay_turned(sm.g, sm.s, mt, t, lane, d);
+            if (t <= mt) decay_turned(sm.g, mt, t, lane, d);
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] = qk[t][r] * d[r];
             sm.p.put4(mt >> 1, t >> 1, 16 * (mt & 1) + m, 16 * (t & 1) + 4 * g, v);
@@ -127,7 +126,7 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
         }
         __syncthreads();
         // what is done goes to memory while X is made
-        for (int i = tid; i < C; i += TH) ((f32x4 *)(w.G + unit * 4 * C))[i] = ((const f32x4 *)&sm.g.al[0])[i];
+        for (int i = tid; i < 6 * C / 4; i += TH) ((f32x4 *)(w.G + unit * 6 * C))[i] = ((const f32x4 *)&sm.g.al[0])[i];
         for (int i = tid; i < NP * NB * 128; i += TH)
             ((u32x4 *)(w.P + unit * NP * NB * 1024))[i] = ((const u32x4 *)&sm.p.x[0])[i];
         if constexpr (!DELTA) continue;
@@ -193,13 +192,13 @@ uint64_t plan_scan_work(bool in_bf16, bool backward, const ScanArgs &a, void *ba
     const uint64_t tri = scan::tri_blocks((int)C) * 2048;       // bytes of a plane
     w->X = (uint16_t *)(a.delta ? cut(units * 3 * tri) : nullptr);
     w->P = (uint16_t *)cut(units * w->p_planes * tri);
-    w->G = (float *)cut(units * 4 * C * 4);
+    w->G = (float *)cut(units * 6 * C * 4);
     w->S = w->dS = w->U = w->Hm = nullptr;
     if (backward) {
-        w->S = (uint16_t *)cut(units * 3 * a.dk * w->dvp * 2);
-        w->dS = (uint16_t *)cut(units * 3 * a.dk * w->dvp * 2);
-        w->U = (uint16_t *)cut(units * 3 * C * w->dvp * 2);
-        w->Hm = (uint16_t *)cut(units * 3 * C * w->dvp * 2);
+        w->S = (float *)cut(units * a.dk * w->dvp * 4);
+        w->dS = (float *)cut(units * a.dk * w->dvp * 4);
+        w->U = (float *)cut(units * C * w->dvp * 4);
+        w->Hm = (float *)cut(units * C * w->dvp * 4);
     }
     return off;
 }

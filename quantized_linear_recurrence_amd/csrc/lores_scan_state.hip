@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
         } else if (part == 2) {
             if constexpr (!BACK) direct_block<sizeof(to.p), NW>(w.P + cu * (NO * Tri<1, C>::NB * 1024), &to.p, wv, lane);
             if constexpr (DELTA) direct_block<sizeof(to.x), NW>(w.X + cu * (3 * Tri<1, C>::NB * 1024), &to.x, wv, lane);
-            direct_block<sizeof(to.g), NW>(w.G + cu * (4 * C), &to.g, wv, lane);
+            direct_block<sizeof(to.g), NW>(w.G + cu * (6 * C), &to.g, wv, lane);
         } else if (mine) {
             if constexpr (VEC) {
                 to.v[wv].fetch(vb + t0 * a.vs[1], a.vs[1], n, a.dv - col0, lane);
@@ -187,20 +187,11 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
         }
         if (more) fetch(1, ch + 1, next);
         if constexpr (BACK) {
-            if constexpr (!DELTA) {
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) split(ks);
-            }
-            // the chunk's first state, as planes
-            uint16_t *sp0 = w.S + cu * 3 * w.dvp * a.dk;
+            float *sp0 = w.S + cu * w.dvp * a.dk;
             const uint32_t at = (uint32_t)col * (uint32_t)a.dk + 8 * g;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                if (32 * ks < a.dk) {
-#pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        store4((float *)(sp0 + (uint32_t)(i * w.dvp * a.dk) + (at + 32 * ks)), __builtin_bit_cast(f32x4, sp[ks][i]));
-                }
+            for (int t = 0; t < 2 * KS; ++t)
+                if (32 * (t >> 1) < a.dk) store4(sp0 + (at + 32 * (t >> 1) + 4 * (t & 1)), st[t]);
         }
         // Q S^T, and beside it E and its planes
         b16x8 ep[SB][3];
@@ -252,7 +243,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
         }
         if (more) fetch(2, ch + 1, next);
         // the last products' left operands come while U is made
-        b16x8 kt[2 * KS][NIN], pv[BACK ? 1 : MT][NO], ut[SB][3], up[SB][BACK ? 3 : NO];
+        b16x8 kt[2 * KS][NIN], pv[BACK ? 1 : MT][NO], ut[SB][3], up[SB][NO];
         f32x4 en[MT];
         auto turned = [&](int sb) {
 #pragma unroll
@@ -298,7 +289,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
         auto split_u = [&](int sb) {
             float x[8];
             pair8(u[2 * sb], u[2 * sb + 1], x);
-            split8(x, up[sb]);
+            if constexpr (!BACK) split8(x, up[sb]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] *= i < 4 ? en[2 * sb][i] : en[2 * sb + 1][i - 4];
             split8(x, ut[sb]);
@@ -320,13 +311,9 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
             mma_all<3, 2 * KS>(kt, ut[SB - 1], st);
         }
         if constexpr (BACK) {
-            uint16_t *u0 = w.U + cu * 3 * w.dvp * C;
+            float *u0 = w.U + cu * w.dvp * C;
 #pragma unroll
-            for (int sb = 0; sb < SB; ++sb)
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    store4((float *)(u0 + (uint32_t)(i * w.dvp * C) + (uint32_t)(col * C + 32 * sb + 8 * g)),
-                           __builtin_bit_cast(f32x4, up[sb][i]));
+            for (int mt = 0; mt < MT; ++mt) store4(u0 + (uint32_t)(col * C + token_of(mt, 4 * g)), u[mt]);
         } else {
             const int nT = min(a.T - t0, C);
             IN *oc = ob + t0 * os;

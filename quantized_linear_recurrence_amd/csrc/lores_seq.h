@@ -52,6 +52,7 @@ struct ScanArgs {
     const float *S0;                   // [B][H][dv][dk], or NULL: zero
     void *o;                           // [B][T][H][dv], input type
     float *S;                          // [B][H][dv][dk], or NULL
+    int32_t vec_g;                     // dq and dk rows are 16-byte aligned
     // backward
     const void *dout;                  // [B][T][H][dv], input type
     const float *dS;                   // [B][H][dv][dk], or NULL: zero
@@ -69,14 +70,13 @@ __host__ __device__ constexpr int scan_chunk(bool in_bf16) { return in_bf16 ? 64
 
 // Workspace of a chunked scan, cut from the caller's buffer.  Per (sequence,
 // head, chunk): the planes of X and P, the gates, and for the backward pass the state
-// and its gradient at the chunk's two ends and U and H, as planes too, value
-// rows first.
+// and its gradient at the chunk's two ends and U and H, value rows first.
 struct ScanWork {
     uint16_t *X;                       // [B][H][chunks][3][blocks][32][32]
     uint16_t *P;                       // [B][H][chunks][p_planes][blocks][32][32]
-    float *G;                          // [B][H][chunks][4][C]: alpha, beta, gamma, D_Cj
-    uint16_t *S, *dS;                  // [B][H][chunks][3][dvp][dk]
-    uint16_t *U, *Hm;                  // [B][H][chunks][3][dvp][C]
+    float *G;                          // [B][H][chunks][6][C]: Gates
+    float *S, *dS;                     // [B][H][chunks][dvp][dk]
+    float *U, *Hm;                     // [B][H][chunks][dvp][C]
     int32_t chunks, p_planes, dvp;
 };
 // Lays `w` out over `base` (which may be NULL) and returns the bytes.

@@ -193,6 +193,7 @@ int lores_scan_backward(const lores_scan_dims *dims, const void *q, const void *
     a.dbeta = dbeta;
     a.dS0 = dS_first;
     if (!aligned(dout, 16) || !aligned(dv, 16)) a.vec_v = 0;
+    a.vec_g = aligned(dq, 16) && aligned(dk, 16);
     lores::ScanWork w;
     std::memset(&w, 0, sizeof w);
     const uint64_t need = scan_work(dims, 1, work, &w);
