@@ -74,8 +74,9 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
     const int mt = wv / RW, half = wv % RW;          // the wavefront's row of tiles, its share of it
-    const int chunk = blockIdx.x % w.chunks;
-    const int bk = blockIdx.x / w.chunks, b = bk / a.Hk, hk = bk - b * a.Hk, G = GROUP ? a.H / a.Hk : 1;
+    int b, hk, chunk;
+    if (!chunk_of(blockIdx.x, a, w, &b, &hk, &chunk)) return;
+    const int G = GROUP ? a.H / a.Hk : 1;
     int len = a.T;
     if (a.lengths) len = min(max(a.lengths[b], 0), a.T);
     const int t0 = chunk * C, n = min(max(len - t0, 0), C), nT = min(a.T - t0, C);
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
 
 template <typename IN, int DKP>
 hipError_t go(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)a.B * a.Hk * w.chunks));
+    const dim3 grid = chunk_grid(a, w);
     constexpr int TH = 64 * grad_waves<IN, DKP>();
     if (a.H > a.Hk) {
         if (a.delta) lores_scan_grad_kernel<IN, DKP, true, true><<<grid, TH, 0, s>>>(a, w);

@@ -311,14 +311,12 @@ __device__ __forceinline__ float scan_product(float x, int lane) {
     return x;
 }
 
-// One wavefront's share `part` of 4 of a chunk's gates; n tokens are there.
+// One wavefront's share `part` of 4 of a chunk's gates, from the lane's alpha
+// and beta (of token lane mod C; 1 and 0 behind the sequence's end).
 template <int C>
-__device__ __forceinline__ void make_gates(Gates<C> &g, int part, const float *alpha,
-                                           const float *beta, int64_t stride, int n, int lane) {
+__device__ __forceinline__ void make_gates(Gates<C> &g, int part, float a, float b, int lane) {
     const int l = lane & (C - 1);
-    const float a = l < n ? alpha[l * stride] : 1.0f;
     if (part == 0) {
-        const float b = l < n ? beta[l * stride] : 0.0f;
         const float x = scan_product<C, true>(a, lane);
         if (lane < C) { g.al[l] = a; g.be[l] = b; g.gam[l] = x; }
     } else if (part == 1) {
@@ -574,6 +572,22 @@ __device__ __forceinline__ bool unit_of(int block, int groups, int units, int *u
     *grp = y % groups;
     *unit = y / groups * 8 + x;
     return *unit < units;
+}
+
+// The chunks' order along the grid of the kernels that take all at once: an
+// XCD gets all key heads of a chunk one after the other, which read and write
+// neighbouring words of alpha and beta's lines.
+__device__ __forceinline__ bool chunk_of(int block, const ScanArgs &a, const ScanWork &w, int *b, int *hk,
+                                         int *chunk) {
+    const int x = block & 7, y = block >> 3;
+    const int at = y / a.Hk * 8 + x;                 // sequence and chunk
+    *hk = y % a.Hk;
+    *b = at / w.chunks;
+    *chunk = at - *b * w.chunks;
+    return *b < a.B;
+}
+inline dim3 chunk_grid(const ScanArgs &a, const ScanWork &w) {
+    return dim3((unsigned)(((int64_t)a.B * w.chunks + 7) / 8 * 8 * a.Hk));
 }
 
 }  // namespace scan

@@ -19,25 +19,31 @@ namespace lores {
 namespace scan {
 namespace {
 
-template <typename IN, int NP>
+template <typename IN, int DKP, int NP>
 struct PrepLds {
-    static constexpr int C = Cfg<IN>::C, NT = C / 16;
+    static constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16;
     Gates<C> g;
-    float nt[NT * (NT - 1) / 2 + 1][16][20];         // N_KJ turned over (rows j), tile K (K - 1) / 2 + J
-    float nd[NT][16][20];                            // N_II, then X_II
-    Tri<3, C> x;
-    Tri<NP, C> p;
+    union {
+        struct { Planes<NIN, C, DKP> k, q; } r;      // until the tiles of q k^T and k k^T are made
+        struct {
+            float nt[NT * (NT - 1) / 2 + 1][16][20]; // N_KJ turned over (rows j), tile K (K - 1) / 2 + J
+            float nd[NT][16][20];                    // N_II, then X_II
+            Tri<3, C> x;
+            Tri<NP, C> p;
+        } t;
+    };
 };
 
 // NP: planes of P.
-template <typename IN, int NP, bool DELTA>
+template <typename IN, int DKP, int NP, bool DELTA>
 __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const ScanArgs a, const ScanWork w) {
     constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, NB = tri_blocks(C), NW = NT, TH = 64 * NW;
-    __shared__ __attribute__((aligned(16))) PrepLds<IN, NP> sm;
+    __shared__ __attribute__((aligned(16))) PrepLds<IN, DKP, NP> sm;
     const int tid = threadIdx.x, lane = tid & 63, mt = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
-    const int chunk = blockIdx.x % w.chunks;
-    const int bk = blockIdx.x / w.chunks, b = bk / a.Hk, hk = bk - b * a.Hk, G = a.H / a.Hk;
+    int b, hk, chunk;
+    if (!chunk_of(blockIdx.x, a, w, &b, &hk, &chunk)) return;
+    const int G = a.H / a.Hk;
     int len = a.T;
     if (a.lengths) len = min(max(a.lengths[b], 0), a.T);
     const int t0 = chunk * C, n = min(len - t0, C);
@@ -48,39 +54,47 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
     f32x4 qk[NT], kk[NT];                            // rows j = 16 nt + 4 g + r of column i = 16 mt + m
 #pragma unroll
     for (int t = 0; t < NT; ++t) qk[t] = kk[t] = zero;
-    {
-        const int row = 16 * mt + m;
-        const IN *qr = qp + (int64_t)min(row, n - 1) * a.qs[1];
-        for (int k0 = 0; k0 < a.dk; k0 += 64) {
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const int c = k0 + 32 * ks + 8 * g;
-                if (k0 + 32 * ks >= a.dk) continue;
-                b16x8 qv[NIN], kv[NT][NIN];
-                get_planes(qr + c, row < n ? 8 : 0, a.vec, qv);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    if (t <= mt) get_planes(kp + (int64_t)min(16 * t + m, n - 1) * a.ks[1] + c, 16 * t + m < n ? 8 : 0, a.vec, kv[t]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    if (t <= mt) {
-                        qk[t] = mma<3>(kv[t], qv, qk[t]);
-                        if constexpr (DELTA) {
-#pragma unroll
-                            for (int u = 0; u < NT; ++u)
-                                if (u == mt) kk[t] = mma<3>(kv[t], kv[u], kk[t]);
-                        }
-                    }
-            }
+    // the first head's gates are on their way with the rows
+    const int l = lane & (C - 1);
+    const int64_t gate0 = ((int64_t)b * a.T + t0) * a.H + hk * G + (int64_t)min(l, n - 1) * a.H;
+    float al = a.alpha[gate0], bt = a.beta[gate0];
+    if constexpr (NIN == 1) {
+        if (a.vec) {
+            direct_rows<C, DKP, NW>(sm.r.k.x[0], (const uint16_t *)kp, a.ks[1], n, a.dk, mt, lane);
+            direct_rows<C, DKP, NW>(sm.r.q.x[0], (const uint16_t *)qp, a.qs[1], n, a.dk, mt, lane);
         }
+    }
+    if (NIN == 3 || !a.vec) {
+        stage_rows(sm.r.k, kp, a.ks[1], n, a.dk, a.vec, tid, TH);
+        stage_rows(sm.r.q, qp, a.qs[1], n, a.dk, a.vec, tid, TH);
+    }
+    arrived();
+    __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < DKP / 32; ++ks) {
+        b16x8 qv[NIN], ko[NIN], kv[NT][NIN];
+        sm.r.q.rows(16 * mt + m, 32 * ks + 8 * g, qv);
+        if constexpr (DELTA) sm.r.k.rows(16 * mt + m, 32 * ks + 8 * g, ko);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            if (t <= mt) sm.r.k.rows(16 * t + m, 32 * ks + 8 * g, kv[t]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            if (t <= mt) {
+                qk[t] = mma<3>(kv[t], qv, qk[t]);
+                if constexpr (DELTA) kk[t] = mma<3>(kv[t], ko, kk[t]);
+            }
     }
     for (int gi = 0; gi < G; ++gi) {
         const int h = hk * G + gi;
-        const int64_t gate = ((int64_t)b * a.T + t0) * a.H + h;
         const int64_t unit = ((int64_t)b * a.H + h) * w.chunks + chunk;
-        if (gi) __syncthreads();                     // the last head's arrays have been read
+        __syncthreads();                             // the rows, or the last head's arrays, have been read
 #pragma unroll
-        for (int q = 0; q < 4; q += NW) make_gates(sm.g, q + mt, a.alpha + gate, a.beta + gate, a.H, n, lane);
+        for (int q = 0; q < 4; q += NW) make_gates(sm.g, q + mt, l < n ? al : 1.0f, l < n ? bt : 0.0f, lane);
+        if (gi + 1 < G) {
+            al = a.alpha[gate0 + gi + 1];
+            bt = a.beta[gate0 + gi + 1];
+        }
         __syncthreads();
         const float be = sm.g.be[16 * mt + m];
 #pragma unroll
@@ -90,16 +104,16 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
             if (t <= mt) decay_turned(sm.g, mt, t, lane, d);
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] = qk[t][r] * d[r];
-            sm.p.put4(mt >> 1, t >> 1, 16 * (mt & 1) + m, 16 * (t & 1) + 4 * g, v);
+            sm.t.p.put4(mt >> 1, t >> 1, 16 * (mt & 1) + m, 16 * (t & 1) + 4 * g, v);
             if constexpr (DELTA) {
                 if (t > mt) continue;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = t < mt || 4 * g + r < m ? be * (kk[t][r] * d[r]) : 0.0f;
                 if (t < mt) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sm.nt[mt * (mt - 1) / 2 + t][4 * g + r][m] = v[r];
+                    for (int r = 0; r < 4; ++r) sm.t.nt[mt * (mt - 1) / 2 + t][4 * g + r][m] = v[r];
                 } else {
-                    *(f32x4 *)&sm.nd[mt][m][4 * g] = f32x4{v[0], v[1], v[2], v[3]};
+                    *(f32x4 *)&sm.t.nd[mt][m][4 * g] = f32x4{v[0], v[1], v[2], v[3]};
                 }
             }
         }
@@ -112,7 +126,7 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
                 float s = i == m ? 1.0f : 0.0f;
 #pragma unroll
                 for (int l = 0; l < i; l += 4) {
-                    const f32x4 nr = *(const f32x4 *)&sm.nd[mt][i][l];
+                    const f32x4 nr = *(const f32x4 *)&sm.t.nd[mt][i][l];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (l + e < i) s = fmaf(-nr[e], x[l + e], s);
@@ -121,14 +135,14 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
             }
             if (g == 0) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sm.nd[mt][i][m] = x[i];
+                for (int i = 0; i < 16; ++i) sm.t.nd[mt][i][m] = x[i];
             }
         }
         __syncthreads();
         // what is done goes to memory while X is made
         for (int i = tid; i < 6 * C / 4; i += TH) ((f32x4 *)(w.G + unit * 6 * C))[i] = ((const f32x4 *)&sm.g.al[0])[i];
         for (int i = tid; i < NP * NB * 128; i += TH)
-            ((u32x4 *)(w.P + unit * NP * NB * 1024))[i] = ((const u32x4 *)&sm.p.x[0])[i];
+            ((u32x4 *)(w.P + unit * NP * NB * 1024))[i] = ((const u32x4 *)&sm.t.p.x[0])[i];
         if constexpr (!DELTA) continue;
         f32x4 xt[NT];                                // X_IJ of block row I = mt: rows j, column i
 #pragma unroll
@@ -136,13 +150,13 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
             xt[J] = zero;
             if (J > mt) continue;
             if (J == mt) {
-                xt[J] = *(const f32x4 *)&sm.nd[mt][m][4 * g];
+                xt[J] = *(const f32x4 *)&sm.t.nd[mt][m][4 * g];
             } else {
                 f32x4 s = zero;
 #pragma unroll
                 for (int K = 0; K < NT; ++K)
                     if (K > J && K <= mt) {
-                        const f32x4 nr = *(const f32x4 *)&sm.nt[K * (K - 1) / 2 + J][m][4 * g];
+                        const f32x4 nr = *(const f32x4 *)&sm.t.nt[K * (K - 1) / 2 + J][m][4 * g];
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             s = __builtin_amdgcn_mfma_f32_16x16x4f32(nr[r], xt[K][r], s, 0, 0, 0);
@@ -150,7 +164,7 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
                 f32x4 y = zero;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    y = __builtin_amdgcn_mfma_f32_16x16x4f32(sm.nd[J][4 * g + r][m], s[r], y, 0, 0, 0);
+                    y = __builtin_amdgcn_mfma_f32_16x16x4f32(sm.t.nd[J][4 * g + r][m], s[r], y, 0, 0, 0);
                 xt[J] = -y;
             }
         }
@@ -158,20 +172,27 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4) lores_scan_prep_kernel(const S
         for (int J = 0; J < NT; ++J) {
             if (J > (mt | 1)) continue;
             const float v[4] = {xt[J][0], xt[J][1], xt[J][2], xt[J][3]};
-            sm.x.put4(mt >> 1, J >> 1, 16 * (mt & 1) + m, 16 * (J & 1) + 4 * g, v);
+            sm.t.x.put4(mt >> 1, J >> 1, 16 * (mt & 1) + m, 16 * (J & 1) + 4 * g, v);
         }
         __syncthreads();
         for (int i = tid; i < 3 * NB * 128; i += TH)
-            ((u32x4 *)(w.X + unit * 3 * NB * 1024))[i] = ((const u32x4 *)&sm.x.x[0])[i];
+            ((u32x4 *)(w.X + unit * 3 * NB * 1024))[i] = ((const u32x4 *)&sm.t.x.x[0])[i];
     }
 }
 
-template <typename IN, int NP>
+template <typename IN, int DKP, int NP>
 hipError_t go(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)a.B * a.Hk * w.chunks));
-    if (a.delta) lores_scan_prep_kernel<IN, NP, true><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
-    else lores_scan_prep_kernel<IN, NP, false><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
+    const dim3 grid = chunk_grid(a, w);
+    if (a.delta) lores_scan_prep_kernel<IN, DKP, NP, true><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
+    else lores_scan_prep_kernel<IN, DKP, NP, false><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
     return hipGetLastError();
+}
+
+template <typename IN, int NP>
+hipError_t by_width(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
+    if (a.dk <= 64) return go<IN, 64, NP>(a, w, s);
+    if (a.dk <= 128) return go<IN, 128, NP>(a, w, s);
+    return go<IN, 256, NP>(a, w, s);
 }
 
 }  // namespace
@@ -204,8 +225,8 @@ uint64_t plan_scan_work(bool in_bf16, bool backward, const ScanArgs &a, void *ba
 }
 
 hipError_t launch_scan_prep(bool in_bf16, const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    if (!in_bf16) return scan::go<float, 3>(a, w, s);
-    return w.p_planes == 2 ? scan::go<uint16_t, 2>(a, w, s) : scan::go<uint16_t, 3>(a, w, s);
+    if (!in_bf16) return scan::by_width<float, 3>(a, w, s);
+    return w.p_planes == 2 ? scan::by_width<uint16_t, 2>(a, w, s) : scan::by_width<uint16_t, 3>(a, w, s);
 }
 
 }  // namespace lores

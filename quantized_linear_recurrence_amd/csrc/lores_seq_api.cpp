@@ -52,8 +52,8 @@ int check_scan(const lores_scan_dims *d) {
             d->v_stride[i] > ((int64_t)1 << 40))
             return fail(LORES_EINVAL, "strides must be in [0, 2^40]");
     // the largest grid: 8 tiles of 32 value rows, or one work-group per chunk
-    const int64_t chunks = (d->T + 31) / 32;
-    if ((int64_t)d->B * d->H * (chunks > 8 ? chunks : 8) > kMaxGroups)
+    const int64_t chunks = (d->T + 31) / 32 + 8;     // and rounding up to 8 at the end
+    if (((int64_t)d->B * chunks + 8) * d->H > kMaxGroups)
         return fail(LORES_EINVAL, "B x H x T is too large for one call");
     return LORES_OK;
 }
