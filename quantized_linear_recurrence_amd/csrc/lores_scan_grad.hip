@@ -48,9 +48,18 @@ struct GradRows {                                    // when they have all gone 
     float a[C + 1][C + 1];                           // A, row C and column 0 its borders
 };
 
+// The sums over the heads of a group: a wavefront's own results, kept in LDS
+// where they fit beside the rest (they would not leave enough registers).
 template <typename IN, int DKP, int NW>
+constexpr bool group_in_lds() {
+    return (sizeof(GradBlock<IN, DKP>) > sizeof(GradRows<IN, DKP>) ? sizeof(GradBlock<IN, DKP>) : sizeof(GradRows<IN, DKP>)) +
+               Cfg<IN>::C * DKP * 8 <= 152 * 1024;
+}
+
+template <typename IN, int DKP, int NW, bool GROUP>
 struct GradLds {
     static constexpr int C = Cfg<IN>::C;
+    f32x4 acc[GROUP && group_in_lds<IN, DKP, NW>() ? C * DKP / 2 : 1];
     union {
         GradBlock<IN, DKP> b;
         GradRows<IN, DKP> r;
@@ -70,9 +79,9 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
     constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, SB = C / 32, NW = grad_waves<IN, DKP>(), TH = 64 * NW;
     constexpr int ST = DKP / 16 / NW, RW = NW / NT;  // strips of a wavefront, wavefronts of a row
     constexpr int NO = sizeof(IN) == 2 ? 2 : 3;      // planes of what ends in the inputs' type
-    __shared__ __attribute__((aligned(16))) GradLds<IN, DKP, NW> sm;
-    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int m = lane & 15, g = lane >> 4;
+    __shared__ __attribute__((aligned(16))) GradLds<IN, DKP, NW, GROUP> sm;
+    constexpr bool ACC = GROUP && group_in_lds<IN, DKP, NW>();
+    const int tid0 = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid0 >> 6);
     const int mt = wv / RW, half = wv % RW;          // the wavefront's row of tiles, its share of it
     int b, hk, chunk;
     if (!chunk_of(blockIdx.x, a, w, &b, &hk, &chunk)) return;
@@ -83,16 +92,16 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
     IN *dqp = (IN *)a.dq + (((int64_t)b * a.T + t0) * a.Hk + hk) * a.dk;
     IN *dkp = (IN *)a.dkey + (((int64_t)b * a.T + t0) * a.Hk + hk) * a.dk;
     if (n == 0) {                                    // behind the sequence's end
-        for (int x = tid; x < nT * a.dk; x += TH) {
+        for (int x = tid0; x < nT * a.dk; x += TH) {
             const int64_t at = (int64_t)(x / a.dk) * a.Hk * a.dk + x % a.dk;
             put1(dqp + at, 0.0f);
             put1(dkp + at, 0.0f);
         }
         for (int gi = 0; gi < G; ++gi) {
             const int h = hk * G + gi;
-            for (int x = tid; x < nT * a.dv; x += TH)
+            for (int x = tid0; x < nT * a.dv; x += TH)
                 put1((IN *)a.dvalue + (((int64_t)b * a.T + t0 + x / a.dv) * a.H + h) * a.dv + x % a.dv, 0.0f);
-            for (int x = tid; x < nT; x += TH) {
+            for (int x = tid0; x < nT; x += TH) {
                 a.dalpha[((int64_t)b * a.T + t0 + x) * a.H + h] = 0.0f;
                 a.dbeta[((int64_t)b * a.T + t0 + x) * a.H + h] = 0.0f;
             }
@@ -102,14 +111,19 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
     const IN *kc = (const IN *)a.k + b * a.ks[0] + t0 * a.ks[1] + hk * a.ks[2];
     const IN *qc = (const IN *)a.q + b * a.qs[0] + t0 * a.qs[1] + hk * a.qs[2];
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    f32x4 dqa[NT][GROUP ? ST : 1], dka[NT][GROUP ? ST : 1];   // sums over the heads
-    if constexpr (GROUP) {
+    f32x4 dqa[NT][GROUP && !ACC ? ST : 1], dka[NT][GROUP && !ACC ? ST : 1];   // sums over the heads
+    if constexpr (GROUP && !ACC) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int s = 0; s < ST; ++s) dqa[t][s] = dka[t][s] = zero;
     }
     for (int gi = 0; gi < G; ++gi) {
+        // the lane's addresses are made anew for every head: kept over the loop they
+        // would take more registers than there are
+        int lane = tid0 & 63;
+        if constexpr (GROUP) asm volatile("" : "+v"(lane));
+        const int tid = wv * 64 + lane, m = lane & 15, g = lane >> 4;
         const int h = hk * G + gi;
         const int64_t cu = ((int64_t)b * a.H + h) * w.chunks + chunk;
         const int64_t tok = ((int64_t)b * a.T + t0) * a.H + h;   // of the chunk's first token
@@ -122,29 +136,35 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
         b16x8 fd[NDP][NIN];
         const float *Sp = w.S + cu * w.dvp * a.dk, *dSp = w.dS + cu * w.dvp * a.dk;
         const float *Up = w.U + cu * w.dvp * C, *Hp = w.Hm + cu * w.dvp * C;
-        auto fetch = [&](int v0) {
+        // In parts that the products are interleaved with: 0 S, 1 dS, 2 U and H,
+        // 3 dO.
+        auto fetch = [&](int part, int v0) {
             const int last = w.dvp - v0 - 1;         // rows behind it are blanked in place()
+            if (part < 2) {
 #pragma unroll
-            for (int i = 0; i < NSP; ++i) {
-                const int x = tid + i * TH, r = min(x / (DKP / 8), last), c = (x % (DKP / 8)) * 8;
-                const uint32_t at = (uint32_t)((v0 + r) * a.dk + (c < a.dk ? c : 0));
+                for (int i = 0; i < NSP; ++i) {
+                    const int x = tid + i * TH, r = min(x / (DKP / 8), last), c = (x % (DKP / 8)) * 8;
+                    const uint32_t at = (uint32_t)((v0 + r) * a.dk + (c < a.dk ? c : 0));
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    fs[i][j] = *(const f32x4 *)(Sp + at + 4 * j);
-                    fe[i][j] = *(const f32x4 *)(dSp + at + 4 * j);
+                    for (int j = 0; j < 2; ++j) {
+                        if (part == 0) fs[i][j] = *(const f32x4 *)(Sp + at + 4 * j);
+                        else fe[i][j] = *(const f32x4 *)(dSp + at + 4 * j);
+                    }
                 }
-            }
+            } else if (part == 2) {
 #pragma unroll
-            for (int i = 0; i < NUP; ++i) {
-                const int x = tid + i * TH, y = x % (VB * (C / 8)), r = min(y / (C / 8), last), c = (y % (C / 8)) * 8;
-                const float *p = (x < VB * (C / 8) ? Up : Hp) + (uint32_t)((v0 + r) * C + c);
+                for (int i = 0; i < NUP; ++i) {
+                    const int x = tid + i * TH, y = x % (VB * (C / 8)), r = min(y / (C / 8), last), c = (y % (C / 8)) * 8;
+                    const float *p = (x < VB * (C / 8) ? Up : Hp) + (uint32_t)((v0 + r) * C + c);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) fu[i][j] = *(const f32x4 *)(p + 4 * j);
-            }
+                    for (int j = 0; j < 2; ++j) fu[i][j] = *(const f32x4 *)(p + 4 * j);
+                }
+            } else {
 #pragma unroll
-            for (int i = 0; i < NDP; ++i) {
-                const int x = tid + i * TH, r = x / (VB / 8), c = (x % (VB / 8)) * 8;
-                get_planes(dc + (int64_t)r * os + v0 + c, x < C * (VB / 8) && r < n ? a.dv - v0 - c : 0, a.vec_v, fd[i]);
+                for (int i = 0; i < NDP; ++i) {
+                    const int x = tid + i * TH, r = x / (VB / 8), c = (x % (VB / 8)) * 8;
+                    get_planes(dc + (int64_t)r * os + v0 + c, x < C * (VB / 8) && r < n ? a.dv - v0 - c : 0, a.vec_v, fd[i]);
+                }
             }
         };
         float ss = 0.0f, hv = 0.0f;                  // <S, dS>; h_i . v_i of token 16 mt + m
@@ -190,7 +210,8 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
                 if (x < C * (VB / 8)) sm.b.d.put8(x / (VB / 8), (x % (VB / 8)) * 8, fd[i]);
             }
         };
-        fetch(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fetch(i, 0);
         __syncthreads();                             // the last head's arrays have been read
         for (int i = tid; i < 6 * C; i += TH) (&sm.g.al[0])[i] = w.G[cu * (6 * C) + i];
         // turned over: the lane's token is the column, its rows four neighbours
@@ -205,7 +226,7 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
             if (v0) __syncthreads();                 // the last block has been read
             place(v0);
             __syncthreads();
-            if (v0 + VB < a.dv) fetch(v0 + VB);
+            const bool more = v0 + VB < a.dv;
             const int row = 16 * mt + m, c = v0 + 8 * g;          // the lane's token and its 8 columns
             // S^T dO, S^T h and dS^T u, the wavefront's strips
             b16x8 sf[ST][3], ef[ST][3];
@@ -216,6 +237,10 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                if (more) {
+                    fetch(t * 4 / NT, v0 + VB);
+                    if (NT == 2) fetch(t * 4 / NT + 1, v0 + VB);
+                }
                 b16x8 x1[NIN], xh[3], xu[3];
                 sm.b.d.rows(16 * t + m, 8 * g, x1);
                 if constexpr (DELTA) sm.b.h.template cols<4>(0, 16 * t, lane, xh);
@@ -484,8 +509,18 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int s = 0; s < ST; ++s) {
-                    dqa[t][s] += sdo[t][s];
-                    dka[t][s] += dsu[t][s];
+                    if constexpr (ACC) {
+                        f32x4 *at = &sm.acc[((wv * NT + t) * ST + s) * 128 + lane];
+                        if (gi) {
+                            sdo[t][s] += at[0];
+                            dsu[t][s] += at[64];
+                        }
+                        at[0] = sdo[t][s];
+                        at[64] = dsu[t][s];
+                    } else {
+                        sdo[t][s] = dqa[t][s] += sdo[t][s];
+                        dsu[t][s] = dka[t][s] += dsu[t][s];
+                    }
                 }
         }
         if (!GROUP || gi + 1 == G) {
@@ -496,8 +531,8 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
                     const int row = 16 * t + m, key = 16 * (wv + NW * s) + 4 * g;
                     if (row < nT && key < a.dk) {
                         const int64_t at = (int64_t)row * a.Hk * a.dk + key;
-                        put4(dqp + at, GROUP ? dqa[t][GROUP ? s : 0] : sdo[t][s], a.vec_g);
-                        put4(dkp + at, GROUP ? dka[t][GROUP ? s : 0] : dsu[t][s], a.vec_g);
+                        put4(dqp + at, sdo[t][s], a.vec_g);
+                        put4(dkp + at, dsu[t][s], a.vec_g);
                     }
                 }
         }
