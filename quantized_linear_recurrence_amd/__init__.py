@@ -26,7 +26,7 @@ __all__ = ["LORES_FP32", "LORES_BF16", "LORES_INT8", "LORES_INT4", "LORES_INT6",
            "lores_state_layout",
            "lores_state_head_map", "lores_decay_stat", "lores_assign_precision",
            "lores_decode_step", "lores_step_launches", "lores_quant_state", "lores_dequant_state",
-           "lores_scan", "lores_scan_backward", "lores_rmsnorm", "lores_rmsnorm_backward",
+           "lores_scan", "lores_scan_workspace", "lores_scan_backward", "lores_rmsnorm", "lores_rmsnorm_backward",
            "LORES_MAX_NORM",
            "lores_last_error", "lores_spec_version"]
 
@@ -257,34 +257,69 @@ def lores_dequant_state(state, out=None, stream=None):
 
 
 # ---------------------------------------------------------------- sequences
+#
+# The smallest of these calls take a few microseconds on the GPU, so the
+# checks below hand plain integers to the library and look nothing up twice.
 
-def _on(stream, device):
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NOTHING = _Nothing()
+
+
+def _on(stream):
     """Allocations inside belong to `stream`, where the kernels that use them run."""
-    import contextlib
-
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NOTHING if stream is None else torch.cuda.stream(stream)
 
 
-def _opt_ptr(t, name, dtype, numel, device):
-    return None if t is None else _dev_ptr(t, name, dtype, numel, device)
+def _raw_stream(stream, device):
+    import torch
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _whole(t, name, dtype, numel, device):
+    """The address of a contiguous tensor of `numel` elements (None: NULL)."""
+    import torch
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the inputs are on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _need(t, name, dtype, numel, device):
+    if t is None:
+        raise TypeError(f"{name} must be a torch tensor")
+    return _whole(t, name, dtype, numel, device)
 
 
 def _rows4(t, name, dtype, shape, device):
     """A [B, T, heads, width] tensor with a contiguous last dimension: its
-    pointer and its other strides."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
+    address and its other strides."""
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, q is on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.stride(3) != 1 and shape[3] != 1:
+    st = t.stride()
+    if st[3] != 1 and shape[3] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), t.stride()[:3]
+    return t.data_ptr(), st[:3]
 
 
 def _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths):
@@ -306,11 +341,23 @@ def _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths):
     kp, d.k_stride[:] = _rows4(k, "k", dt, (B, T, Hk, dk), dev)
     vp, d.v_stride[:] = _rows4(v, "v", dt, (B, T, H, dv), dev)
     f32 = torch.float32
-    args = (qp, kp, vp, _dev_ptr(alpha, "alpha", f32, B * T * H, dev),
-            _dev_ptr(beta, "beta", f32, B * T * H, dev),
-            _opt_ptr(lengths, "lengths", torch.int32, B, dev),
-            _opt_ptr(S0, "S0", f32, B * H * dv * dk, dev))
+    args = (qp, kp, vp, _need(alpha, "alpha", f32, B * T * H, dev),
+            _need(beta, "beta", f32, B * T * H, dev),
+            _whole(lengths, "lengths", torch.int32, B, dev),
+            _whole(S0, "S0", f32, B * H * dv * dk, dev))
     return d, args, dev, dt
+
+
+def lores_scan_workspace(q, v, delta, backward=False):
+    """Bytes of device workspace a lores_scan (or lores_scan_backward) of these
+    shapes needs."""
+    import torch
+    B, T, Hk, dk = q.shape
+    d = _lib.LoresScanDims(B, T, v.shape[2], Hk, dk, v.shape[3], int(q.dtype == torch.bfloat16),
+                           int(delta))
+    n = ctypes.c_size_t(0)
+    _check(_lib.lib().lores_scan_workspace(ctypes.byref(d), int(backward), ctypes.byref(n)))
+    return n.value
 
 
 def _scan_work(d, backward, workspace, dev):
@@ -318,11 +365,12 @@ def _scan_work(d, backward, workspace, dev):
     n = ctypes.c_size_t(0)
     _check(_lib.lib().lores_scan_workspace(ctypes.byref(d), backward, ctypes.byref(n)))
     if workspace is None:
+        if not n.value:
+            return None, None, 0
         workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    return workspace, ctypes.c_void_p(workspace.data_ptr() if n.value else None), \
-        workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def lores_scan(q, k, v, alpha, beta, delta, S0=None, lengths=None, o=None, S=None, workspace=None,
@@ -334,21 +382,21 @@ def lores_scan(q, k, v, alpha, beta, delta, S0=None, lengths=None, o=None, S=Non
     a contiguous last dimension; H_k divides H), alpha, beta [B, T, H] fp32,
     S0 [B, H, d_v, d_k] fp32 or None (zero), lengths [B] int32 on the device
     or None.  Returns (o [B, T, H, d_v] of q's type, S [B, H, d_v, d_k] fp32);
-    S is what lores_quant_state takes.  workspace: a device tensor of at least
-    the bytes that lores_scan_workspace says, or None to allocate it.
+    S is what lores_quant_state takes, and may be S0.  workspace: a device
+    tensor of at least lores_scan_workspace bytes, or None to allocate it.
     """
     import torch
     d, args, dev, dt = _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths)
-    with _on(stream, dev):
+    with _on(stream):
         if o is None:
             o = torch.empty((d.B, d.T, d.H, d.d_v), dtype=dt, device=dev)
         if S is None:
             S = torch.empty((d.B, d.H, d.d_v, d.d_k), dtype=torch.float32, device=dev)
         work, wp, wn = _scan_work(d, 0, workspace, dev)
     _check(_lib.lib().lores_scan(
-        ctypes.byref(d), *args, _dev_ptr(o, "o", dt, d.B * d.T * d.H * d.d_v, dev),
-        _dev_ptr(S, "S", torch.float32, d.B * d.H * d.d_v * d.d_k, dev), wp, wn,
-        _stream_ptr(stream, dev)))
+        ctypes.byref(d), *args, _need(o, "o", dt, d.B * d.T * d.H * d.d_v, dev),
+        _need(S, "S", torch.float32, d.B * d.H * d.d_v * d.d_k, dev), wp, wn,
+        _raw_stream(stream, dev)))
     return o, S
 
 
@@ -363,9 +411,9 @@ def lores_scan_backward(q, k, v, alpha, beta, delta, do, dS=None, S0=None, lengt
     import torch
     d, args, dev, dt = _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths)
     n, f32 = d.B * d.H * d.d_v * d.d_k, torch.float32
-    dop = _dev_ptr(do, "do", dt, d.B * d.T * d.H * d.d_v, dev)
-    dSp = _opt_ptr(dS, "dS", f32, n, dev)
-    with _on(stream, dev):
+    dop = _need(do, "do", dt, d.B * d.T * d.H * d.d_v, dev)
+    dSp = _whole(dS, "dS", f32, n, dev)
+    with _on(stream):
         dq = torch.empty((d.B, d.T, d.H_k, d.d_k), dtype=dt, device=dev)
         dk = torch.empty_like(dq)
         dv = torch.empty((d.B, d.T, d.H, d.d_v), dtype=dt, device=dev)
@@ -375,13 +423,13 @@ def lores_scan_backward(q, k, v, alpha, beta, delta, do, dS=None, S0=None, lengt
         work, wp, wn = _scan_work(d, 1, workspace, dev)
     out = (dq, dk, dv, da, db, dS0)
     _check(_lib.lib().lores_scan_backward(
-        ctypes.byref(d), *args, dop, dSp, *(ctypes.c_void_p(t.data_ptr()) for t in out), wp, wn,
-        _stream_ptr(stream, dev)))
+        ctypes.byref(d), *args, dop, dSp, *(t.data_ptr() for t in out), wp, wn,
+        _raw_stream(stream, dev)))
     return out
 
 
 def _norm_rows(t, name, dtype, shape, device):
-    """A tensor of rows [..., n]: its pointer and the elements between rows."""
+    """A tensor of rows [..., n]: its address and the elements between rows."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -389,14 +437,14 @@ def _norm_rows(t, name, dtype, shape, device):
         raise ValueError(f"{name} is on {t.device}, the rows are on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     n = shape[-1]
     if t.is_contiguous():
-        return ctypes.c_void_p(t.data_ptr()), n
-    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < n:
+        return t.data_ptr(), n
+    if t.dim() != 2 or (t.stride(1) != 1 and n != 1) or t.stride(0) < n:
         raise ValueError(f"{name} must be contiguous, or [rows, n] with contiguous rows")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0)
+    return t.data_ptr(), t.stride(0)
 
 
 def _norm_shape(x, weight):
@@ -405,15 +453,15 @@ def _norm_shape(x, weight):
         raise TypeError("the rows and weight must be torch tensors")
     if x.device.type != "cuda":
         raise ValueError(f"the rows must be on the GPU, got {x.device}")
+    bf, f32 = torch.bfloat16, torch.float32
     for t, name in ((x, "the rows"), (weight, "weight")):
-        if t.dtype not in (torch.bfloat16, torch.float32):
+        if t.dtype is not bf and t.dtype is not f32:
             raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"rows must be [..., n] with n >= 1, got {list(x.shape)}")
     n = x.shape[-1]
-    wp = _dev_ptr(weight, "weight", weight.dtype, n, x.device)
-    bf = torch.bfloat16
-    return x.numel() // n, n, wp, int(weight.dtype == bf), int(x.dtype == bf)
+    wp = _need(weight, "weight", weight.dtype, n, x.device)
+    return x.numel() // n, n, wp, int(weight.dtype is bf), int(x.dtype is bf)
 
 
 def lores_rmsnorm(x, weight, eps, residual=None, out_prec=None, stream=None):
@@ -426,27 +474,26 @@ def lores_rmsnorm(x, weight, eps, residual=None, out_prec=None, stream=None):
     """
     import torch
     rows, n, wp, w_bf16, in_bf16 = _norm_shape(x, weight)
-    dev = x.device
-    xp, xs = _norm_rows(x, "x", x.dtype, x.shape, dev)
-    rp, rs = (None, 0) if residual is None else _norm_rows(residual, "residual", x.dtype, x.shape,
-                                                           dev)
+    dev, dt = x.device, x.dtype
+    xp, xs = _norm_rows(x, "x", dt, x.shape, dev)
+    rp, rs = (None, 0) if residual is None else _norm_rows(residual, "residual", dt, x.shape, dev)
     if out_prec is None:
         out_prec = LORES_BF16 if in_bf16 else LORES_FP32
     types = {LORES_FP32: torch.float32, LORES_BF16: torch.bfloat16, LORES_INT8: torch.int8,
              LORES_FP8: torch.float8_e4m3fn}
     if out_prec not in types:
         raise ValueError("out_prec must be LORES_FP32, LORES_BF16, LORES_INT8 or LORES_FP8")
-    with _on(stream, dev):
+    h, hp, scales, sp = x, None, None, None
+    with _on(stream):
         y = torch.empty(x.shape, dtype=types[out_prec], device=dev)
-        scales = None
-        if out_prec in (LORES_INT8, LORES_FP8):
+        if out_prec == LORES_INT8 or out_prec == LORES_FP8:
             scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        h = x if residual is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _check(_lib.lib().lores_rmsnorm(
-        xp, xs, rp, rs, wp, w_bf16, rows, n, in_bf16, float(eps), int(out_prec),
-        ctypes.c_void_p(y.data_ptr()),
-        None if scales is None else ctypes.c_void_p(scales.data_ptr()),
-        None if residual is None else ctypes.c_void_p(h.data_ptr()), _stream_ptr(stream, dev)))
+            sp = scales.data_ptr()
+        if residual is not None:
+            h = torch.empty(x.shape, dtype=dt, device=dev)
+            hp = h.data_ptr()
+    _check(_lib.lib().lores_rmsnorm(xp, xs, rp, rs, wp, w_bf16, rows, n, in_bf16, eps, out_prec,
+                                    y.data_ptr(), sp, hp, _raw_stream(stream, dev)))
     return y, scales, h
 
 
@@ -456,18 +503,17 @@ def lores_rmsnorm_backward(h, weight, dy, eps, dresidual=None, stream=None):
     reaches h otherwise added; dw [n] fp32."""
     import torch
     rows, n, wp, w_bf16, in_bf16 = _norm_shape(h, weight)
-    dev = h.device
-    hp, hs = _norm_rows(h, "h", h.dtype, h.shape, dev)
-    dyp = _dev_ptr(dy, "dy", h.dtype, rows * n, dev)
-    drp = _opt_ptr(dresidual, "dresidual", h.dtype, rows * n, dev)
+    dev, dt = h.device, h.dtype
+    hp, hs = _norm_rows(h, "h", dt, h.shape, dev)
+    dyp = _need(dy, "dy", dt, rows * n, dev)
+    drp = _whole(dresidual, "dresidual", dt, rows * n, dev)
     size = ctypes.c_size_t(0)
     _check(_lib.lib().lores_rmsnorm_workspace(rows, n, ctypes.byref(size)))
-    with _on(stream, dev):
-        dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+    with _on(stream):
+        dx = torch.empty(h.shape, dtype=dt, device=dev)
         dw = torch.empty(n, dtype=torch.float32, device=dev)
         work = torch.empty(size.value, dtype=torch.uint8, device=dev)
-    _check(_lib.lib().lores_rmsnorm_backward(
-        hp, hs, wp, w_bf16, dyp, drp, rows, n, in_bf16, float(eps),
-        ctypes.c_void_p(dx.data_ptr()), ctypes.c_void_p(dw.data_ptr()),
-        ctypes.c_void_p(work.data_ptr()), size.value, _stream_ptr(stream, dev)))
+    _check(_lib.lib().lores_rmsnorm_backward(hp, hs, wp, w_bf16, dyp, drp, rows, n, in_bf16, eps,
+                                             dx.data_ptr(), dw.data_ptr(), work.data_ptr(),
+                                             size.value, _raw_stream(stream, dev)))
     return dx, dw

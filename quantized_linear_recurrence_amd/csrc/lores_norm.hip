@@ -330,7 +330,7 @@ hipError_t by_width(bool vec, bool back, const NormArgs &a, hipStream_t s) {
 }  // namespace
 
 int norm_groups(int64_t rows, int32_t n) {
-    const int64_t most = n <= 128 ? 16384 : n <= 1024 ? 4096 : n <= 4096 ? 1024 : 512;
+    const int64_t most = n <= 128 ? 16384 : n <= 1024 ? 4096 : n <= 4096 ? 2048 : 512;
     return (int)(rows < most ? rows : most);
 }
 
