@@ -62,14 +62,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, b16x2));
 }
 
-// Four neighbours of a row to memory (vec: a whole piece of 4 elements).
-__device__ __forceinline__ void put4(float *p, f32x4 v, bool vec) {
-    if (vec) {
-        store4(p, v);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = v[e];
-    }
+// Four neighbours of a row to memory (vec: the address is a multiple of their
+// size; four words need no more than their own alignment).
+__device__ __forceinline__ void put4(float *p, f32x4 v, bool) {
+    // the instruction itself: the compiler would store these results from
+    // accumulation registers.  The wait state keeps the data registers from
+    // being rewritten before the store has read them.
+    asm volatile("global_store_dwordx4 %0, %1, off\n\ts_nop 0" :: "v"(p), "v"(v) : "memory");
 }
 __device__ __forceinline__ void put4(uint16_t *p, f32x4 v, bool vec) {
     const u32x2 w = {pack2(v[0], v[1]), pack2(v[2], v[3])};
