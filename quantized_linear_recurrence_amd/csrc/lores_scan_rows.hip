@@ -1,4 +1,4 @@
-// The recurrence over a few tokens (lores_scan at T <= kScanRowsTokens), token
+// The recurrence over a few tokens (lores_scan at few tokens, scan_rows_tokens), token
 // by token in fp32:
 //   S' = alpha S,  g = beta (v - delta S' k),  S = S' + g k^T,
 //   o = S q = S' q + g (k . q)
@@ -6,7 +6,10 @@
 // neighbouring elements of every 32) for the whole call; the three dot
 // products of a token are reduced over 8 lanes together.  With one token the
 // call is bound by reading and writing the fp32 state once: 16-byte accesses,
-// 128 bytes of a row per instruction and 8 lanes.
+// 128 bytes of a row per instruction and 8 lanes.  64 x 32 units of 128 x 128
+// take 48 us (5.6 TB/s); a further token costs about 14 us of issue and of
+// waiting for its q and k (fetching them a token ahead took so many registers
+// that it cost more: 98 instead of 63, 21 us a token).
 #include "lores_seq.h"
 
 namespace lores {
@@ -37,10 +40,16 @@ __device__ __forceinline__ f32x4 get4(const uint16_t *p, bool vec) {
     return f32x4{bf2f(p[0]), bf2f(p[1]), bf2f(p[2]), bf2f(p[3])};
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+// Sum over 8 neighbouring lanes, in all of them: pairs, quads, and the other
+// quad mirrored.
 __device__ __forceinline__ float sum8(float x) {
-    x += __shfl_xor(x, 1);
-    x += __shfl_xor(x, 2);
-    return x + __shfl_xor(x, 4);
+    x = dpp_add<0xb1>(x);                            // quad_perm 1 0 3 2
+    x = dpp_add<0x4e>(x);                            // quad_perm 2 3 0 1
+    return dpp_add<0x141>(x);                        // row_half_mirror
 }
 
 // NC = d_k / 32

@@ -61,8 +61,11 @@ struct ScanArgs {
     float *dS0;                        // [B][H][dv][dk], or NULL
 };
 
-// Sequences of at most this many tokens take the token-by-token kernel.
-constexpr int kScanRowsTokens = 8;
+// Sequences of at most this many tokens take the token-by-token kernel, whose
+// time grows with them, others the chunked ones.  At d_k = d_v = 128, 2, 4 and
+// 8 tokens: 512 (sequence, head) units 19, 24 and 35 us against 43 by chunks;
+// 2048 units 70, 97 and 153 us against 136.
+inline int scan_rows_tokens(int64_t units) { return units <= 1024 ? 8 : 6; }
 
 // Chunked scans: tokens of a chunk (the products' operands are held as bf16
 // planes, and an fp32 input has three).

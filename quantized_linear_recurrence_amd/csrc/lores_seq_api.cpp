@@ -108,7 +108,7 @@ int check_scan_inputs(const lores_scan_dims *d, const void *q, const void *k, co
 
 // The chunked kernels' workspace, or 0 for a call that does not take them.
 uint64_t scan_work(const lores_scan_dims *d, int32_t backward, void *base, lores::ScanWork *w) {
-    if (backward ? d->T == 0 : d->T <= lores::kScanRowsTokens) return 0;
+    if (backward ? d->T == 0 : d->T <= lores::scan_rows_tokens((int64_t)d->B * d->H)) return 0;
     return lores::plan_scan_work(d->in_bf16, backward, scan_args(d), base, w);
 }
 
