@@ -15,9 +15,9 @@
 // 64, 256 or 1024 threads so that a thread holds one or two vectors: a decode
 // batch of 64 rows of 4096 then spreads its loads over 64 x 256 threads, and
 // heads of 128 elements fill whole wavefronts (four rows in each).  Sums are
-// fp32.  dw is summed by row groups, each in its own registers in row order,
-// and the groups' sums are added by a second kernel in a fixed order: the
-// result does not depend on scheduling.
+// fp32.  dw is summed by work-groups, each over its rows in registers and over
+// the rows it takes side by side in LDS, and the work-groups' sums are added by
+// a second kernel in a fixed order: the result does not depend on scheduling.
 #include "lores_seq.h"
 
 namespace lores {
@@ -239,16 +239,15 @@ template <typename T, int TPR, int VPT, bool VEC>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_backward_kernel(const NormArgs a) {
     constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
     __shared__ float sm[TPR > 64 ? TPR / 64 : 1][2];
-    const int t = threadIdx.x % TPR;
-    const int group = blockIdx.x * ROWS + threadIdx.x / TPR;
-    if (group >= a.groups) return;
+    __shared__ __attribute__((aligned(16))) float sums[ROWS > 1 ? ROWS : 1][ROWS > 1 ? TPR * VPT * 8 : 1];
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     float w[VPT][8], dw[VPT][8];
     load_weight<T, TPR, VPT, VEC>(a, t, w);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
-    for (int64_t row = group; row < a.rows; row += a.groups) {
+    for (int64_t row = (int64_t)blockIdx.x * ROWS + sub; row < a.rows; row += (int64_t)a.groups * ROWS) {
         float h[VPT][8], g[VPT][8], d[VPT][8];
         load_row<T, TPR, VPT, VEC>((const T *)a.x + row * a.x_stride, t, a.n, h);
         load_row<T, TPR, VPT, VEC>((const T *)a.dy + row * a.n, t, a.n, g);
@@ -281,7 +280,19 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_backward_ker
             }
         store_row<T, TPR, VPT, VEC>((T *)a.dx + row * a.n, t, a.n, d);
     }
-    store_row<float, TPR, VPT, VEC>(a.part + (int64_t)group * a.n, t, a.n, dw);
+    float *part = a.part + (int64_t)blockIdx.x * a.n;
+    if constexpr (ROWS > 1) {                        // the rows side by side, in their order
+        store_row<float, TPR, VPT, VEC>(sums[sub], t, a.n, dw);
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.n; c += 256) {
+            float x = sums[0][c];
+#pragma unroll
+            for (int i = 1; i < ROWS; ++i) x += sums[i][c];
+            part[c] = x;
+        }
+    } else {
+        store_row<float, TPR, VPT, VEC>(part, t, a.n, dw);
+    }
 }
 
 // dw = the groups' sums added up: 16 columns per work-group, 64 slices of the
@@ -304,8 +315,7 @@ __global__ void __launch_bounds__(1024) lores_norm_dw_kernel(const NormArgs a) {
 template <typename T, int TPR, int VPT>
 hipError_t go(bool vec, bool back, const NormArgs &a, hipStream_t s) {
     constexpr int ROWS = TPR < 256 ? 256 / TPR : 1, TH = TPR < 256 ? 256 : TPR;
-    const int64_t units = back ? a.groups : a.rows;
-    const dim3 grid((unsigned)((units + ROWS - 1) / ROWS));
+    const dim3 grid((unsigned)(back ? a.groups : (a.rows + ROWS - 1) / ROWS));
     if (back) {
         if (vec) lores_norm_backward_kernel<T, TPR, VPT, true><<<grid, TH, 0, s>>>(a);
         else lores_norm_backward_kernel<T, TPR, VPT, false><<<grid, TH, 0, s>>>(a);
@@ -316,6 +326,12 @@ hipError_t go(bool vec, bool back, const NormArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Threads per row: one or two vectors each.  Measured (us forward / backward,
+// bf16): a quarter of the threads with four times the vectors is the same at
+// 128 and 8192 elements, 17.2 / 46 instead of 15.3 / 36 at 8192 x 1024 and
+// 125 / 217 instead of 92 / 116 at 16384 x 4096, and a small batch (64 x 4096)
+// waits 10 instead of 4.6 us; four times the threads with idle ones take 34 instead of 14 us at
+// 65536 x 128 and 150 instead of 92 at 16384 x 4096.
 template <typename T>
 hipError_t by_width(bool vec, bool back, const NormArgs &a, hipStream_t s) {
     if (a.n <= 128) return go<T, 16, 1>(vec, back, a, s);
@@ -329,9 +345,19 @@ hipError_t by_width(bool vec, bool back, const NormArgs &a, hipStream_t s) {
 
 }  // namespace
 
+// As many as run at once, or fewer where the groups' sums would then weigh: us
+// of both kernels, bf16, without dresidual:
+//   rows x n        256    512   1024   2048  work-groups
+//   65536 x 128       -   18.7   18.9   23.7
+//   8192 x 1024       -   19.0   19.8   28.2
+//   16384 x 2048      -   55.6   45.2   51.4
+//   16384 x 4096      -      -   90.6   98.6
+//   8192 x 8192     109    114      -      -
+//   4096 x 16384    102    110      -      -
 int norm_groups(int64_t rows, int32_t n) {
-    const int64_t most = n <= 128 ? 16384 : n <= 1024 ? 4096 : n <= 4096 ? 2048 : 512;
-    return (int)(rows < most ? rows : most);
+    const int side = n <= 128 ? 16 : n <= 1024 ? 4 : 1;      // rows a work-group takes side by side
+    const int64_t most = n <= 1024 ? 512 : n <= 4096 ? 1024 : 256, need = (rows + side - 1) / side;
+    return (int)(need < most ? need : most);
 }
 
 hipError_t launch_norm(bool in_bf16, bool vec, const NormArgs &a, hipStream_t s) {

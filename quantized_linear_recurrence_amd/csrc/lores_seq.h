@@ -29,10 +29,10 @@ struct NormArgs {
     const void *dy, *dres;
     void *dx;
     float *dw, *part;
-    int32_t groups;                    // row groups that sum dw apart
+    int32_t groups;                    // work-groups that sum dw apart
 };
 
-// Row groups of the backward pass: each keeps its own column sums of dw.
+// Work-groups of the backward pass: each keeps its own column sums of dw.
 int norm_groups(int64_t rows, int32_t n);
 hipError_t launch_norm(bool in_bf16, bool vec, const NormArgs &a, hipStream_t s);
 hipError_t launch_norm_backward(bool in_bf16, bool vec, const NormArgs &a, hipStream_t s);

@@ -64,4 +64,4 @@ def test_refusals_without_a_gpu(lores_lib):
     assert lores_lib.lores_scan(ctypes.byref(d), None, p, p, p, p, None, None, p, p, p, 1 << 30, None) == _lib.LORES_EINVAL
     assert lores_lib.lores_rmsnorm(p, 8, None, 0, p, 0, 4, 0, 0, 1e-6, 0, p, None, None, None) == _lib.LORES_EINVAL
     assert b"n must be" in lores_lib.lores_last_error()
-    assert lores_lib.lores_rmsnorm_workspace(4, 64, ctypes.byref(n)) == 0 and n.value == 4 * 64 * 4
+    assert lores_lib.lores_rmsnorm_workspace(4, 64, ctypes.byref(n)) == 0 and 0 < n.value <= 4 * 64 * 4
