@@ -288,35 +288,39 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_back_kernel(const ScanArgs
     }
 }
 
-template <typename IN, int DKP, bool FAST, bool VEC, int NW>
+template <typename IN, int DKP, bool DELTA, bool FAST, bool VEC, int NW>
 hipError_t go(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
     const int groups = (a.dv + 16 * NW - 1) / (16 * NW);
     const dim3 grid((unsigned)(((int64_t)a.B * a.H + 7) / 8 * 8 * groups));
-    if (a.delta) lores_scan_back_kernel<IN, DKP, true, FAST, VEC, NW><<<grid, 64 * NW, 0, s>>>(a, w, groups);
-    else lores_scan_back_kernel<IN, DKP, false, FAST, VEC, NW><<<grid, 64 * NW, 0, s>>>(a, w, groups);
+    lores_scan_back_kernel<IN, DKP, DELTA, FAST, VEC, NW><<<grid, 64 * NW, 0, s>>>(a, w, groups);
     return hipGetLastError();
 }
 
-template <typename IN, int DKP>
+template <typename IN, int DKP, bool DELTA>
 hipError_t by_rows(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    if (!a.vec) return go<IN, DKP, false, false, 4>(a, w, s);
-    if (!a.vec_v) return go<IN, DKP, true, false, 4>(a, w, s);
-    if (scan_waves(a) == 8) return go<IN, DKP, true, true, 8>(a, w, s);
-    return go<IN, DKP, true, true, 4>(a, w, s);
+    if (!a.vec) return go<IN, DKP, DELTA, false, false, 4>(a, w, s);
+    if (!a.vec_v) return go<IN, DKP, DELTA, true, false, 4>(a, w, s);
+    // With delta, fp32 operands of 128 keys leave too few registers for eight
+    // (256 units x 512 tokens, all kernels: 947 us by eight, 818 by four;
+    // without delta 567 and 619)
+    if constexpr (DKP <= (sizeof(IN) == 4 && DELTA ? 64 : 128))
+        if (scan_waves(a) == 8) return go<IN, DKP, DELTA, true, true, 8>(a, w, s);
+    return go<IN, DKP, DELTA, true, true, 4>(a, w, s);
 }
 
-template <typename IN>
+template <typename IN, bool DELTA>
 hipError_t by_width(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    if (a.dk <= 64) return by_rows<IN, 64>(a, w, s);
-    if (a.dk <= 128) return by_rows<IN, 128>(a, w, s);
-    return by_rows<IN, 256>(a, w, s);
+    if (a.dk <= 64) return by_rows<IN, 64, DELTA>(a, w, s);
+    if (a.dk <= 128) return by_rows<IN, 128, DELTA>(a, w, s);
+    return by_rows<IN, 256, DELTA>(a, w, s);
 }
 
 }  // namespace
 }  // namespace scan
 
 hipError_t launch_scan_back(bool in_bf16, const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    return in_bf16 ? scan::by_width<uint16_t>(a, w, s) : scan::by_width<float>(a, w, s);
+    if (a.delta) return in_bf16 ? scan::by_width<uint16_t, true>(a, w, s) : scan::by_width<float, true>(a, w, s);
+    return in_bf16 ? scan::by_width<uint16_t, false>(a, w, s) : scan::by_width<float, false>(a, w, s);
 }
 
 }  // namespace lores

@@ -557,8 +557,11 @@ struct RowFetch {
 // each).  Eight share a chunk's rows in LDS and fill a compute unit's SIMDs
 // twice, which pays where that still leaves a work-group for each of the 256
 // compute units; with fewer units the rows are spread over more of them.
-// Measured at d_k = d_v = 128: 256 units x 4096 tokens 1517 us by eight, 1705
-// by four; 32 units 478 and 424; 128 units (training step) 1978 and 1743.
+// Measured at bf16, d_k = d_v = 128, all kernels of the call: 256 units x 4096
+// tokens 697 us by eight, 818 by four; 32 units 376 and 317; a training step
+// of 128 units 1288 and 1105.  At d_k = 256 eight wavefronts have too few
+// registers for the state (256 units x 512 tokens, d_v = 256: 370 us by eight,
+// 317 by four; fp32 1372 and 776), so the callers ask only at d_k <= 128.
 inline int scan_waves(const ScanArgs &a) {
     return (int64_t)a.B * a.H * ((a.dv + 127) / 128) >= 256 ? 8 : 4;
 }

@@ -34,10 +34,11 @@ struct PrepLds {
     };
 };
 
-// NP: planes of P.  Three work-groups share a compute unit where their LDS
-// allows it (750 us at two, 695 at three for 8 x 4096 tokens with the pass behind).
+// NP: planes of P.  Two work-groups share a compute unit; asking for registers
+// for three is the same within 1 % (8 x 4096 tokens x 32 heads with the pass
+// behind: 692 and 693 us).
 template <typename IN, int DKP, int NP, bool DELTA>
-__global__ void __launch_bounds__(Cfg<IN>::C * 4, (sizeof(IN) == 2 && DKP <= 128 ? 3 : 1)) lores_scan_prep_kernel(const ScanArgs a, const ScanWork w) {
+__global__ void __launch_bounds__(Cfg<IN>::C * 4, (sizeof(IN) == 2 && DKP <= 128 ? 2 : 1)) lores_scan_prep_kernel(const ScanArgs a, const ScanWork w) {
     constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, NB = tri_blocks(C), NW = NT, TH = 64 * NW;
     __shared__ __attribute__((aligned(16))) PrepLds<IN, DKP, NP> sm;
     const int tid = threadIdx.x, lane = tid & 63, mt = __builtin_amdgcn_readfirstlane(tid >> 6);

@@ -373,7 +373,8 @@ template <typename IN, int DKP>
 hipError_t by_rows(bool backward, const ScanArgs &a, const ScanWork &w, hipStream_t s) {
     if (!a.vec) return go<IN, DKP, false, false, 4>(backward, a, w, s);
     if (!a.vec_v) return go<IN, DKP, true, false, 4>(backward, a, w, s);
-    if (scan_waves(a) == 8) return go<IN, DKP, true, true, 8>(backward, a, w, s);
+    if constexpr (DKP <= 128)
+        if (scan_waves(a) == 8) return go<IN, DKP, true, true, 8>(backward, a, w, s);
     return go<IN, DKP, true, true, 4>(backward, a, w, s);
 }
 
