@@ -8,6 +8,11 @@
 // 16 value rows and holds dS^T (d_k x 16), the left operands come from LDS (P^T,
 // X^T, Q^T and K^T by transposing reads), the right ones from its registers.
 // Every chunk's dS and H are stored for the inputs' gradients.
+//
+// Measured (bf16, d_k = d_v = 128, delta): 128 units x 2048 tokens 230 us, 0.77
+// GB at 3.4 TB/s, matrix instructions busy for 21 % of the time.  With 1024
+// wavefronts there is one per SIMD, and each waits on its own chain of products;
+// issuing products and splits in a fixed interleaving changed it by 1 %.
 #include "lores_scan_impl.h"
 
 namespace lores {

@@ -137,6 +137,18 @@ def test_backward(dtype, r, n):
         assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("r,n", [(8193, 100), (9001, 128), (2050, 130), (2101, 1024), (1100, 2048)])
+def test_backward_with_more_rows_than_work_groups_take_at_once(dtype, r, n):
+    h, w, dy = rows(r, n, dtype, r + n, 2.0), weight(n, dtype, 8), rows(r, n, dtype, r + n + 1)
+    dx, dw = lores.lores_rmsnorm_backward(h, w, dy, EPS)
+    rx, rw = oseq.rmsnorm_backward(_np(h), _np(w), EPS, _np(dy), None)
+    near(dx, rx, TOL[dtype], "dx")
+    near(dw, rw, 2.0 ** -17, "dw")
+    again = lores.lores_rmsnorm_backward(h, w, dy, EPS)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
 def test_gradient_matches_differences():
     h, w, dy = rows(5, 130, F32, 20), weight(130, F32, 21), rows(5, 130, F32, 22)
     dx, dw = lores.lores_rmsnorm_backward(h, w, dy, EPS)
