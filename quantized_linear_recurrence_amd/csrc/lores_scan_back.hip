@@ -186,16 +186,16 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_back_kernel(const ScanArgs
                 }
                 fence();
                 if (ks + 1 < KS) split(ks + 1, (ks + 1) & 1);
-                mma_all<3, MT>(kv[ks & 1], sp[ks & 1], y);
+                mma_all<MT>(kv[ks & 1], sp[ks & 1], y);
                 if (ks >= 1 && ks - 1 < SB) {
-                    if (ks == 1) mma_all<3, 2>(pv[0], dp[0], z);
-                    else if constexpr (SB > 1) mma_all<3, MT>(pv[SB - 1], dp[SB - 1], z);
+                    if (ks == 1) mma_all<2>(pv[0], dp[0], z);
+                    else if constexpr (SB > 1) mma_all<MT>(pv[SB - 1], dp[SB - 1], z);
                 }
             }
             fence();
             if (KS - 1 < SB) {
-                if (KS == 1) mma_all<3, 2>(pv[0], dp[0], z);
-                else if constexpr (SB > 1) mma_all<3, MT>(pv[SB - 1], dp[SB - 1], z);
+                if (KS == 1) mma_all<2>(pv[0], dp[0], z);
+                else if constexpr (SB > 1) mma_all<MT>(pv[SB - 1], dp[SB - 1], z);
             }
         }
 #pragma unroll
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_back_kernel(const ScanArgs
                 b16x8 yp[3];
                 pair8(y[2 * sb], y[2 * sb + 1], x);
                 split8(x, yp);
-                if (sb == 0) mma_all<3, 2>(xv[0], yp, hm);
-                else mma_all<3, MT>(xv[SB - 1], yp, hm);
+                if (sb == 0) mma_all<2>(xv[0], yp, hm);
+                else mma_all<MT>(xv[SB - 1], yp, hm);
             }
             fence();
         } else {
@@ -263,10 +263,10 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_back_kernel(const ScanArgs
             }
             b16x8 xp[3], vp[3];
             split8(x, xp);
-            mma_all<3, 2 * KS>(qt, xp, st);
+            mma_all<2 * KS>(qt, xp, st);
             if constexpr (DELTA) {
                 split8(v, vp);
-                mma_all<3, 2 * KS>(kt, vp, st);
+                mma_all<2 * KS>(kt, vp, st);
             }
             if (sb + 1 < SB) {
                 fence();

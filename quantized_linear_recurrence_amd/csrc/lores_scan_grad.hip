@@ -48,9 +48,9 @@ struct GradBlock {                                   // value columns v0 .. v0 +
 
 template <typename IN, int DKP>
 struct GradRows {                                    // when they have all gone by
-    static constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NO = sizeof(IN) == 2 ? 2 : 3;
+    static constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN;
     Planes<NIN, C, DKP> k, q;
-    Planes<NO, C, C> p, z;                           // dP.D and -beta Z.D
+    Tri<3, C> p, z;                                  // dP.D and -beta Z.D
     float a[C + 1][C + 1];                           // A, row C and column 0 its borders
 };
 
@@ -84,7 +84,6 @@ template <typename IN, int DKP, bool DELTA, bool GROUP>
 __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_kernel(const ScanArgs a, const ScanWork w) {
     constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, SB = C / 32, NW = grad_waves<IN, DKP>(), TH = 64 * NW;
     constexpr int ST = DKP / 16 / NW, RW = NW / NT;  // strips of a wavefront, wavefronts of a row
-    constexpr int NO = sizeof(IN) == 2 ? 2 : 3;      // planes of what ends in the inputs' type
     __shared__ __attribute__((aligned(16))) GradLds<IN, DKP, NW, GROUP> sm;
     constexpr bool ACC = GROUP && group_in_lds<IN, DKP, NW>();
     const int tid0 = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid0 >> 6);
@@ -253,9 +252,9 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
                 sm.b.u.template cols<4>(0, 16 * t, lane, xu);
 #pragma unroll
                 for (int s = 0; s < ST; ++s) {
-                    sdo[t][s] = mma<3>(sf[s], x1, sdo[t][s]);
-                    if constexpr (DELTA) sh[t][s] = mma<3>(sf[s], xh, sh[t][s]);
-                    dsu[t][s] = mma<3>(ef[s], xu, dsu[t][s]);
+                    sdo[t][s] = mma(sf[s], x1, sdo[t][s]);
+                    if constexpr (DELTA) sh[t][s] = mma(sf[s], xh, sh[t][s]);
+                    dsu[t][s] = mma(ef[s], xu, dsu[t][s]);
                 }
             }
             // dP and Z, the wavefront's tiles
@@ -269,8 +268,8 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
                     if (t <= mt && t % RW == half) {
                         b16x8 ub[3];
                         sm.b.u.template cols<4>(0, 16 * t, lane, ub);
-                        dp[t] = mma<3>(ub, da, dp[t]);
-                        if constexpr (DELTA) z[t] = mma<3>(ub, ha, z[t]);
+                        dp[t] = mma(ub, da, dp[t]);
+                        if constexpr (DELTA) z[t] = mma(ub, ha, z[t]);
                     }
             }
             // h of the row's tokens: dv and h . v
@@ -381,8 +380,8 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
                     if (t <= mt && t % RW == half) {
                         b16x8 kb[NIN];
                         sm.r.k.rows(16 * t + m, 32 * ks + 8 * g, kb);
-                        qk[t] = mma<3>(kb, qa, qk[t]);
-                        if constexpr (DELTA) kk[t] = mma<3>(kb, ka, kk[t]);
+                        qk[t] = mma(kb, qa, qk[t]);
+                        if constexpr (DELTA) kk[t] = mma(kb, ka, kk[t]);
                     }
             }
             const int i = 16 * mt + m;               // the lane's row; its columns j = 16 t + 4 g + r
@@ -406,8 +405,8 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
                     pv[r] = dp[t][r] * d[r];
                     if (i >= j) sm.r.a[i][j + 1] = fmaf(dp[t][r], qk[t][r], zr * kk[t][r]);
                 }
-                sm.r.p.put4(i, 16 * t + 4 * g, pv);
-                if constexpr (DELTA) sm.r.z.put4(i, 16 * t + 4 * g, zv);
+                sm.r.p.put4(mt >> 1, t >> 1, 16 * (mt & 1) + m, 16 * (t & 1) + 4 * g, pv);
+                if constexpr (DELTA) sm.r.z.put4(mt >> 1, t >> 1, 16 * (mt & 1) + m, 16 * (t & 1) + 4 * g, zv);
             }
             if constexpr (DELTA) {
                 mz += __shfl_xor(mz, 16);
@@ -489,23 +488,23 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                b16x8 x[NO], y[NO];
+                b16x8 x[3], y[3];
                 if (t >= 2 * sb) {                   // rows t read tokens of block sb
-                    sm.r.p.rows(16 * t + m, 32 * sb + 8 * g, x);
-                    if constexpr (DELTA) sm.r.z.rows(16 * t + m, 32 * sb + 8 * g, y);
+                    sm.r.p.rows(t >> 1, sb, 16 * (t & 1) + m, g, x);
+                    if constexpr (DELTA) sm.r.z.rows(t >> 1, sb, 16 * (t & 1) + m, g, y);
 #pragma unroll
                     for (int s = 0; s < ST; ++s) {
-                        sdo[t][s] = mma<NO>(kv[s], x, sdo[t][s]);
-                        if constexpr (DELTA) dsu[t][s] = mma<NO>(kv[s], y, dsu[t][s]);
+                        sdo[t][s] = mma(kv[s], x, sdo[t][s]);
+                        if constexpr (DELTA) dsu[t][s] = mma(kv[s], y, dsu[t][s]);
                     }
                 }
                 if (t < 2 * sb + 2) {                // tokens t are read by rows of block sb
-                    sm.r.p.template cols<4>(32 * sb, 16 * t, lane, x);
-                    if constexpr (DELTA) sm.r.z.template cols<4>(32 * sb, 16 * t, lane, y);
+                    sm.r.p.template cols<4>(sb, t >> 1, 16 * (t & 1), lane, x);
+                    if constexpr (DELTA) sm.r.z.template cols<4>(sb, t >> 1, 16 * (t & 1), lane, y);
 #pragma unroll
                     for (int s = 0; s < ST; ++s) {
-                        dsu[t][s] = mma<NO>(qv[s], x, dsu[t][s]);
-                        if constexpr (DELTA) dsu[t][s] = mma<NO>(kv[s], y, dsu[t][s]);
+                        dsu[t][s] = mma(qv[s], x, dsu[t][s]);
+                        if constexpr (DELTA) dsu[t][s] = mma(kv[s], y, dsu[t][s]);
                     }
                 }
             }

@@ -148,11 +148,11 @@ __device__ __forceinline__ f32x4 mfma(b16x8 a, b16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// c += a b over the planes' products i + j < ORD, the smallest first
-template <int ORD, int NA, int NB>
+// c += a b over the planes' products i + j < 3, the smallest first
+template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const b16x8 (&a)[NA], const b16x8 (&b)[NB], f32x4 c) {
 #pragma unroll
-    for (int o = ORD - 1; o >= 0; --o)
+    for (int o = 2; o >= 0; --o)
 #pragma unroll
         for (int i = 0; i <= o; ++i)
             if (i < NA && o - i < NB) c = mfma(a[i], b[o - i], c);
@@ -161,10 +161,10 @@ __device__ __forceinline__ f32x4 mma(const b16x8 (&a)[NA], const b16x8 (&b)[NB],
 
 // The same for MT results at once: products of planes outermost, so that
 // neighbouring instructions add to different results.
-template <int ORD, int MT, int NA, int NB>
+template <int MT, int NA, int NB>
 __device__ __forceinline__ void mma_all(const b16x8 (*a)[NA], const b16x8 (&b)[NB], f32x4 *c) {
 #pragma unroll
-    for (int o = ORD - 1; o >= 0; --o)
+    for (int o = 2; o >= 0; --o)
 #pragma unroll
         for (int i = 0; i <= o; ++i)
             if (i < NA && o - i < NB) {
@@ -402,6 +402,29 @@ struct Tri {
             const s16x8 w = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
             o[k] = __builtin_bit_cast(b16x8, w);
         }
+    }
+};
+
+// The same triangle in fp32, on its way from the prep kernel to the forward pass
+// over bf16 chunks: as many bytes as two planes, and the wavefronts make three of
+// it as they read.  (Three planes in LDS would not leave room for two chunks.)  A
+// row's 16-byte pieces lie in turned order, so that the 16 rows token_of(mt, m)
+// that an operand reads at one piece hit different banks.
+template <int C>
+struct TriWords {
+    static constexpr int NB = tri_blocks(C);
+    float x[NB][32 * 32];
+    static __device__ __forceinline__ int at_(int row, int piece) {
+        return row * 32 + ((piece ^ (((row >> 1) & 1) | (((row >> 3) & 3) << 1))) << 2);
+    }
+    // rows `row` of block (I, J), columns 8 g .. 8 g + 7
+    __device__ __forceinline__ void rows(int I, int J, int row, int g, f32x4 (&o)[2]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) o[i] = *(const f32x4 *)&x[tri_block(I, J)][at_(row, 2 * g + i)];
+    }
+    // four neighbours c .. c + 3 of a row (c a multiple of 4)
+    __device__ __forceinline__ void put4(int I, int J, int row, int c, const float (&v)[4]) {
+        *(f32x4 *)&x[tri_block(I, J)][at_(row, c >> 2)] = f32x4{v[0], v[1], v[2], v[3]};
     }
 };
 

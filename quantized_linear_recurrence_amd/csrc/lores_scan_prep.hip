@@ -22,7 +22,11 @@ namespace lores {
 namespace scan {
 namespace {
 
-template <typename IN, int DKP, int NP>
+// P as the passes behind read it: in fp32 or as planes
+template <int C, bool WORDS> struct PrepP : TriWords<C> {};
+template <int C> struct PrepP<C, false> : Tri<3, C> {};
+
+template <typename IN, int DKP, bool WORDS>
 struct PrepLds {
     static constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16;
     Gates<C> g;
@@ -32,18 +36,18 @@ struct PrepLds {
             float nt[NT * (NT - 1) / 2 + 1][16][20]; // N_KJ turned over (rows j), tile K (K - 1) / 2 + J
             float nd[NT][16][20];                    // N_II, then X_II
             Tri<3, C> x;
-            Tri<NP, C> p;
+            PrepP<C, WORDS> p;
         } t;
     };
 };
 
-// NP: planes of P.  Two work-groups share a compute unit; asking for registers
+// WORDS: P in fp32 instead of planes.  Two work-groups share a compute unit; asking for registers
 // for three is the same within 1 % (8 x 4096 tokens x 32 heads with the pass
 // behind: 692 and 693 us).
-template <typename IN, int DKP, int NP, bool DELTA>
+template <typename IN, int DKP, bool WORDS, bool DELTA>
 __global__ void __launch_bounds__(Cfg<IN>::C * 4, (sizeof(IN) == 2 && DKP <= 128 ? 2 : 1)) lores_scan_prep_kernel(const ScanArgs a, const ScanWork w) {
     constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, NB = tri_blocks(C), NW = NT, TH = 64 * NW;
-    __shared__ __attribute__((aligned(16))) PrepLds<IN, DKP, NP> sm;
+    __shared__ __attribute__((aligned(16))) PrepLds<IN, DKP, WORDS> sm;
     const int tid = threadIdx.x, lane = tid & 63, mt = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
     int b, hk, chunk;
@@ -86,8 +90,8 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4, (sizeof(IN) == 2 && DKP <= 128
 #pragma unroll
         for (int t = 0; t < NT; ++t)
             if (t <= mt) {
-                qk[t] = mma<3>(kv[t], qv, qk[t]);
-                if constexpr (DELTA) kk[t] = mma<3>(kv[t], ko, kk[t]);
+                qk[t] = mma(kv[t], qv, qk[t]);
+                if constexpr (DELTA) kk[t] = mma(kv[t], ko, kk[t]);
             }
     }
     for (int gi = 0; gi < G; ++gi) {
@@ -146,8 +150,8 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4, (sizeof(IN) == 2 && DKP <= 128
         __syncthreads();
         // what is done goes to memory while X is made
         for (int i = tid; i < 6 * C / 4; i += TH) ((f32x4 *)(w.G + unit * 6 * C))[i] = ((const f32x4 *)&sm.g.al[0])[i];
-        for (int i = tid; i < NP * NB * 128; i += TH)
-            ((u32x4 *)(w.P + unit * NP * NB * 1024))[i] = ((const u32x4 *)&sm.t.p.x[0])[i];
+        for (int i = tid; i < (int)sizeof(sm.t.p) / 16; i += TH)
+            ((u32x4 *)((uint8_t *)w.P + unit * sizeof(sm.t.p)))[i] = ((const u32x4 *)&sm.t.p.x[0])[i];
         if constexpr (!DELTA) continue;
         f32x4 xt[NT];                                // X_IJ of block row I = mt: rows j, column i
 #pragma unroll
@@ -185,19 +189,19 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4, (sizeof(IN) == 2 && DKP <= 128
     }
 }
 
-template <typename IN, int DKP, int NP>
+template <typename IN, int DKP, bool WORDS>
 hipError_t go(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
     const dim3 grid = chunk_grid(a, w);
-    if (a.delta) lores_scan_prep_kernel<IN, DKP, NP, true><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
-    else lores_scan_prep_kernel<IN, DKP, NP, false><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
+    if (a.delta) lores_scan_prep_kernel<IN, DKP, WORDS, true><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
+    else lores_scan_prep_kernel<IN, DKP, WORDS, false><<<grid, Cfg<IN>::C * 4, 0, s>>>(a, w);
     return hipGetLastError();
 }
 
-template <typename IN, int NP>
+template <typename IN, bool WORDS>
 hipError_t by_width(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    if (a.dk <= 64) return go<IN, 64, NP>(a, w, s);
-    if (a.dk <= 128) return go<IN, 128, NP>(a, w, s);
-    return go<IN, 256, NP>(a, w, s);
+    if (a.dk <= 64) return go<IN, 64, WORDS>(a, w, s);
+    if (a.dk <= 128) return go<IN, 128, WORDS>(a, w, s);
+    return go<IN, 256, WORDS>(a, w, s);
 }
 
 }  // namespace
@@ -206,7 +210,7 @@ hipError_t by_width(const ScanArgs &a, const ScanWork &w, hipStream_t s) {
 uint64_t plan_scan_work(bool in_bf16, bool backward, const ScanArgs &a, void *base, ScanWork *w) {
     const uint64_t C = scan_chunk(in_bf16);
     w->chunks = (int32_t)((a.T + C - 1) / C);
-    w->p_planes = backward || !in_bf16 ? 3 : 2;
+    w->p_words = !backward && in_bf16;
     w->dvp = (a.dv + 15) / 16 * 16;
     const uint64_t units = (uint64_t)a.B * a.H * w->chunks;
     uint64_t off = 0;
@@ -217,7 +221,7 @@ uint64_t plan_scan_work(bool in_bf16, bool backward, const ScanArgs &a, void *ba
     };
     const uint64_t tri = scan::tri_blocks((int)C) * 2048;       // bytes of a plane
     w->X = (uint16_t *)(a.delta ? cut(units * 3 * tri) : nullptr);
-    w->P = (uint16_t *)cut(units * w->p_planes * tri);
+    w->P = (uint16_t *)cut(units * (w->p_words ? 2 : 3) * tri);
     w->G = (float *)cut(units * 6 * C * 4);
     w->S = w->dS = w->U = w->Hm = nullptr;
     if (backward) {
@@ -230,8 +234,8 @@ uint64_t plan_scan_work(bool in_bf16, bool backward, const ScanArgs &a, void *ba
 }
 
 hipError_t launch_scan_prep(bool in_bf16, const ScanArgs &a, const ScanWork &w, hipStream_t s) {
-    if (!in_bf16) return scan::by_width<float, 3>(a, w, s);
-    return w.p_planes == 2 ? scan::by_width<uint16_t, 2>(a, w, s) : scan::by_width<uint16_t, 3>(a, w, s);
+    if (!in_bf16) return scan::by_width<float, false>(a, w, s);
+    return w.p_words ? scan::by_width<uint16_t, true>(a, w, s) : scan::by_width<uint16_t, false>(a, w, s);
 }
 
 }  // namespace lores

@@ -23,13 +23,18 @@ namespace lores {
 namespace scan {
 namespace {
 
+// P: planes of fp32 inputs, fp32 of bf16 ones
+template <typename IN, bool BACK> struct StateP : TriWords<Cfg<IN>::C> {};
+template <> struct StateP<float, false> : Tri<3, Cfg<float>::C> {};
+template <typename IN> struct alignas(16) StateP<IN, true> {};   // is not read
+
 template <typename IN, int DKP, bool BACK, int NW>
 struct StateLds {
-    static constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NP = sizeof(IN) == 2 ? 2 : 3;
+    static constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN;
     Planes<NIN, C, DKP> k;
     Planes<NIN, BACK ? 1 : C, DKP> q;
     Tri<3, C> x;
-    Tri<BACK ? 1 : NP, BACK ? 32 : C> p;
+    StateP<IN, BACK> p;
     Gates<C> g;
     Tile<IN, C> v[NW];
 };
@@ -45,8 +50,7 @@ template <typename L> __host__ __device__ constexpr int stages() { return 2 * si
 template <typename IN, int DKP, bool DELTA, bool BACK, bool FAST, bool VEC, int NW>
 __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArgs a, const ScanWork w, const int groups) {
     constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, MT = C / 16, SB = C / 32, KS = DKP / 32, TH = 64 * NW;
-    constexpr bool OUT16 = sizeof(IN) == 2;          // outputs end in bf16: two planes carry them
-    constexpr int NO = OUT16 ? 2 : 3;
+    constexpr bool IN16 = sizeof(IN) == 2;
     typedef StateLds<IN, DKP, BACK, NW> Lds;
     constexpr int NS = stages<Lds>();
     __shared__ __attribute__((aligned(16))) Lds lds[NS];
@@ -73,7 +77,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
     const int64_t os = (int64_t)a.H * a.dv;
     IN *ob = (IN *)a.o + ((int64_t)b * a.T * a.H + h) * a.dv + col0;
     const int chunks = (len + C - 1) / C;
-    RowFetch<C, OUT16 ? 8 : DKP, TH> kf, qf;         // fp32 only
+    RowFetch<C, IN16 ? 8 : DKP, TH> kf, qf;          // fp32 only
     IN vf[VEC ? 1 : MT][4];
     // A chunk's rows to stage `to`, in parts that the compute steps below are
     // interleaved with: part 0 k, 1 q, 2 what the tokens do to one another,
@@ -82,13 +86,13 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
         const int t0 = ch * C, n = min(len - t0, C);
         const int64_t cu = (int64_t)unit * w.chunks + ch;
         if (part == 0) {
-            if constexpr (FAST && OUT16) direct_rows<C, DKP, NW>(to.k.x[0], kb + t0 * a.ks[1], a.ks[1], n, a.dk, wv, lane);
+            if constexpr (FAST && IN16) direct_rows<C, DKP, NW>(to.k.x[0], kb + t0 * a.ks[1], a.ks[1], n, a.dk, wv, lane);
             else if constexpr (FAST) kf.load(kb + t0 * a.ks[1], a.ks[1], n, a.dk, tid);
         } else if (part == 1) {
-            if constexpr (!BACK && FAST && OUT16) direct_rows<C, DKP, NW>(to.q.x[0], qb + t0 * a.qs[1], a.qs[1], n, a.dk, wv, lane);
+            if constexpr (!BACK && FAST && IN16) direct_rows<C, DKP, NW>(to.q.x[0], qb + t0 * a.qs[1], a.qs[1], n, a.dk, wv, lane);
             else if constexpr (!BACK && FAST) qf.load(qb + t0 * a.qs[1], a.qs[1], n, a.dk, tid);
         } else if (part == 2) {
-            if constexpr (!BACK) direct_block<sizeof(to.p), NW>(w.P + cu * (NO * Tri<1, C>::NB * 1024), &to.p, wv, lane);
+            if constexpr (!BACK) direct_block<sizeof(to.p), NW>((const uint8_t *)w.P + cu * (int64_t)sizeof(to.p), &to.p, wv, lane);
             if constexpr (DELTA) direct_block<sizeof(to.x), NW>(w.X + cu * (3 * Tri<1, C>::NB * 1024), &to.x, wv, lane);
             direct_block<sizeof(to.g), NW>(w.G + cu * (6 * C), &to.g, wv, lane);
         } else if (mine) {
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
         if constexpr (!FAST) {
             stage_rows(to.k, kb + t0 * a.ks[1], a.ks[1], n, a.dk, false, tid, TH);
             if constexpr (!BACK) stage_rows(to.q, qb + t0 * a.qs[1], a.qs[1], n, a.dk, false, tid, TH);
-        } else if constexpr (!OUT16) {
+        } else if constexpr (!IN16) {
             kf.store(to.k, n, a.dk, tid);
             if constexpr (!BACK) qf.store(to.q, n, a.dk, tid);
         }
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
                 else gates();
                 fence();
                 if (ks + 1 < KS) split(ks + 1);
-                mma_all<3, MT>(rv[ks & 1], sp[ks], e);
+                mma_all<MT>(rv[ks & 1], sp[ks], e);
                 mix<(NIN == 1 ? 3 : 6) * MT, 4>();
             }
             fence();
@@ -238,8 +242,8 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
                     if (ks + 1 < KS) split(ks + 1);
                 }
                 if (ks < SB) finish_e(ks);
-                mma_all<OUT16 ? 2 : 3, MT>(rv[ks & 1], sp[ks], o);
-                mix<(NIN == 1 ? 2 : 6) * MT, 6>();
+                mma_all<MT>(rv[ks & 1], sp[ks], o);
+                mix<(NIN == 1 ? 3 : 6) * MT, 4>();
             }
             fence();
         } else {
@@ -250,7 +254,8 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
         }
         if (more) fetch(2, ch + 1, next);
         // the last products' left operands come while U is made
-        b16x8 kt[2 * KS][NIN], pv[BACK ? 1 : MT][NO], ut[SB][3], up[SB][NO];
+        b16x8 kt[2 * KS][NIN], pv[BACK ? 1 : MT][3], ut[SB][3], up[SB][3];
+        f32x4 pw[IN16 && !BACK ? MT : 1][2];         // P before it becomes planes
         f32x4 en[MT];
         auto turned = [&](int sb) {
 #pragma unroll
@@ -258,7 +263,20 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
                 sm.k.template cols<8>(32 * sb, 32 * (t >> 1) + 4 * (t & 1), lane, kt[t]);
             if constexpr (!BACK) {
 #pragma unroll
-                for (int mt = 2 * sb; mt < MT; ++mt) sm.p.rows(mt >> 1, sb, token_of(mt, m) & 31, g, pv[mt]);
+                for (int mt = 2 * sb; mt < MT; ++mt) {
+                    if constexpr (IN16) sm.p.rows(mt >> 1, sb, token_of(mt, m) & 31, g, pw[mt]);
+                    else sm.p.rows(mt >> 1, sb, token_of(mt, m) & 31, g, pv[mt]);
+                }
+            }
+        };
+        auto split_p = [&](int mt0) {
+            if constexpr (IN16 && !BACK) {
+#pragma unroll
+                for (int mt = mt0; mt < MT; ++mt) {
+                    float x[8];
+                    pair8(pw[mt][0], pw[mt][1], x);
+                    split8(x, pv[mt]);
+                }
             }
         };
         // U = X beta E, one block of 32 tokens after the other
@@ -271,7 +289,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
             fence();
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) e[mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            mma_all<3, MT>(xv, ep[0], e);
+            mma_all<MT>(xv, ep[0], e);
             if constexpr (!BACK) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) o[mt] *= gm[mt];
@@ -279,7 +297,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
             fence();
             turned(0);
             fence();
-            if constexpr (SB > 1) mma_all<3, MT - 2>(xn + 2, ep[SB - 1], e + 2);
+            if constexpr (SB > 1) mma_all<MT - 2>(xn + 2, ep[SB - 1], e + 2);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) u[mt] = e[mt];
         } else {
@@ -307,15 +325,18 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
         fence();
         if (more) fetch(3, ch + 1, next);
         if constexpr (SB > 1) split_u(SB - 1);
-        mma_all<3, 2 * KS>(kt, ut[0], st);
-        if constexpr (!BACK) mma_all<NO, MT>(pv, up[0], o);
-        mix<(NIN == 1 ? 3 : 6) * 2 * KS + (BACK ? 0 : (OUT16 ? 3 : 6) * MT), 3>();
+        split_p(0);
+        mma_all<2 * KS>(kt, ut[0], st);
+        if constexpr (!BACK) mma_all<MT>(pv, up[0], o);
+        mix<(NIN == 1 ? 3 : 6) * 2 * KS + (BACK ? 0 : 6 * MT), 3>();
         fence();
         if constexpr (SB > 1) {
             turned(1);
             fence();
-            if constexpr (!BACK) mma_all<NO, MT - 2>(pv + 2, up[SB - 1], o + 2);
-            mma_all<3, 2 * KS>(kt, ut[SB - 1], st);
+            split_p(2);
+            mma_all<2 * KS>(kt, ut[SB - 1], st);
+            if constexpr (!BACK) mma_all<MT - 2>(pv + 2, up[SB - 1], o + 2);
+            mix<3 * 2 * KS + (BACK ? 0 : 6 * (MT - 2)), 2>();
         }
         if constexpr (BACK) {
             float *u0 = w.U + cu * w.dvp * C;

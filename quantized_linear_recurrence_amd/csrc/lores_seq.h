@@ -76,11 +76,11 @@ __host__ __device__ constexpr int scan_chunk(bool in_bf16) { return in_bf16 ? 64
 // and its gradient at the chunk's two ends and U and H, value rows first.
 struct ScanWork {
     uint16_t *X;                       // [B][H][chunks][3][blocks][32][32]
-    uint16_t *P;                       // [B][H][chunks][p_planes][blocks][32][32]
+    uint16_t *P;                       // [B][H][chunks][3][blocks][32][32], or fp32 words (p_words)
     float *G;                          // [B][H][chunks][6][C]: Gates
     float *S, *dS;                     // [B][H][chunks][dvp][dk]
     float *U, *Hm;                     // [B][H][chunks][dvp][C]
-    int32_t chunks, p_planes, dvp;
+    int32_t chunks, p_words, dvp;
 };
 // Lays `w` out over `base` (which may be NULL) and returns the bytes.
 uint64_t plan_scan_work(bool in_bf16, bool backward, const ScanArgs &a, void *base, ScanWork *w);
