@@ -193,15 +193,20 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
         store_row<T, TPR, VPT, VEC>((T *)a.h + row * a.n, t, a.n, h);
     }
     load_weight<T, TPR, VPT, VEC>(a, t, w);
-    float sum = 0.0f, mx = 0.0f;
+    // magnitudes are compared as bits, where a NaN is above all numbers: the
+    // floating-point maximum would drop it.  It goes on as an infinity.
+    const float inf = __builtin_inff();
+    float sum = 0.0f;
+    uint32_t bits = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             sum = fmaf(h[i][e], h[i][e], sum);
             h[i][e] = h[i][e] * w[i][e];             // z
-            mx = fmaxf(mx, fabsf(h[i][e]));
+            bits = max(bits, __float_as_uint(fabsf(h[i][e])));
         }
+    float mx = __uint_as_float(min(bits, __float_as_uint(inf)));
     reduce<TPR, true>(sum, mx, sm);
     const float rstd = 1.0f / sqrtf(sum / (float)a.n + a.eps);
     if (a.out_prec == LORES_FP32 || a.out_prec == LORES_BF16) {
@@ -216,9 +221,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
         return;
     }
     const float top = a.out_prec == LORES_INT8 ? 127.0f : 448.0f;
+    // a row with a z that is not finite, or with squares beyond fp32, has the
+    // scale NaN and the codes 0
+    const bool lost = !(mx < inf) || !(sum < inf);
+    const float nan = __builtin_nanf("");
     // a maximum under 2^-119 (top / m would leave fp32's range) divides as
     // 2^-119: the codes of such a row round to zero
-    const float inv = top * (1.0f / fmaxf(mx, 0x1p-119f));
+    const float inv = lost ? nan : top * (1.0f / fmaxf(mx, 0x1p-119f));
     uint8_t c[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -226,7 +235,6 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
         for (int e = 0; e < 8; ++e) {
             const float x = h[i][e] * inv;
             if (a.out_prec == LORES_INT8) {
-                // a row with an infinity or NaN has the scale NaN; its NaN codes are 0
                 const float q = rintf(fminf(fmaxf(x, -127.0f), 127.0f));
                 c[i][e] = x == x ? (uint8_t)(int8_t)(int)q : (uint8_t)0;
             } else {
@@ -236,7 +244,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
             }
         }
     store_bytes<TPR, VPT, VEC>((uint8_t *)a.y + row * a.n, t, a.n, c);
-    if (t == 0) a.scales[row] = mx / top * rstd;
+    if (t == 0) a.scales[row] = lost ? nan : mx / top * rstd;
 }
 
 template <typename T, int TPR, int VPT, bool VEC>
