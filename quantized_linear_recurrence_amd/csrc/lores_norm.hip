@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
             }
         }
     store_bytes<TPR, VPT, VEC>((uint8_t *)a.y + row * a.n, t, a.n, c);
-    if (t == 0) a.scales[row] = lost ? nan : mx / top * rstd;
+    // (without an epsilon the r of a row of zeros is an infinity)
+    if (t == 0) a.scales[row] = lost ? nan : mx == 0.0f ? 0.0f : mx / top * rstd;
 }
 
 template <typename T, int TPR, int VPT, bool VEC>

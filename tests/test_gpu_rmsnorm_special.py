@@ -79,3 +79,16 @@ def test_a_row_whose_squares_leave_fp32_shows(n, prec):
     x[1] = 2.0 ** 66
     y, s, _ = lores.lores_rmsnorm(x, ones(n, BF16), 1e-6, out_prec=prec)
     assert is_lost(y[1:2], s[1:2]) and torch.isfinite(s[[0, 2]]).all()
+
+
+@pytest.mark.parametrize("prec", EIGHT)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", WIDTHS)
+def test_rows_of_zeros_without_an_epsilon(n, dtype, prec):
+    x = rows(3, n, dtype)
+    x[1] = 0.0
+    y, s, _ = lores.lores_rmsnorm(x, ones(n, dtype), 0.0, out_prec=prec)
+    assert float(s[1]) == 0.0 and (y[1].float() == 0).all()
+    check_values(x[[0, 2]], ones(n, dtype), 0.0, prec)
+    y, s, _ = lores.lores_rmsnorm(x, torch.zeros_like(ones(n, dtype)), 0.0, out_prec=prec)
+    assert (s == 0).all() and (y.float() == 0).all()
