@@ -447,13 +447,14 @@ int lores_scan_backward(const lores_scan_dims *dims, const void *q, const void *
  * and an output in 8 bits with one scale per row:
  *   h = rnd(x + residual) in the inputs' type (x itself without a residual),
  *   z_j = fl(h_j w_j),  r = (mean_j h_j^2 + eps)^(-1/2),  y_j = rnd(z_j r)
- *   out_prec LORES_INT8: m = max_j |z_j|, code_j = z_j fl(127 fl(1 / m)) rounded to
- *     nearest (ties to even), scale = fl(fl(m / 127) r): y_j ~ scale code_j
+ *   out_prec LORES_INT8: m = max_j |z_j| (at least 2^-119), code_j =
+ *     z_j fl(127 fl(1 / m)) rounded to nearest (ties to even),
+ *     scale = fl(fl(m / 127) r): y_j ~ scale code_j
  *   out_prec LORES_FP8: the same with 448 and E4M3 values
- * A row whose z are all zero has the scale 0, also at eps = 0 (where its y of the
- * other outputs are 0 times an infinite r: NaN).  A row where an h_j or z_j is not finite (a
- * weight can make it so) or where the sum of the squares leaves fp32's range
- * has the scale NaN and the codes 0.
+ * A row whose z are all zero has the scale 0, also at eps = 0 (where its y of
+ * the other outputs are 0 times an infinite r: NaN).  A row where an h_j or z_j
+ * is not finite (a weight can make it so), or where the sum of the squares
+ * leaves fp32's range, has the scale NaN and the codes 0.
  *   x          device [rows][n], in_bf16 ? bf16 : fp32, rows x_stride elements
  *              apart; 1 <= n <= LORES_MAX_NORM, 0 <= rows < 2^31
  *   residual   device [rows][n] of x's type, rows res_stride apart, or NULL

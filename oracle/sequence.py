@@ -104,8 +104,9 @@ def rmsnorm_backward(h, weight, eps, dy, dresidual=None):
 
 def rmsnorm_codes(h, weight, top):
     """The codes of an 8-bit output, before their own rounding: z fl(top fl(1 / m))
-    in fp32, with z = fl(h w) and m its largest magnitude (at least 2^-119), and m."""
+    in fp32, with z = fl(h w) and m its largest magnitude (at least 2^-119); and the
+    m of the scale, which is 0 for a row of zeros."""
     z = np.asarray(h, np.float32) * np.asarray(weight, np.float32)
-    m = np.abs(z).max(-1, keepdims=True)
-    inv = np.float32(top) * (np.float32(1.0) / np.maximum(m, np.float32(2.0 ** -119)))
-    return z * inv, m[..., 0]
+    most = np.abs(z).max(-1, keepdims=True)
+    m = np.maximum(most, np.float32(2.0 ** -119))
+    return z * (np.float32(top) * (np.float32(1.0) / m)), np.where(most > 0, m, most)[..., 0]

@@ -3,7 +3,7 @@
 //
 // Per row, with h = rnd(x + res) in the inputs' type, z_j = fl(h_j w_j):
 //   r = (mean_j h_j^2 + eps)^(-1/2),  y_j = rnd(z_j r)
-// 8-bit outputs: m = max_j |z_j|, code_j = rnd(z_j fl(top fl(1 / m))), scale =
+// 8-bit outputs: m = max_j |z_j| (at least 2^-119), code_j = rnd(z_j fl(top fl(1 / m))), scale =
 // fl(fl(m / top) r): the row's factor r cancels in the codes, so they depend
 // on elementwise roundings alone and not on the order of the row's sum.
 // Backward, with dy and the gradient dres that arrives at h by itself:
@@ -225,9 +225,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
     // scale NaN and the codes 0
     const bool lost = !(mx < inf) || !(sum < inf);
     const float nan = __builtin_nanf("");
-    // a maximum under 2^-119 (top / m would leave fp32's range) divides as
-    // 2^-119: the codes of such a row round to zero
-    const float inv = lost ? nan : top * (1.0f / fmaxf(mx, 0x1p-119f));
+    // a maximum under 2^-119 (top / m would leave fp32's range) counts as
+    // 2^-119, in the codes and in the scale: such a row uses fewer codes
+    const float m = fmaxf(mx, 0x1p-119f);
+    const float inv = lost ? nan : top * (1.0f / m);
     uint8_t c[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
         }
     store_bytes<TPR, VPT, VEC>((uint8_t *)a.y + row * a.n, t, a.n, c);
     // (without an epsilon the r of a row of zeros is an infinity)
-    if (t == 0) a.scales[row] = lost ? nan : mx == 0.0f ? 0.0f : mx / top * rstd;
+    if (t == 0) a.scales[row] = lost ? nan : mx == 0.0f ? 0.0f : m / top * rstd;
 }
 
 template <typename T, int TPR, int VPT, bool VEC>

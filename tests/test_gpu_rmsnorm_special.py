@@ -92,3 +92,13 @@ def test_rows_of_zeros_without_an_epsilon(n, dtype, prec):
     check_values(x[[0, 2]], ones(n, dtype), 0.0, prec)
     y, s, _ = lores.lores_rmsnorm(x, torch.zeros_like(ones(n, dtype)), 0.0, out_prec=prec)
     assert (s == 0).all() and (y.float() == 0).all()
+
+
+@pytest.mark.parametrize("prec", EIGHT)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", WIDTHS)
+def test_scale_times_code_is_the_value_for_tiny_rows(n, dtype, prec):
+    e = torch.tensor([-126.0, -125.0, -123.0, -120.0, -119.5, -119.0, -118.0, -100.0]).to("cuda:0")
+    x = rows(len(e), n, F32)
+    x = (x / x.abs().amax(1, keepdim=True) * torch.exp2(e)[:, None]).to(dtype)
+    check_values(x, ones(n, dtype), 1e-6, prec)
