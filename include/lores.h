@@ -373,7 +373,9 @@ int lores_quant_state(lores_state *st, const float *X, uint64_t seed, int64_t se
  * heads; the last dimension is contiguous.  Any stride >= 0 will do (0
  * broadcasts); 16-byte aligned q and k rows are read faster. */
 typedef struct {
-    int32_t B, T;              /* sequences (1 .. 65535), tokens (0 .. 2^28)            */
+    int32_t B, T;              /* sequences (1 .. 65535), tokens (0 .. 2^28); the heads'
+                                  chunks, H (B (T / 32 + 9) + 8), number at most
+                                  2^31 - 2^21 - 1                                      */
     int32_t H, H_k;            /* value heads (as lores_state_alloc), and query / key
                                   heads: H_k divides H, and value head h reads
                                   query / key head h / (H / H_k)                       */

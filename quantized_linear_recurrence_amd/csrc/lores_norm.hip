@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
     constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;  // rows of a work-group
     __shared__ float sm[TPR > 64 ? TPR / 64 : 1][2];
     const int t = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+    const int64_t row = block_at(blockIdx.x, blockIdx.y) * ROWS + threadIdx.x / TPR;
     if (row >= a.rows) return;                       // whole groups of TPR threads; no barrier for TPR <= 64
     float h[VPT][8], w[VPT][8];
     load_row<T, TPR, VPT, VEC>((const T *)a.x + row * a.x_stride, t, a.n, h);
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(1024) lores_norm_dw_kernel(const NormArgs a) {
 template <typename T, int TPR, int VPT>
 hipError_t go(bool vec, bool back, const NormArgs &a, hipStream_t s) {
     constexpr int ROWS = TPR < 256 ? 256 / TPR : 1, TH = TPR < 256 ? 256 : TPR;
-    const dim3 grid((unsigned)(back ? a.groups : (a.rows + ROWS - 1) / ROWS));
+    const dim3 grid = grid_of(back ? a.groups : (a.rows + ROWS - 1) / ROWS);
     if (back) {
         if (vec) lores_norm_backward_kernel<T, TPR, VPT, true><<<grid, TH, 0, s>>>(a);
         else lores_norm_backward_kernel<T, TPR, VPT, false><<<grid, TH, 0, s>>>(a);

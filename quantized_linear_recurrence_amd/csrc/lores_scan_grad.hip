@@ -89,7 +89,7 @@ __global__ void __launch_bounds__((64 * grad_waves<IN, DKP>())) lores_scan_grad_
     const int tid0 = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid0 >> 6);
     const int mt = wv / RW, half = wv % RW;          // the wavefront's row of tiles, its share of it
     int b, hk, chunk;
-    if (!chunk_of(blockIdx.x, a, w, &b, &hk, &chunk)) return;
+    if (!chunk_of((int)block_at(blockIdx.x, blockIdx.y), a, w, &b, &hk, &chunk)) return;
     const int G = GROUP ? a.H / a.Hk : 1;
     int len = a.T;
     if (a.lengths) len = min(max(a.lengths[b], 0), a.T);

@@ -612,7 +612,7 @@ __device__ __forceinline__ bool chunk_of(int block, const ScanArgs &a, const Sca
     return *b < a.B;
 }
 inline dim3 chunk_grid(const ScanArgs &a, const ScanWork &w) {
-    return dim3((unsigned)(((int64_t)a.B * w.chunks + 7) / 8 * 8 * a.Hk));
+    return grid_of(((int64_t)a.B * w.chunks + 7) / 8 * 8 * a.Hk);
 }
 
 }  // namespace scan

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(Cfg<IN>::C * 4, (sizeof(IN) == 2 && DKP <= 128
     const int tid = threadIdx.x, lane = tid & 63, mt = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
     int b, hk, chunk;
-    if (!chunk_of(blockIdx.x, a, w, &b, &hk, &chunk)) return;
+    if (!chunk_of((int)block_at(blockIdx.x, blockIdx.y), a, w, &b, &hk, &chunk)) return;
     const int G = a.H / a.Hk;
     int len = a.T;
     if (a.lengths) len = min(max(a.lengths[b], 0), a.T);

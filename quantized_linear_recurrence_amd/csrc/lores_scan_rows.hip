@@ -55,7 +55,8 @@ __device__ __forceinline__ float sum8(float x) {
 // NC = d_k / 32
 template <typename IN, int NC>
 __global__ void __launch_bounds__(256) lores_scan_rows_kernel(const ScanArgs a, const int tiles) {
-    const int unit = blockIdx.x / tiles, tile = blockIdx.x - unit * tiles;
+    const int block = (int)block_at(blockIdx.x, blockIdx.y), unit = block / tiles, tile = block - unit * tiles;
+    if (unit >= a.B * a.H) return;
     const int b = unit / a.H, h = unit - b * a.H, hk = h / (a.H / a.Hk);
     const int l = threadIdx.x & 7, row = tile * 32 + (threadIdx.x >> 3);
     if (row >= a.dv) return;                         // whole groups of 8 lanes
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(256) lores_scan_rows_kernel(const ScanArgs a, 
 template <typename IN>
 hipError_t by_width(const ScanArgs &a, hipStream_t s) {
     const int tiles = (a.dv + 31) / 32;
-    const dim3 grid((unsigned)((int64_t)a.B * a.H * tiles));
+    const dim3 grid = grid_of((int64_t)a.B * a.H * tiles);
     switch (a.dk / 32) {
         case 1: lores_scan_rows_kernel<IN, 1><<<grid, 256, 0, s>>>(a, tiles); break;
         case 2: lores_scan_rows_kernel<IN, 2><<<grid, 256, 0, s>>>(a, tiles); break;

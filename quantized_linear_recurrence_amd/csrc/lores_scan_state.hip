@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = lane & 15, g = lane >> 4;
     int unit, grp;
-    if (!unit_of(blockIdx.x, groups, a.B * a.H, &unit, &grp)) return;
+    if (!unit_of((int)block_at(blockIdx.x, blockIdx.y), groups, a.B * a.H, &unit, &grp)) return;
     const int b = unit / a.H, h = unit - b * a.H, hk = h / (a.H / a.Hk);
     const int col0 = (grp * NW + wv) * 16, col = col0 + m;   // the wavefront's value rows of S, the lane's
     const bool mine = col0 < a.dv, ok = col < a.dv;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(64 * NW) lores_scan_state_kernel(const ScanArg
 template <typename IN, int DKP, bool FAST, bool VEC, int NW>
 hipError_t go(bool backward, const ScanArgs &a, const ScanWork &w, hipStream_t s) {
     const int groups = (a.dv + 16 * NW - 1) / (16 * NW);
-    const dim3 grid((unsigned)(((int64_t)a.B * a.H + 7) / 8 * 8 * groups));
+    const dim3 grid = grid_of(((int64_t)a.B * a.H + 7) / 8 * 8 * groups);
     if (backward) {
         if (a.delta) lores_scan_state_kernel<IN, DKP, true, true, FAST, VEC, NW><<<grid, 64 * NW, 0, s>>>(a, w, groups);
         else lores_scan_state_kernel<IN, DKP, false, true, FAST, VEC, NW><<<grid, 64 * NW, 0, s>>>(a, w, groups);

@@ -14,6 +14,16 @@ namespace lores {
 int set_error(int code, const char *msg);
 int set_ok();
 
+// A launch takes fewer than 2^32 work-items along x, so more work-groups than
+// kGridRow (of at most 1024 threads; a multiple of the 8 XCDs) go over rows of the
+// grid.  The last row may be longer than what is left: kernels return at a
+// block_at() behind their work.
+constexpr int kGridRow = 1 << 21;
+inline dim3 grid_of(int64_t groups) {
+    return groups <= kGridRow ? dim3((uint32_t)groups) : dim3(kGridRow, (uint32_t)((groups + kGridRow - 1) / kGridRow));
+}
+__host__ __device__ constexpr int64_t block_at(uint32_t x, uint32_t y) { return (int64_t)y * kGridRow + x; }
+
 // ------------------------------------------------------------ the norm
 
 struct NormArgs {

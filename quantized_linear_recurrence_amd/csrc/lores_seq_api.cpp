@@ -30,7 +30,8 @@ int hip_status(hipError_t e, const char *what) {
     return lores::set_ok();
 }
 
-constexpr int64_t kMaxGroups = 0x7fffffff;           // work-groups along grid x
+// work-groups of a launch: with a row of the grid added they number below 2^31
+constexpr int64_t kMaxGroups = (int64_t)0x7fffffff - lores::kGridRow;
 
 int check_scan(const lores_scan_dims *d) {
     if (!d) return fail(LORES_EINVAL, "dims is NULL");
@@ -123,7 +124,7 @@ int check_work(uint64_t need, const void *work, size_t bytes) {
 }
 
 int check_norm(int64_t rows, int32_t n, int32_t in_bf16, int32_t w_bf16, float eps) {
-    if (rows < 0 || rows > kMaxGroups) return fail(LORES_EINVAL, "rows must be in [0, 2^31)");
+    if (rows < 0 || rows > 0x7fffffff) return fail(LORES_EINVAL, "rows must be in [0, 2^31)");
     if (n < 1 || n > LORES_MAX_NORM)
         return fail(LORES_EINVAL, "n must be in [1, %d] (got %d)", LORES_MAX_NORM, n);
     if (in_bf16 != 0 && in_bf16 != 1) return fail(LORES_EINVAL, "in_bf16 must be 0 or 1");
