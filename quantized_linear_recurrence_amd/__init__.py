@@ -286,8 +286,8 @@ def _raw_stream(stream, device):
     return (torch.cuda.current_stream(device.index) if stream is None else stream).cuda_stream
 
 
-def _whole(t, name, dtype, numel, device):
-    """The address of a contiguous tensor of `numel` elements (None: NULL)."""
+def _whole(t, name, dtype, shape, device):
+    """The address of a contiguous tensor of this shape (None: NULL)."""
     import torch
     if t is None:
         return None
@@ -299,15 +299,15 @@ def _whole(t, name, dtype, numel, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
 
 
-def _need(t, name, dtype, numel, device):
+def _need(t, name, dtype, shape, device):
     if t is None:
         raise TypeError(f"{name} must be a torch tensor")
-    return _whole(t, name, dtype, numel, device)
+    return _whole(t, name, dtype, shape, device)
 
 
 def _rows4(t, name, dtype, shape, device):
@@ -344,10 +344,10 @@ def _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths):
     kp, d.k_stride[:] = _rows4(k, "k", dt, (B, T, Hk, dk), dev)
     vp, d.v_stride[:] = _rows4(v, "v", dt, (B, T, H, dv), dev)
     f32 = torch.float32
-    args = (qp, kp, vp, _need(alpha, "alpha", f32, B * T * H, dev),
-            _need(beta, "beta", f32, B * T * H, dev),
-            _whole(lengths, "lengths", torch.int32, B, dev),
-            _whole(S0, "S0", f32, B * H * dv * dk, dev))
+    args = (qp, kp, vp, _need(alpha, "alpha", f32, (B, T, H), dev),
+            _need(beta, "beta", f32, (B, T, H), dev),
+            _whole(lengths, "lengths", torch.int32, (B,), dev),
+            _whole(S0, "S0", f32, (B, H, dv, dk), dev))
     return d, args, dev, dt
 
 
@@ -397,8 +397,8 @@ def lores_scan(q, k, v, alpha, beta, delta, S0=None, lengths=None, o=None, S=Non
             S = v.new_empty((d.B, d.H, d.d_v, d.d_k), dtype=torch.float32)
         work, wp, wn = _scan_work(d, 0, workspace, dev)
     _check(_lib.lib().lores_scan(
-        ctypes.byref(d), *args, _need(o, "o", dt, d.B * d.T * d.H * d.d_v, dev),
-        _need(S, "S", torch.float32, d.B * d.H * d.d_v * d.d_k, dev), wp, wn,
+        ctypes.byref(d), *args, _need(o, "o", dt, v.shape, dev),
+        _need(S, "S", torch.float32, (d.B, d.H, d.d_v, d.d_k), dev), wp, wn,
         _raw_stream(stream, dev)))
     return o, S
 
@@ -413,9 +413,9 @@ def lores_scan_backward(q, k, v, alpha, beta, delta, do, dS=None, S0=None, lengt
     """
     import torch
     d, args, dev, dt = _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths)
-    n, f32 = d.B * d.H * d.d_v * d.d_k, torch.float32
-    dop = _need(do, "do", dt, d.B * d.T * d.H * d.d_v, dev)
-    dSp = _whole(dS, "dS", f32, n, dev)
+    f32 = torch.float32
+    dop = _need(do, "do", dt, v.shape, dev)
+    dSp = _whole(dS, "dS", f32, (d.B, d.H, d.d_v, d.d_k), dev)
     with _on(stream):
         dq, dk, dv = q.new_empty(q.shape), q.new_empty(q.shape), v.new_empty(v.shape)
         da = v.new_empty((d.B, d.T, d.H), dtype=f32)
@@ -461,7 +461,7 @@ def _norm_shape(x, weight):
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"rows must be [..., n] with n >= 1, got {list(x.shape)}")
     n = x.shape[-1]
-    wp = _need(weight, "weight", weight.dtype, n, x.device)
+    wp = _need(weight, "weight", weight.dtype, (n,), x.device)
     return x.numel() // n, n, wp, int(weight.dtype is bf), int(x.dtype is bf)
 
 
@@ -509,8 +509,8 @@ def lores_rmsnorm_backward(h, weight, dy, eps, dresidual=None, stream=None):
     rows, n, wp, w_bf16, in_bf16 = _norm_shape(h, weight)
     dev, dt = h.device, h.dtype
     hp, hs = _norm_rows(h, "h", dt, h.shape, dev)
-    dyp = _need(dy, "dy", dt, rows * n, dev)
-    drp = _whole(dresidual, "dresidual", dt, rows * n, dev)
+    dyp = _need(dy, "dy", dt, h.shape, dev)
+    drp = _whole(dresidual, "dresidual", dt, h.shape, dev)
     size = ctypes.c_size_t(0)
     _check(_lib.lib().lores_rmsnorm_workspace(rows, n, ctypes.byref(size)))
     with _on(stream):
