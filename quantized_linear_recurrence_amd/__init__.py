@@ -10,6 +10,7 @@ kernels of liblores.so; if the library is missing, calls raise.
 PyTorch serves only as the device allocator and stream provider.
 """
 import ctypes
+import warnings
 
 import numpy as np
 
@@ -286,6 +287,11 @@ def _raw_stream(stream, device):
     return (torch.cuda.current_stream(device.index) if stream is None else stream).cuda_stream
 
 
+def _no_graph(what):
+    warnings.warn(f"{what} records no autograd graph: no gradient will reach its inputs. Call it and "
+                  f"{what}_backward from a torch.autograd.Function, or under torch.no_grad()", stacklevel=3)
+
+
 def _whole(t, name, dtype, shape, device):
     """The address of a contiguous tensor of this shape (None: NULL)."""
     import torch
@@ -387,9 +393,13 @@ def lores_scan(q, k, v, alpha, beta, delta, S0=None, lengths=None, o=None, S=Non
     or None.  Returns (o [B, T, H, d_v] of q's type, S [B, H, d_v, d_k] fp32);
     S is what lores_quant_state takes, and may be S0.  workspace: a device
     tensor of at least lores_scan_workspace bytes, or None to allocate it.
+    No autograd graph is recorded (lores_scan_backward has the gradients).
     """
     import torch
     d, args, dev, dt = _scan_inputs(q, k, v, alpha, beta, delta, S0, lengths)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or alpha.requires_grad
+                                    or beta.requires_grad or S0 is not None and S0.requires_grad):
+        _no_graph("lores_scan")
     with _on(stream):
         if o is None:
             o = v.new_empty(v.shape)
@@ -472,9 +482,13 @@ def lores_rmsnorm(x, weight, eps, residual=None, out_prec=None, stream=None):
     type, fp32 or bf16, scales None.  LORES_INT8 / LORES_FP8: y holds int8
     codes / torch.float8_e4m3fn values and scales [...] fp32 one factor per
     row.  h is the sum x + residual in x's type (x itself without a residual).
+    No autograd graph is recorded (lores_rmsnorm_backward has the gradients).
     """
     import torch
     rows, n, wp, w_bf16, in_bf16 = _norm_shape(x, weight)
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad
+                                    or residual is not None and residual.requires_grad):
+        _no_graph("lores_rmsnorm")
     dev, dt = x.device, x.dtype
     xp, xs = _norm_rows(x, "x", dt, x.shape, dev)
     rp, rs = (None, 0) if residual is None else _norm_rows(residual, "residual", dt, x.shape, dev)
