@@ -24,12 +24,13 @@
 // two lane exchanges.  A wavefront owns strips of 16 keys of the products with
 // S and dS, and a share of 16 tokens' rows of dP and Z.
 //
-// Measured (bf16, d_k = d_v = 128, delta): 128 units x 2048 tokens 453 us, 1.3
-// GB (0.8 of it S, dS, U and H) at 2.9 TB/s, matrix instructions busy for 18 %
+// Measured (bf16, d_k = d_v = 128, delta): 128 units x 2048 tokens 464 us, 1.3
+// GB (0.8 of it S, dS, U and H) at 2.8 TB/s, matrix instructions busy for 19 %
 // of the time.  Two thirds of a chunk go to the value columns, bound by the
 // loads and the planes' way through LDS; the last third is the double sum of
 // dalpha and the products with q and k, short steps between barriers with two
-// wavefronts per SIMD.  At d_k = 256 a wavefront holds two strips and spills.
+// wavefronts per SIMD.  At d_k > 128 a wavefront holds two strips and spills (84
+// to 684 bytes a lane at bf16, 156 at fp32 with delta and shared heads).
 #include "lores_scan_impl.h"
 
 namespace lores {

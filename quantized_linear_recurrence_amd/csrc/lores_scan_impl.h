@@ -581,10 +581,13 @@ struct RowFetch {
 // twice, which pays where that still leaves a work-group for each of the 256
 // compute units; with fewer units the rows are spread over more of them.
 // Measured at bf16, d_k = d_v = 128, all kernels of the call: 256 units x 4096
-// tokens 697 us by eight, 818 by four; 32 units 376 and 317; a training step
-// of 128 units 1288 and 1105.  At d_k = 256 eight wavefronts have too few
-// registers for the state (256 units x 512 tokens, d_v = 256: 370 us by eight,
-// 317 by four; fp32 1372 and 776), so the callers ask only at d_k <= 128.
+// tokens 723 us by eight, 859 by four; 32 units 439 and 351; backward, 256 units
+// x 1024 tokens 836 and 875, 128 units x 2048 1050 and 868.  With 64 value rows
+// four of the eight only fetch, and 256 units x 2048 tokens still take 267 us
+// by eight and 279 by four (512 units without delta 286 and 319).  At d_k = 256
+// eight wavefronts have too few registers for the state (256 units x 512 tokens,
+// d_v = 256: 395 us by eight, 331 by four; fp32 1359 and 770), so the callers ask
+// only at d_k <= 128.
 inline int scan_waves(const ScanArgs &a) {
     return (int64_t)a.B * a.H * ((a.dv + 127) / 128) >= 256 ? 8 : 4;
 }

@@ -14,8 +14,8 @@
 // follows the recurrence itself, so X stays as bounded as the tokens'
 // transition products are.
 //
-// Measured (bf16, d_k = 128, delta): 256 units x 4096 tokens 229 us, 1.07 GB at
-// 4.7 TB/s, close to a copy: bound by reading q and k and by writing the planes.
+// Measured (bf16, d_k = 128, delta): 256 units x 4096 tokens 220 us, 1.07 GB at
+// 4.9 TB/s, close to a copy: bound by reading q and k and by writing X and P.
 #include "lores_scan_impl.h"
 
 namespace lores {
@@ -43,7 +43,7 @@ struct PrepLds {
 
 // WORDS: P in fp32 instead of planes.  Two work-groups share a compute unit; asking for registers
 // for three is the same within 1 % (8 x 4096 tokens x 32 heads with the pass
-// behind: 692 and 693 us).
+// behind: 721 and 724 us).
 template <typename IN, int DKP, bool WORDS, bool DELTA>
 __global__ void __launch_bounds__(Cfg<IN>::C * 4, (sizeof(IN) == 2 && DKP <= 128 ? 2 : 1)) lores_scan_prep_kernel(const ScanArgs a, const ScanWork w) {
     constexpr int C = Cfg<IN>::C, NIN = Cfg<IN>::NIN, NT = C / 16, NB = tri_blocks(C), NW = NT, TH = 64 * NW;

@@ -11,12 +11,13 @@
 // LDS once for the work-group's wavefronts; K^T comes from the same rows by
 // transposing LDS reads.  Nothing but the chunks' order is sequential.
 //
-// Measured (bf16, d_k = d_v = 128, delta): 256 units x 4096 tokens 415 us, 1.6
-// GB at 3.9 TB/s with the matrix instructions busy for 47 % of the time, two
+// Measured (bf16, d_k = d_v = 128, delta): 256 units x 4096 tokens 494 us, 1.6
+// GB at 3.3 TB/s with the matrix instructions busy for 46 % of the time, two
 // wavefronts per SIMD taking turns between them and the splitting into planes.
-// 32 units x 4096 tokens 278 us, 4.3 us for each of 64 chunks: one wavefront
-// per SIMD, bound by the chain of a chunk's five products.  Storing S and U
-// for the backward pass, 128 units x 2048 tokens take 148 us (0.62 GB, 4.2 TB/s).
+// 32 units x 4096 tokens 321 us, 5.0 us for each of 64 chunks: one wavefront
+// on a quarter of the SIMDs, bound by the chain of a chunk's five products.
+// Storing S and U for the backward pass, 128 units x 2048 tokens take 149 us
+// (0.62 GB, 4.1 TB/s).
 #include "lores_scan_impl.h"
 
 namespace lores {
