@@ -11,7 +11,14 @@ DEV = "cuda:0"
 F32, BF16 = torch.float32, torch.bfloat16
 
 
+@pytest.fixture(autouse=True)
+def _give_back():
+    yield
+    torch.cuda.empty_cache()
+
+
 def _needs(gib):
+    torch.cuda.empty_cache()
     free, _ = torch.cuda.mem_get_info()
     if free < gib << 30:
         pytest.skip(f"needs {gib} GiB of GPU memory")
