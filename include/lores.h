@@ -56,6 +56,12 @@ enum {
     LORES_FP8 = 5   /* E4M3 (OCP fp8) values     + one fp32 scale per value row     */
 };
 #define LORES_NUM_PREC 6
+/* An output or operand of the layer operators, not a state: rows of E2M1 values
+ * with one power of two per 32 neighbours (see lores_mx_quant). */
+#define LORES_MXFP4 16
+
+/* What a gate z is put through: z, z / (1 + e^-z), 1 / (1 + e^-z). */
+enum { LORES_ACT_NONE = 0, LORES_ACT_SILU = 1, LORES_ACT_SIGMOID = 2 };
 
 /* Rounding of the requantization (per state; lores_state_set_rounding). */
 enum {
@@ -495,6 +501,158 @@ int lores_rmsnorm_backward(const void *h, int64_t h_stride, const void *weight, 
                            const void *dy, const void *dresidual, int64_t rows, int32_t n,
                            int32_t in_bf16, float eps, void *dx, float *dw, void *work,
                            size_t work_bytes, void *stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * Layer operators: what a layer runs per token around the recurrence - the
+ * norm behind it with its gate, the norms before and after a block with its
+ * gate and residual scale, and projections on microscaled 4-bit rows.
+ * ------------------------------------------------------------------------
+ * Rows may have any length 1 .. LORES_MAX_NORM and any alignment of their type;
+ * 16-byte aligned rows of a multiple of 8 elements are read faster.  Every row is
+ * computed.  Sums are fp32, results are rounded once, and do not depend on
+ * scheduling.  The gradients are those of the formula before its rounding.  At
+ * eps = 0 a row of zeros has an infinite r, and its y are NaN (4-bit rows: 0).
+ * An input of a call may be one of its outputs where the two have the same
+ * layout, for x (or h), the gate, the residual, dy and dh.
+ */
+
+/* Shapes of a gated norm: rows (token, head) of n elements.  Strides are in
+ * elements, between tokens and heads (0 or more: 0 broadcasts); a row is contiguous. */
+typedef struct {
+    int64_t tokens;            /* 0 .. ; tokens x heads < 2^31                       */
+    int32_t heads, n;          /* 1 .. LORES_MAX_HEADS, 1 .. LORES_MAX_NORM          */
+    int32_t in_bf16, w_bf16;   /* bf16 (1) or fp32 (0): x, gate and gradients; weight */
+    int32_t per_head;          /* weight [heads][n] (1) or [n] (0)                   */
+    int32_t act, gate_first;   /* LORES_ACT_*; 1: the gate comes before the norm     */
+    float eps;                 /* finite, >= 0                                       */
+    int64_t x_stride[2], gate_stride[2];
+} lores_gated_dims;
+
+/*
+ * lores_gated_norm - the norm of the recurrence's readout with its gate, per head:
+ *   gate_first 0: y_j = x_j r w_j a(z_j),  r = (mean_j x_j^2 + eps)^(-1/2)
+ *   gate_first 1: u_j = x_j a(z_j),  y_j = u_j r w_j,  r of u
+ *   x, gate    device rows by dims' strides
+ *   weight     device [n] or [heads][n]
+ *   out_prec   LORES_FP32, LORES_BF16 or LORES_MXFP4 (n a multiple of 32)
+ *   y          device out [tokens][heads][n] contiguous; LORES_MXFP4: codes
+ *              [tokens][heads n / 2], 16-byte aligned
+ *   scales     device out [tokens][4 ceil(heads n / 128)] (LORES_MXFP4: a token's
+ *              row as lores_mx_matmul reads it; else unused)
+ */
+int lores_gated_norm(const lores_gated_dims *dims, const void *x, const void *gate,
+                     const void *weight, int32_t out_prec, void *y, uint8_t *scales, void *stream);
+
+/* Bytes of device workspace of a lores_gated_norm_backward (host out). */
+int lores_gated_norm_workspace(const lores_gated_dims *dims, size_t *bytes);
+
+/*
+ * lores_gated_norm_backward - gradients of lores_gated_norm's inputs from dy:
+ *   dy         device [tokens][heads][n] contiguous, x's type
+ *   dx, dgate  device out [tokens][heads][n] contiguous, x's type
+ *   dw         device out [n] or [heads][n] fp32
+ *   work       device workspace of lores_gated_norm_workspace bytes, 16-byte aligned
+ */
+int lores_gated_norm_backward(const lores_gated_dims *dims, const void *x, const void *gate,
+                              const void *weight, const void *dy, void *dx, void *dgate, float *dw,
+                              void *work, size_t work_bytes, void *stream);
+
+/* Shapes of the norms around a block.  Strides in elements between rows, 0 or
+ * at least n (0 broadcasts one row). */
+typedef struct {
+    int64_t rows;              /* 0 .. 2^31 - 1                                      */
+    int32_t n;                 /* 1 .. LORES_MAX_NORM                                */
+    int32_t in_bf16, w_bf16;   /* bf16 (1) or fp32 (0): rows; both weights           */
+    int32_t act;               /* LORES_ACT_* of the gate                            */
+    float eps, scale;          /* eps of both norms; the residual scale (finite)     */
+    int64_t x_stride, res_stride, gate_stride;
+} lores_block_dims;
+
+/*
+ * lores_block_norm - a block's output x into the residual stream, and the next
+ * block's input:
+ *   p_j = x_j r1 w_j with r1 = (mean_j x_j^2 + eps)^(-1/2)   (x_j without a weight)
+ *   h_j = rnd(residual_j + scale a(gate_j) p_j)              (a = 1 without a gate)
+ *   y_j = h_j r2 wn_j with r2 = (mean_j h_j^2 + eps)^(-1/2)
+ *   x, residual, gate  device [rows][n] by dims' strides; residual and gate may be NULL
+ *   weight      device [n], the norm after the block, or NULL: none
+ *   weight_next device [n], the norm before the next one
+ *   out_prec    LORES_FP32, LORES_BF16, LORES_INT8, LORES_FP8 (z_j = fl(h_j wn_j)
+ *               coded as by lores_rmsnorm) or LORES_MXFP4 (n a multiple of 32; a row
+ *               that is not finite, or whose squares leave fp32's range, has NaN scales)
+ *   y           device out [rows][n] contiguous; LORES_MXFP4: codes [rows][n / 2],
+ *               16-byte aligned
+ *   scales      device out: 8 bits [rows] fp32; LORES_MXFP4 [rows][4 ceil(n / 128)] bytes
+ *   h           device out [rows][n] contiguous, x's type
+ */
+int lores_block_norm(const lores_block_dims *dims, const void *x, const void *residual,
+                     const void *gate, const void *weight, const void *weight_next,
+                     int32_t out_prec, void *y, void *scales, void *h, void *stream);
+
+/* Bytes of device workspace of a lores_block_norm_backward (host out). */
+int lores_block_norm_workspace(const lores_block_dims *dims, size_t *bytes);
+
+/*
+ * lores_block_norm_backward - gradients of lores_block_norm's inputs:
+ *   x, gate, weight, weight_next  as given to lores_block_norm
+ *   h          device [rows][n] contiguous, the sum that it stored
+ *   dy         device [rows][n] contiguous, x's type
+ *   dh         device [rows][n] contiguous, x's type: the gradient that reaches h
+ *              by other ways, or NULL
+ *   dx, dresidual  device out [rows][n] contiguous, x's type
+ *   dgate      device out [rows][n] contiguous, x's type (with a gate; else unused)
+ *   dw         device out [n] fp32 (with a weight; else unused)
+ *   dw_next    device out [n] fp32
+ *   work       device workspace of lores_block_norm_workspace bytes, 16-byte aligned
+ */
+int lores_block_norm_backward(const lores_block_dims *dims, const void *x, const void *h,
+                              const void *gate, const void *weight, const void *weight_next,
+                              const void *dy, const void *dh, void *dx, void *dresidual,
+                              void *dgate, float *dw, float *dw_next, void *work,
+                              size_t work_bytes, void *stream);
+
+/*
+ * lores_mx_quant - rows to microscaled 4-bit blocks: 32 neighbours share the
+ * scale 2^e, the smallest power of two (e >= -127) with max |x| < 7 2^e, and
+ * each is x 2^-e rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to
+ * the even code; the largest is rounded, never cut off).
+ *   x       device [rows][n], in_bf16 ? bf16 : fp32, rows x_stride elements apart;
+ *           n a multiple of 32 up to 2^24, 0 <= rows < 2^31, rows x n at most 2^38
+ *   codes   device out [rows][n / 2], 16-byte aligned: code c of column j in bits
+ *           4 (j & 1) .. of byte j / 2, its sign in bit 3
+ *   scales  device out [rows][4 ceil(n / 128)]: e + 127 of block j / 32, 0 behind the
+ *           last; 4-byte aligned
+ * A block with a value that is not finite has the scale 255 (NaN) and codes of 0.
+ */
+int lores_mx_quant(const void *x, int64_t x_stride, int64_t rows, int32_t n, int32_t in_bf16,
+                   uint8_t *codes, uint8_t *scales, void *stream);
+
+/* lores_mx_dequant - the values of such rows, device out [rows][n] contiguous, bf16
+ * or fp32, 16-byte aligned (values beyond the type's range become infinite; scale 255: NaN).  codes
+ * and scales as lores_mx_quant writes them. */
+int lores_mx_dequant(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t n,
+                     int32_t out_bf16, void *out, void *stream);
+
+/*
+ * lores_mx_matmul - a projection on 4-bit weights: out[m][j] = sum_k a[m][k] w[j][k].
+ *   a, a_scales  a_prec LORES_MXFP4: device codes [M][K / 2] and scales
+ *                [M][4 ceil(K / 128)]; LORES_FP8: device E4M3 [M][K] and one fp32
+ *                factor per row [M] (the rows that lores_rmsnorm writes)
+ *   w, w_scales  device codes [N][K / 2] and scales [N][4 ceil(K / 128)]
+ *   M, N, K      0 <= M < 2^31, 1 <= N <= 2^24, M x N at most 2^38, K a multiple of 32
+ *                in [32, 2^24]
+ *   out_prec     LORES_BF16, or with LORES_MXFP4 rows LORES_FP32
+ *   out          device out [M][N] contiguous, 16-byte aligned
+ * Codes are 16-byte aligned, scales 4-byte aligned; bytes behind the last block of a
+ * row's scales must be 0.  Products of 4-bit values are exact and summed in fp32.
+ * With E4M3 rows the matrix instruction adds 8 neighbours of k on a grid of 2^-13 of
+ * the power of two of the largest of the 8 (whose own E4M3 rounding is up to 2^-4 of
+ * it), and those sums in fp32; outputs are bf16 only for that.
+ */
+int lores_mx_matmul(const void *a, const void *a_scales, int32_t a_prec, const uint8_t *w,
+                    const uint8_t *w_scales, int64_t M, int32_t N, int32_t K, int32_t out_prec,
+                    void *out, void *stream);
 
 /* Thread-local description of the last error (empty string if none). */
 const char *lores_last_error(void);

@@ -15,8 +15,8 @@ import warnings
 import numpy as np
 
 from . import _lib
-from ._lib import (LORES_BF16, LORES_FP8, LORES_FP32, LORES_INT4, LORES_INT6, LORES_INT8,
-                   LORES_MAX_NORM, LORES_MAX_WINDOW, LORES_ROUND_NEAREST, LORES_ROUND_STOCHASTIC, LORES_SCALE_KEY,
+from ._lib import (LORES_ACT_NONE, LORES_ACT_SIGMOID, LORES_ACT_SILU, LORES_BF16, LORES_FP8, LORES_FP32, LORES_INT4, LORES_INT6, LORES_INT8,
+                   LORES_MAX_NORM, LORES_MAX_WINDOW, LORES_MXFP4, LORES_ROUND_NEAREST, LORES_ROUND_STOCHASTIC, LORES_SCALE_KEY,
                    LORES_SCALE_VALUE, LoresLayout, LoresLibraryMissing)
 
 __all__ = ["LORES_FP32", "LORES_BF16", "LORES_INT8", "LORES_INT4", "LORES_INT6", "LORES_FP8",
@@ -28,7 +28,9 @@ __all__ = ["LORES_FP32", "LORES_BF16", "LORES_INT8", "LORES_INT4", "LORES_INT6",
            "lores_state_head_map", "lores_decay_stat", "lores_assign_precision",
            "lores_decode_step", "lores_step_launches", "lores_quant_state", "lores_dequant_state",
            "lores_scan", "lores_scan_workspace", "lores_scan_backward", "lores_rmsnorm", "lores_rmsnorm_backward",
-           "LORES_MAX_NORM",
+           "LORES_MAX_NORM", "LORES_MXFP4", "LORES_ACT_NONE", "LORES_ACT_SILU", "LORES_ACT_SIGMOID",
+           "lores_gated_norm", "lores_gated_norm_backward", "lores_block_norm", "lores_block_norm_backward",
+           "lores_mx_quant", "lores_mx_dequant", "lores_mx_matmul",
            "lores_last_error", "lores_spec_version"]
 
 
@@ -535,3 +537,327 @@ def lores_rmsnorm_backward(h, weight, dy, eps, dresidual=None, stream=None):
                                              dx.data_ptr(), dw.data_ptr(), work.data_ptr(),
                                              size.value, _raw_stream(stream, dev)))
     return dx, dw
+
+
+# ------------------------------------------------------------------- layers
+
+def _current(device):
+    """Launches inside go to `device`, where the tensors are."""
+    import torch
+    return _NOTHING if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _strided(t, name, like, kept):
+    """A tensor of like's shape, type and device whose last dimension is
+    contiguous and whose dimensions before the last `kept` have one stride: its
+    address, that stride and those of the kept dimensions but the last."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t is not like:
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, x is on {like.device}")
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must be {list(like.shape)}, got {list(t.shape)}")
+    shape, st = t.shape, t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    step, size = None, 1
+    for d in range(len(shape) - kept - 1, -1, -1):
+        if shape[d] == 1:
+            continue
+        if step is None:
+            step = st[d]
+        elif st[d] != step * size:
+            raise ValueError(f"the leading dimensions of {name} must lie one stride apart")
+        size *= shape[d]
+    return t.data_ptr(), step, st[len(shape) - kept:-1]
+
+
+def _layer_types(x, weight, name):
+    import torch
+    if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
+        raise TypeError(f"x and {name} must be torch tensors")
+    if x.device.type != "cuda":
+        raise ValueError(f"x must be on the GPU, got {x.device}")
+    bf, f32 = torch.bfloat16, torch.float32
+    for t, what in ((x, "x"), (weight, name)):
+        if t.dtype is not bf and t.dtype is not f32:
+            raise TypeError(f"{what} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return int(x.dtype is bf), int(weight.dtype is bf)
+
+
+def _needs_grad(*ts):
+    import torch
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+
+
+def _mx_pair(t, lead, n):
+    """Tensors for rows of n 4-bit values: codes and scales."""
+    import torch
+    return (t.new_empty((*lead, n // 2), dtype=torch.uint8),
+            t.new_empty((*lead, (n + 127) // 128 * 4), dtype=torch.uint8))
+
+
+def _row_out(x, out_prec, in_bf16, allowed):
+    """The output precision and its torch type (None: 4-bit blocks)."""
+    import torch
+    if out_prec is None:
+        out_prec = LORES_BF16 if in_bf16 else LORES_FP32
+    if out_prec not in allowed:
+        raise ValueError("out_prec must be one of " + ", ".join(allowed.values()))
+    return out_prec, {LORES_FP32: torch.float32, LORES_BF16: torch.bfloat16, LORES_INT8: torch.int8,
+                      LORES_FP8: torch.float8_e4m3fn}.get(out_prec)
+
+
+def _gated_dims(x, gate, weight, eps, act, gate_first):
+    in_bf16, w_bf16 = _layer_types(x, weight, "weight")
+    if x.dim() < 2 or x.shape[-1] < 1 or x.shape[-2] < 1:
+        raise ValueError(f"x must be [..., heads, n], got {list(x.shape)}")
+    heads, n = x.shape[-2:]
+    xp, xt, (xh,) = _strided(x, "x", x, 2)
+    gp, gt, (gh,) = _strided(gate, "gate", x, 2)
+    per_head = weight.dim() == 2
+    wp = _need(weight, "weight", weight.dtype, (heads, n) if per_head else (n,), x.device)
+    d = _lib.LoresGatedDims(x.numel() // (heads * n), heads, n, in_bf16, w_bf16, int(per_head), int(act),
+                            int(gate_first), eps)
+    d.x_stride[:] = (xt or 0, xh)
+    d.gate_stride[:] = (gt or 0, gh)
+    return d, xp, gp, wp
+
+
+_GATED_OUT = {LORES_FP32: "LORES_FP32", LORES_BF16: "LORES_BF16", LORES_MXFP4: "LORES_MXFP4"}
+_BLOCK_OUT = {LORES_FP32: "LORES_FP32", LORES_BF16: "LORES_BF16", LORES_INT8: "LORES_INT8",
+              LORES_FP8: "LORES_FP8", LORES_MXFP4: "LORES_MXFP4"}
+
+
+def lores_gated_norm(x, gate, weight, eps, act=LORES_ACT_SILU, gate_first=False, out_prec=None,
+                     stream=None):
+    """The norm of the recurrence's readout with its gate, per head.
+
+    x, gate [..., heads, n] (bf16 or fp32, alike; the last dimension contiguous,
+    the leading ones one stride apart: a slice of a projection's rows will do),
+    weight [n] or [heads, n].  norm(x) weight a(gate), or with gate_first
+    norm(x a(gate)) weight; act: LORES_ACT_SILU, LORES_ACT_SIGMOID or
+    LORES_ACT_NONE.  Returns (y, scales): out_prec None, LORES_FP32 or
+    LORES_BF16: y [..., heads, n] in x's type, fp32 or bf16, scales None;
+    LORES_MXFP4: codes [..., heads n / 2] and scales as lores_mx_matmul takes them.
+    No autograd graph is recorded (lores_gated_norm_backward has the gradients).
+    """
+    d, xp, gp, wp = _gated_dims(x, gate, weight, eps, act, gate_first)
+    if _needs_grad(x, gate, weight):
+        _no_graph("lores_gated_norm")
+    out_prec, dt = _row_out(x, out_prec, d.in_bf16, _GATED_OUT)
+    scales = None
+    with _current(x.device):
+        with _on(stream):
+            if dt is None:
+                y, scales = _mx_pair(x, x.shape[:-2], d.heads * d.n)
+            else:
+                y = x.new_empty(x.shape, dtype=dt)
+        _check(_lib.lib().lores_gated_norm(ctypes.byref(d), xp, gp, wp, out_prec, y.data_ptr(),
+                                           None if scales is None else scales.data_ptr(),
+                                           _raw_stream(stream, x.device)))
+    return y, scales
+
+
+def lores_gated_norm_backward(x, gate, weight, dy, eps, act=LORES_ACT_SILU, gate_first=False,
+                              stream=None):
+    """Gradients (dx, dgate, dw) of lores_gated_norm's unquantized output: dx, dgate
+    of x's shape and type, contiguous; dw of the weight's shape, fp32."""
+    import torch
+    d, xp, gp, wp = _gated_dims(x, gate, weight, eps, act, gate_first)
+    dyp = _need(dy, "dy", x.dtype, x.shape, x.device)
+    size = ctypes.c_size_t(0)
+    _check(_lib.lib().lores_gated_norm_workspace(ctypes.byref(d), ctypes.byref(size)))
+    with _current(x.device):
+        with _on(stream):
+            dx, dgate = x.new_empty(x.shape), x.new_empty(x.shape)
+            dw = x.new_empty(weight.shape, dtype=torch.float32)
+            work = x.new_empty(size.value, dtype=torch.uint8)
+        _check(_lib.lib().lores_gated_norm_backward(
+            ctypes.byref(d), xp, gp, wp, dyp, dx.data_ptr(), dgate.data_ptr(), dw.data_ptr(),
+            work.data_ptr(), size.value, _raw_stream(stream, x.device)))
+    return dx, dgate, dw
+
+
+def _block_dims(x, residual, weight, weight_next, eps, scale, gate, act):
+    in_bf16, w_bf16 = _layer_types(x, weight_next, "weight_next")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must be [..., n] with n >= 1, got {list(x.shape)}")
+    n = x.shape[-1]
+    ptrs, strides = [], []
+    for t, name in ((x, "x"), (residual, "residual"), (gate, "gate")):
+        p, s, _ = (None, None, None) if t is None else _strided(t, name, x, 1)
+        ptrs.append(p)
+        strides.append(n if s is None else s)
+    wn = _need(weight_next, "weight_next", weight_next.dtype, (n,), x.device)
+    w = _whole(weight, "weight", weight_next.dtype, (n,), x.device)
+    d = _lib.LoresBlockDims(x.numel() // n, n, in_bf16, w_bf16, int(act), eps, scale, *strides)
+    return d, ptrs, w, wn
+
+
+def lores_block_norm(x, residual, weight, weight_next, eps, scale=1.0, gate=None, act=LORES_ACT_NONE,
+                     out_prec=None, stream=None):
+    """The norms around a block: its output x into the residual stream, and the
+    next block's input.
+
+    h = residual + scale a(gate) norm(x) weight, y = norm(h) weight_next.  x,
+    residual and gate [..., n] (bf16 or fp32, alike; contiguous last dimension, the
+    leading ones one stride apart), residual and gate may be None; weight [n] or
+    None (x as it is), weight_next [n] of the same type.  Returns (y, scales, h) as
+    lores_rmsnorm does; out_prec LORES_MXFP4 gives codes [..., n / 2] and scales as
+    lores_mx_matmul takes them.  No autograd graph is recorded
+    (lores_block_norm_backward has the gradients).
+    """
+    import torch
+    d, (xp, rp, gp), w, wn = _block_dims(x, residual, weight, weight_next, eps, scale, gate, act)
+    if _needs_grad(x, residual, weight, weight_next, gate):
+        _no_graph("lores_block_norm")
+    out_prec, dt = _row_out(x, out_prec, d.in_bf16, _BLOCK_OUT)
+    scales = None
+    with _current(x.device):
+        with _on(stream):
+            if dt is None:
+                y, scales = _mx_pair(x, x.shape[:-1], d.n)
+            else:
+                y = x.new_empty(x.shape, dtype=dt)
+                if out_prec in (LORES_INT8, LORES_FP8):
+                    scales = x.new_empty(x.shape[:-1], dtype=torch.float32)
+            h = x.new_empty(x.shape)
+        _check(_lib.lib().lores_block_norm(ctypes.byref(d), xp, rp, gp, w, wn, out_prec, y.data_ptr(),
+                                           None if scales is None else scales.data_ptr(), h.data_ptr(),
+                                           _raw_stream(stream, x.device)))
+    return y, scales, h
+
+
+def lores_block_norm_backward(x, h, weight, weight_next, dy, eps, scale=1.0, gate=None,
+                              act=LORES_ACT_NONE, dh=None, stream=None):
+    """Gradients (dx, dresidual, dgate, dw, dw_next) of lores_block_norm's
+    unquantized outputs, from dy and the gradient dh that reaches h otherwise (or
+    None).  h is the sum that lores_block_norm returned.  dgate and dw are None
+    without a gate or a weight; the weights' gradients are fp32."""
+    import torch
+    d, (xp, _, gp), w, wn = _block_dims(x, None, weight, weight_next, eps, scale, gate, act)
+    hp = _need(h, "h", x.dtype, x.shape, x.device)
+    dyp = _need(dy, "dy", x.dtype, x.shape, x.device)
+    dhp = _whole(dh, "dh", x.dtype, x.shape, x.device)
+    size = ctypes.c_size_t(0)
+    _check(_lib.lib().lores_block_norm_workspace(ctypes.byref(d), ctypes.byref(size)))
+    with _current(x.device):
+        with _on(stream):
+            dx, dres = x.new_empty(x.shape), x.new_empty(x.shape)
+            dgate = None if gate is None else x.new_empty(x.shape)
+            dwn = x.new_empty(d.n, dtype=torch.float32)
+            dw = None if weight is None else torch.empty_like(dwn)
+            work = x.new_empty(size.value, dtype=torch.uint8)
+        _check(_lib.lib().lores_block_norm_backward(
+            ctypes.byref(d), xp, hp, gp, w, wn, dyp, dhp, dx.data_ptr(), dres.data_ptr(),
+            None if dgate is None else dgate.data_ptr(), None if dw is None else dw.data_ptr(),
+            dwn.data_ptr(), work.data_ptr(), size.value, _raw_stream(stream, x.device)))
+    return dx, dres, dgate, dw, dwn
+
+
+def lores_mx_quant(x, stream=None):
+    """Rows x [..., n] (bf16 or fp32, n a multiple of 32) as 4-bit blocks.
+
+    Returns (codes, scales), uint8: codes [..., n / 2], two E2M1 values a byte, the
+    even column in the low half; scales [..., 4 ceil(n / 128)], the biased power of
+    two of each block of 32 (255: a value that is not finite), 0 behind the last.
+    """
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch tensor")
+    if x.device.type != "cuda":
+        raise ValueError(f"x must be on the GPU, got {x.device}")
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    if x.dim() < 1 or x.shape[-1] < 32 or x.shape[-1] % 32:
+        raise ValueError(f"x must be [..., n] with n a multiple of 32, got {list(x.shape)}")
+    n = x.shape[-1]
+    xp, step, _ = _strided(x, "x", x, 1)
+    with _current(x.device):
+        with _on(stream):
+            codes, scales = _mx_pair(x, x.shape[:-1], n)
+        _check(_lib.lib().lores_mx_quant(xp, n if step is None else step, x.numel() // n, n,
+                                         int(x.dtype is torch.bfloat16), codes.data_ptr(),
+                                         scales.data_ptr(), _raw_stream(stream, x.device)))
+    return codes, scales
+
+
+def _mx_rows(codes, scales, name):
+    """Checks a pair of lores_mx_quant's: rows and their length."""
+    import torch
+    if not isinstance(codes, torch.Tensor) or not isinstance(scales, torch.Tensor):
+        raise TypeError(f"{name} and its scales must be torch tensors")
+    if codes.device.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU, got {codes.device}")
+    if codes.dim() < 1 or codes.shape[-1] < 16 or codes.shape[-1] % 16:
+        raise ValueError(f"{name} must be [..., n / 2] with n a multiple of 32, got {list(codes.shape)}")
+    n = 2 * codes.shape[-1]
+    u8, lead = torch.uint8, codes.shape[:-1]
+    return (_need(codes, name, u8, codes.shape, codes.device),
+            _need(scales, f"{name}'s scales", u8, (*lead, (n + 127) // 128 * 4), codes.device),
+            codes.numel() // (n // 2), n)
+
+
+def lores_mx_dequant(codes, scales, dtype=None, stream=None):
+    """The values [..., n] of lores_mx_quant's rows, in dtype (torch.bfloat16, the
+    default, or torch.float32)."""
+    import torch
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    cp, sp, rows, n = _mx_rows(codes, scales, "codes")
+    with _current(codes.device):
+        with _on(stream):
+            out = codes.new_empty((*codes.shape[:-1], n), dtype=dtype)
+        _check(_lib.lib().lores_mx_dequant(cp, sp, rows, n, int(dtype is torch.bfloat16), out.data_ptr(),
+                                           _raw_stream(stream, codes.device)))
+    return out
+
+
+def lores_mx_matmul(a, a_scales, w, w_scales, out_prec=LORES_BF16, out=None, stream=None):
+    """A projection on 4-bit weights: [..., N] = a [..., K] times w [N, K] transposed.
+
+    w, w_scales: lores_mx_quant's of the weights.  a, a_scales: 4-bit rows
+    (lores_mx_quant, or a norm with LORES_MXFP4), or torch.float8_e4m3fn [..., K] with
+    one fp32 factor per row [...] (lores_rmsnorm, lores_block_norm with LORES_FP8).
+    out_prec: LORES_BF16, or for 4-bit rows LORES_FP32.  out: a contiguous tensor to
+    write to, or None.
+    """
+    import torch
+    if out_prec != LORES_BF16 and out_prec != LORES_FP32:
+        raise ValueError("out_prec must be LORES_BF16 or LORES_FP32")
+    wp, wsp, N, K = _mx_rows(w, w_scales, "w")
+    if w.dim() != 2:
+        raise ValueError(f"w must be [N, K / 2], got {list(w.shape)}")
+    if not isinstance(a, torch.Tensor):
+        raise TypeError("a must be a torch tensor")
+    if a.device != w.device:
+        raise ValueError(f"a is on {a.device}, w is on {w.device}")
+    if a.dtype is torch.float8_e4m3fn:
+        prec = LORES_FP8
+        if a.dim() < 1 or a.shape[-1] != K:
+            raise ValueError(f"a must be [..., {K}], got {list(a.shape)}")
+        if out_prec != LORES_BF16:
+            raise ValueError("E4M3 rows give LORES_BF16")
+        ap = _need(a, "a", a.dtype, a.shape, w.device)
+        asp = _need(a_scales, "a_scales", torch.float32, a.shape[:-1], w.device)
+    else:
+        prec = LORES_MXFP4
+        ap, asp, _, ka = _mx_rows(a, a_scales, "a")
+        if ka != K:
+            raise ValueError(f"a has rows of {ka}, w of {K}")
+    lead = a.shape[:-1]
+    dt = torch.bfloat16 if out_prec == LORES_BF16 else torch.float32
+    with _current(w.device):
+        with _on(stream):
+            if out is None:
+                out = w.new_empty((*lead, N), dtype=dt)
+        op = _need(out, "out", dt, (*lead, N), w.device)
+        _check(_lib.lib().lores_mx_matmul(ap, asp, prec, wp, wsp, lead.numel(), N, K, out_prec, op,
+                                          _raw_stream(stream, w.device)))
+    return out

@@ -11,6 +11,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblores.so
 SPEC_VERSION = 8                     # LORES_SPEC_VERSION of include/lores.h
 LORES_FP32, LORES_BF16, LORES_INT8, LORES_INT4, LORES_INT6, LORES_FP8 = 0, 1, 2, 3, 4, 5
 NUM_PREC = 6
+LORES_MXFP4 = 16                     # rows of 4-bit blocks: of the layer operators, not a state
+LORES_ACT_NONE, LORES_ACT_SILU, LORES_ACT_SIGMOID = 0, 1, 2
 LORES_ROUND_STOCHASTIC, LORES_ROUND_NEAREST = 0, 1
 LORES_SCALE_VALUE, LORES_SCALE_KEY = 0, 1
 LORES_MAX_WINDOW = 16
@@ -27,6 +29,9 @@ EXPORTS = ("lores_state_alloc", "lores_state_alloc_axis", "lores_state_alloc_win
            "lores_dequant_state",
            "lores_scan_workspace", "lores_scan", "lores_scan_backward",
            "lores_rmsnorm", "lores_rmsnorm_workspace", "lores_rmsnorm_backward",
+           "lores_gated_norm", "lores_gated_norm_workspace", "lores_gated_norm_backward",
+           "lores_block_norm", "lores_block_norm_workspace", "lores_block_norm_backward",
+           "lores_mx_quant", "lores_mx_dequant", "lores_mx_matmul",
            "lores_last_error", "lores_spec_version")
 
 
@@ -53,6 +58,20 @@ class LoresScanDims(ctypes.Structure):
                 ("in_bf16", ctypes.c_int32), ("delta", ctypes.c_int32),
                 ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
                 ("v_stride", ctypes.c_int64 * 3)]
+
+
+class LoresGatedDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("in_bf16", ctypes.c_int32), ("w_bf16", ctypes.c_int32), ("per_head", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("gate_first", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x_stride", ctypes.c_int64 * 2), ("gate_stride", ctypes.c_int64 * 2)]
+
+
+class LoresBlockDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n", ctypes.c_int32), ("in_bf16", ctypes.c_int32),
+                ("w_bf16", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("x_stride", ctypes.c_int64), ("res_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -107,6 +126,20 @@ def lib():
     L.lores_rmsnorm_workspace.argtypes = [i64, i32, ctypes.POINTER(sz)]
     L.lores_rmsnorm_backward.argtypes = [vp, i64, vp, i32, vp, vp, i64, i32, i32, ctypes.c_float,
                                          vp, vp, vp, sz, vp]
+    gated, block = ctypes.POINTER(LoresGatedDims), ctypes.POINTER(LoresBlockDims)
+    L.lores_gated_norm.argtypes = [gated, vp, vp, vp, i32, vp, vp, vp]
+    L.lores_gated_norm_workspace.argtypes = [gated, ctypes.POINTER(sz)]
+    L.lores_gated_norm_backward.argtypes = [gated] + [vp] * 8 + [sz, vp]
+    L.lores_block_norm.argtypes = [block] + [vp] * 5 + [i32] + [vp] * 4
+    L.lores_block_norm_workspace.argtypes = [block, ctypes.POINTER(sz)]
+    L.lores_block_norm_backward.argtypes = [block] + [vp] * 13 + [sz, vp]
+    L.lores_mx_quant.argtypes = [vp, i64, i64, i32, i32, vp, vp, vp]
+    L.lores_mx_dequant.argtypes = [vp, vp, i64, i32, i32, vp, vp]
+    L.lores_mx_matmul.argtypes = [vp, vp, i32, vp, vp, i64, i32, i32, i32, vp, vp]
+    for f in (L.lores_gated_norm, L.lores_gated_norm_workspace, L.lores_gated_norm_backward,
+              L.lores_block_norm, L.lores_block_norm_workspace, L.lores_block_norm_backward,
+              L.lores_mx_quant, L.lores_mx_dequant, L.lores_mx_matmul):
+        f.restype = ctypes.c_int
     for f in (L.lores_scan_workspace, L.lores_scan, L.lores_scan_backward, L.lores_rmsnorm,
               L.lores_rmsnorm_workspace, L.lores_rmsnorm_backward):
         f.restype = ctypes.c_int

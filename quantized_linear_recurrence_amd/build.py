@@ -25,7 +25,8 @@ SOURCES = ["lores_api.cpp", "lores_seq_api.cpp", "lores_aux.hip", "lores_step_in
            "lores_step_key_int6.hip", "lores_step_key_fp8.hip", "lores_window.hip",
            "lores_window_int8.hip", "lores_window_int4.hip", "lores_window_int6.hip",
            "lores_window_fp8.hip", "lores_norm.hip", "lores_scan_rows.hip", "lores_scan_prep.hip",
-           "lores_scan_state.hip", "lores_scan_back.hip", "lores_scan_grad.hip"]
+           "lores_scan_state.hip", "lores_scan_back.hip", "lores_scan_grad.hip", "lores_layer_api.cpp",
+           "lores_gated.hip", "lores_block.hip", "lores_mx.hip", "lores_mx_product.hip"]
 
 COMMON = [
     "-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",

@@ -1,0 +1,38 @@
+// A gate's activation and its slope, for the norms that take a gate.
+#pragma once
+
+#include "lores_rows.h"
+
+namespace lores {
+namespace {
+
+// 1 / (1 + e^-z), as 2^(-z log2 e) and a reciprocal (1 ulp each).  The exponent
+// -z log2 e is off by up to 2^-24 |z| log2 e, which bf16 inputs do not see; for fp32
+// the rounded part is carried on as a factor 1 + x ln 2.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z) {
+    constexpr float log2e = 0x1.715476p+0f;
+    if constexpr (sizeof(T) == 2) {
+        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * log2e));
+    } else {
+        // beyond +-150 the result is 0 or 1; NaN goes by itself
+        const float m = -fminf(fmaxf(z, -150.0f), 150.0f);
+        const float t = m * log2e;
+        const float lo = fmaf(m, 0x1.4ae0cp-26f, fmaf(m, log2e, -t));   // log2 e = log2e + 0x1.4ae0cp-26
+        const float e = __builtin_amdgcn_exp2f(t);
+        const float s = __builtin_amdgcn_rcpf(1.0f + fmaf(e, lo * 0x1.62e43p-1f, e));
+        return z != z ? z : s;
+    }
+}
+
+// a(z) from z and s = 1 / (1 + e^-z)
+__device__ __forceinline__ float gate_value(int act, float z, float s) {
+    return act == LORES_ACT_SILU ? z * s : act == LORES_ACT_SIGMOID ? s : z;
+}
+// da/dz
+__device__ __forceinline__ float gate_slope(int act, float z, float s) {
+    return act == LORES_ACT_SILU ? s * fmaf(z, 1.0f - s, 1.0f) : act == LORES_ACT_SIGMOID ? s * (1.0f - s) : 1.0f;
+}
+
+}  // namespace
+}  // namespace lores

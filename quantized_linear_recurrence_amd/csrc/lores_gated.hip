@@ -1,0 +1,197 @@
+// The norm of the recurrence's readout with its gate (lores_gated_norm), and
+// its backward pass.  Rows are (token, head); with a(z) the gate, s its slope:
+//   norm first: y = n w a(z), n = x r       gate first: u = x a(z), y = n w, n = u r
+// Backward, from dy:
+//   norm first: e = dy w a,  dx = r (e - n mean(e n)),  dz = dy w n s,  dw = sum dy a n
+//   gate first: e = dy w,  du = r (e - n mean(e n)),  dx = du a,  dz = du x s,  dw = sum dy n
+//
+// Bound by memory: a row is read once, kept in registers and written once.
+#include "lores_gate.h"
+#include "lores_layer.h"
+
+namespace lores {
+namespace {
+
+// the token of a row: the quotient by the reciprocal is at most one too small
+__device__ __forceinline__ void split_row(const GatedArgs &a, uint32_t row, uint32_t &token, uint32_t &head) {
+    token = __umulhi(row, a.per_heads);
+    head = row - token * (uint32_t)a.heads;
+    if (head >= (uint32_t)a.heads) { ++token; head -= (uint32_t)a.heads; }
+}
+
+template <typename T, int TPR, int VPT, int VEC>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_kernel(const GatedArgs a) {
+    constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;  // rows of a work-group
+    __shared__ float sm[TPR > 64 ? TPR / 64 : 1][2];
+    const int t = threadIdx.x % TPR;
+    const int64_t row = block_at(blockIdx.x, blockIdx.y) * ROWS + threadIdx.x / TPR;
+    if (row >= a.rows) return;                       // whole groups of TPR threads; no barrier for TPR <= 64
+    uint32_t token, head;
+    split_row(a, (uint32_t)row, token, head);
+    float x[VPT][8], z[VPT][8], w[VPT][8];
+    load_row<T, TPR, VPT, VEC>((const T *)a.x + token * a.xs[0] + head * a.xs[1], t, a.n, x);
+    load_row<T, TPR, VPT, VEC>((const T *)a.gate + token * a.gs[0] + head * a.gs[1], t, a.n, z);
+    const int64_t w_at = a.per_head ? (int64_t)head * a.n : 0;
+    load_either<TPR, VPT, VEC>((const uint8_t *)a.w + w_at * (a.w_bf16 ? 2 : 4), a.w_bf16, t, a.n, w);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float g = gate_value(a.act, z[i][e], a.act ? sigmoid<T>(z[i][e]) : 0.0f);
+            if (a.gate_first) x[i][e] = x[i][e] * g;
+            sum = fmaf(x[i][e], x[i][e], sum);
+            w[i][e] = a.gate_first ? w[i][e] : w[i][e] * g;
+        }
+    sum = row_sum<TPR>(sum, sm);
+    const float rstd = 1.0f / sqrtf(sum / (float)a.n + a.eps);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * rstd * w[i][e];
+    if (a.out_prec == LORES_FP32) {
+        store_row<float, TPR, VPT, VEC>((float *)a.y + row * a.n, t, a.n, x);
+    } else if (a.out_prec == LORES_BF16) {
+        store_row<uint16_t, TPR, VPT, VEC>((uint16_t *)a.y + row * a.n, t, a.n, x);
+    } else if constexpr (VEC != ROWS_ANY) {          // a token's heads are one row of blocks
+        const int per = mx_scale_stride((int64_t)a.heads * a.n), blocks = a.n / 32;
+        if (sum == 0.0f) {                           // (without an epsilon r is an infinity)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+        }
+        store_mx<TPR, VPT>((uint8_t *)a.y + row * (a.n / 2), a.scales + (int64_t)token * per + head * blocks,
+                           head + 1 == (uint32_t)a.heads ? per - a.heads * blocks : 0, t, a.n,
+                           !(sum < __builtin_inff()), x);
+    }
+}
+
+// dw is summed by each work-group over its rows (with weights per head, the
+// rows of one head), in registers and over the rows side by side in LDS; a
+// second kernel adds the work-groups' sums in a fixed order.
+template <typename T, int TPR, int VPT, int VEC>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_backward_kernel(const GatedArgs a) {
+    constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
+    __shared__ float sm[TPR > 64 ? TPR / 64 : 1][2];
+    __shared__ __attribute__((aligned(16))) float sums[ROWS > 1 ? ROWS : 1][ROWS > 1 ? TPR * VPT * 8 : 1];
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    // weights per head: the work-groups of neighbouring heads are neighbours
+    const uint32_t own = a.per_head ? blockIdx.x % (uint32_t)a.heads : 0;
+    const uint32_t group = a.per_head ? blockIdx.x / (uint32_t)a.heads : blockIdx.x;
+    const int64_t count = a.per_head ? a.rows / a.heads : a.rows;    // rows the groups share out
+    float w[VPT][8], dw[VPT][8];
+    load_either<TPR, VPT, VEC>((const uint8_t *)a.w + (int64_t)own * a.n * (a.w_bf16 ? 2 : 4), a.w_bf16, t, a.n, w);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+    for (int64_t r = (int64_t)group * ROWS + sub; r < count; r += (int64_t)a.groups * ROWS) {
+        uint32_t token = (uint32_t)r, head = own;
+        if (!a.per_head) split_row(a, (uint32_t)r, token, head);
+        const int64_t row = (int64_t)token * a.heads + head;
+        Kept<T> kx[VPT], kz[VPT], kg[VPT];
+        keep_row<T, TPR, VPT, VEC>((const T *)a.x + token * a.xs[0] + head * a.xs[1], t, a.n, kx);
+        keep_row<T, TPR, VPT, VEC>((const T *)a.gate + token * a.gs[0] + head * a.gs[1], t, a.n, kz);
+        keep_row<T, TPR, VPT, VEC>((const T *)a.dy + row * a.n, t, a.n, kg);
+        float s[VPT][8], ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float z = kz[i].at(e), x = kx[i].at(e);
+                s[i][e] = a.act ? sigmoid<T>(z) : 0.0f;
+                const float g = gate_value(a.act, z, s[i][e]), u = a.gate_first ? x * g : x;
+                const float d = kg[i].at(e) * w[i][e];
+                ss = fmaf(u, u, ss);
+                dot = fmaf(u, a.gate_first ? d : d * g, dot);
+            }
+        reduce<TPR, false>(ss, dot, sm);
+        const float rstd = 1.0f / sqrtf(ss / (float)a.n + a.eps);
+        const float c = dot * rstd / (float)a.n;     // mean(e n)
+        float dx[VPT][8], dz[VPT][8];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float z = kz[i].at(e), x = kx[i].at(e), dy = kg[i].at(e);
+                const float g = gate_value(a.act, z, s[i][e]), sl = gate_slope(a.act, z, s[i][e]);
+                if (a.gate_first) {
+                    const float n = x * g * rstd, du = rstd * fmaf(-n, c, dy * w[i][e]);
+                    dw[i][e] = fmaf(dy, n, dw[i][e]);
+                    dx[i][e] = du * g;
+                    dz[i][e] = du * x * sl;
+                } else {
+                    const float n = x * rstd, d = dy * w[i][e];
+                    dw[i][e] = fmaf(dy * g, n, dw[i][e]);
+                    dx[i][e] = rstd * fmaf(-n, c, d * g);
+                    dz[i][e] = d * n * sl;
+                }
+            }
+        store_row<T, TPR, VPT, VEC>((T *)a.dx + row * a.n, t, a.n, dx);
+        store_row<T, TPR, VPT, VEC>((T *)a.dgate + row * a.n, t, a.n, dz);
+    }
+    float *part = a.part + ((int64_t)group * (a.per_head ? a.heads : 1) + own) * a.n;
+    if constexpr (ROWS > 1) {                        // the rows side by side, in their order
+        store_row<float, TPR, VPT, VEC>(sums[sub], t, a.n, dw);
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.n; c += 256) {
+            float x = sums[0][c];
+#pragma unroll
+            for (int i = 1; i < ROWS; ++i) x += sums[i][c];
+            part[c] = x;
+        }
+    } else {
+        store_row<float, TPR, VPT, VEC>(part, t, a.n, dw);
+    }
+}
+
+template <typename T, int TPR, int VPT>
+hipError_t go(int mode, bool back, const GatedArgs &a, hipStream_t s) {
+    constexpr int ROWS = TPR < 256 ? 256 / TPR : 1, TH = TPR < 256 ? 256 : TPR;
+    if (back) {
+        const dim3 grid((uint32_t)a.groups * (a.per_head ? a.heads : 1));
+        if (mode == ROWS_VEC) lores_gated_backward_kernel<T, TPR, VPT, ROWS_VEC><<<grid, TH, 0, s>>>(a);
+        else lores_gated_backward_kernel<T, TPR, VPT, ROWS_ANY><<<grid, TH, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    const dim3 grid = grid_of((a.rows + ROWS - 1) / ROWS);
+    if (mode == ROWS_VEC) lores_gated_kernel<T, TPR, VPT, ROWS_VEC><<<grid, TH, 0, s>>>(a);
+    else if (mode == ROWS_BLOCKS) lores_gated_kernel<T, TPR, VPT, ROWS_BLOCKS><<<grid, TH, 0, s>>>(a);
+    else lores_gated_kernel<T, TPR, VPT, ROWS_ANY><<<grid, TH, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t by_width(int mode, bool back, const GatedArgs &a, hipStream_t s) {
+    if (a.n <= 128) return go<T, 16, 1>(mode, back, a, s);
+    if (a.n <= 512) return go<T, 64, 1>(mode, back, a, s);
+    if (a.n <= 1024) return go<T, 64, 2>(mode, back, a, s);
+    if (a.n <= 2048) return go<T, 256, 1>(mode, back, a, s);
+    if (a.n <= 4096) return go<T, 256, 2>(mode, back, a, s);
+    if (a.n <= 8192) return go<T, 1024, 1>(mode, back, a, s);
+    return go<T, 1024, 2>(mode, back, a, s);
+}
+
+}  // namespace
+
+int gated_groups(int64_t tokens, int32_t heads, int32_t n, int32_t per_head) {
+    if (!per_head) return norm_groups(tokens * heads, n);
+    const int all = norm_groups(tokens, n), most = (1024 + heads - 1) / heads;
+    return all < most ? all : most;
+}
+
+hipError_t launch_gated(bool in_bf16, int mode, const GatedArgs &a, hipStream_t s) {
+    return in_bf16 ? by_width<uint16_t>(mode, false, a, s) : by_width<float>(mode, false, a, s);
+}
+
+hipError_t launch_gated_backward(bool in_bf16, int mode, const GatedArgs &a, hipStream_t s) {
+    if (a.rows) {                                    // without rows dw is a sum of nothing
+        const hipError_t e = in_bf16 ? by_width<uint16_t>(mode, true, a, s) : by_width<float>(mode, true, a, s);
+        if (e != hipSuccess) return e;
+    }
+    const int cols = a.n * (a.per_head ? a.heads : 1);
+    return launch_group_sums(a.part, a.rows ? a.groups : 0, cols, cols, a.dw, nullptr, s);
+}
+
+}  // namespace lores

@@ -22,157 +22,10 @@
 // Measured (bf16, 16384 x 4096, residual): forward 87 us, 0.54 GB at 6.2 TB/s;
 // backward 112 us, 0.55 GB at 5.0 TB/s, and 7 us for the groups' sums.
 // 64 x 4096 to int8 take 5.0 us, launch and two waits on memory.
-#include "lores_seq.h"
+#include "lores_rows.h"
 
 namespace lores {
 namespace {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ float bf2f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-// round to nearest even; a NaN stays one
-__device__ __forceinline__ uint16_t f2bf(float f) {
-    const __bf16 b = (__bf16)f;
-    return __builtin_bit_cast(uint16_t, b);
-}
-
-template <typename T> struct Elem;
-template <> struct Elem<float> {
-    static __device__ __forceinline__ float get(const float *p) { return *p; }
-    static __device__ __forceinline__ void put(float *p, float x) { *p = x; }
-    static __device__ __forceinline__ float rnd(float x) { return x; }
-    static __device__ __forceinline__ void get8(const float *p, float *x) {
-        const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) { x[e] = a[e]; x[4 + e] = b[e]; }
-    }
-    static __device__ __forceinline__ void put8(float *p, const float *x) {
-        *(f32x4 *)p = f32x4{x[0], x[1], x[2], x[3]};
-        *(f32x4 *)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
-    }
-};
-template <> struct Elem<uint16_t> {
-    static __device__ __forceinline__ float get(const uint16_t *p) { return bf2f(*p); }
-    static __device__ __forceinline__ void put(uint16_t *p, float x) { *p = f2bf(x); }
-    static __device__ __forceinline__ float rnd(float x) { return bf2f(f2bf(x)); }
-    static __device__ __forceinline__ void get8(const uint16_t *p, float *x) {
-        const u32x4 a = *(const u32x4 *)p;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __uint_as_float(a[e] << 16);
-            x[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
-        }
-    }
-    static __device__ __forceinline__ void put8(uint16_t *p, const float *x) {
-        u32x4 a;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            a[e] = (uint32_t)f2bf(x[2 * e]) | ((uint32_t)f2bf(x[2 * e + 1]) << 16);
-        *(u32x4 *)p = a;
-    }
-};
-
-// One thread's elements of a row: VPT vectors of 8.  VEC: 8 neighbours per
-// vector and thread (16-byte accesses); else element e of vector i is 8 i + e
-// strides of TPR away, so that neighbouring threads read neighbouring
-// elements of rows at any alignment.
-template <int TPR, bool VEC>
-__device__ __forceinline__ int col(int t, int i, int e) {
-    return VEC ? (i * TPR + t) * 8 + e : (i * 8 + e) * TPR + t;
-}
-
-template <typename T, int TPR, int VPT, bool VEC>
-__device__ __forceinline__ void load_row(const T *p, int t, int n, float (&x)[VPT][8]) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if constexpr (VEC) {
-            const int c = (i * TPR + t) * 8;
-            if (c < n) {
-                Elem<T>::get8(p + c, x[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = col<TPR, VEC>(t, i, e);
-                x[i][e] = c < n ? Elem<T>::get(p + c) : 0.0f;
-            }
-        }
-    }
-}
-
-template <typename T, int TPR, int VPT, bool VEC>
-__device__ __forceinline__ void store_row(T *p, int t, int n, const float (&x)[VPT][8]) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if constexpr (VEC) {
-            const int c = (i * TPR + t) * 8;
-            if (c < n) Elem<T>::put8(p + c, x[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = col<TPR, VEC>(t, i, e);
-                if (c < n) Elem<T>::put(p + c, x[i][e]);
-            }
-        }
-    }
-}
-
-template <int TPR, int VPT, bool VEC>
-__device__ __forceinline__ void store_bytes(uint8_t *p, int t, int n, const uint8_t (&x)[VPT][8]) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if constexpr (VEC) {
-            const int c = (i * TPR + t) * 8;
-            u32x2 w = {0, 0};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)x[i][e] << (8 * (e & 3));
-            if (c < n) *(u32x2 *)(p + c) = w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = col<TPR, VEC>(t, i, e);
-                if (c < n) p[c] = x[i][e];
-            }
-        }
-    }
-}
-
-// Over one row's threads: the sum of `a`, and the maximum (MAX) or the sum of
-// `b`, in every one of them.
-template <int TPR, bool MAX>
-__device__ __forceinline__ void reduce(float &a, float &b, float (*sm)[2]) {
-    constexpr int W = TPR < 64 ? TPR : 64;
-#pragma unroll
-    for (int d = 1; d < W; d <<= 1) {
-        a += __shfl_xor(a, d);
-        const float o = __shfl_xor(b, d);
-        b = MAX ? fmaxf(b, o) : b + o;
-    }
-    if constexpr (TPR > 64) {
-        const int wv = threadIdx.x >> 6;
-        __syncthreads();                             // the last row's values have been read
-        if ((threadIdx.x & 63) == 0) { sm[wv][0] = a; sm[wv][1] = b; }
-        __syncthreads();
-        a = sm[0][0];
-        b = sm[0][1];
-#pragma unroll
-        for (int i = 1; i < TPR / 64; ++i) {
-            a += sm[i][0];
-            b = MAX ? fmaxf(b, sm[i][1]) : b + sm[i][1];
-        }
-    }
-}
-
-template <typename T, int TPR, int VPT, bool VEC>
-__device__ __forceinline__ void load_weight(const NormArgs &a, int t, float (&w)[VPT][8]) {
-    if (a.w_bf16) load_row<uint16_t, TPR, VPT, VEC>((const uint16_t *)a.w, t, a.n, w);
-    else load_row<float, TPR, VPT, VEC>((const float *)a.w, t, a.n, w);
-}
 
 template <typename T, int TPR, int VPT, bool VEC>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const NormArgs a) {
@@ -192,7 +45,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
             for (int e = 0; e < 8; ++e) h[i][e] = Elem<T>::rnd(h[i][e] + r[i][e]);
         store_row<T, TPR, VPT, VEC>((T *)a.h + row * a.n, t, a.n, h);
     }
-    load_weight<T, TPR, VPT, VEC>(a, t, w);
+    load_either<TPR, VPT, VEC>(a.w, a.w_bf16, t, a.n, w);
     // magnitudes are compared as bits, where a NaN is above all numbers: the
     // floating-point maximum would drop it.  It goes on as an infinity.
     const float inf = __builtin_inff();
@@ -209,44 +62,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_kernel(const
     float mx = __uint_as_float(min(bits, __float_as_uint(inf)));
     reduce<TPR, true>(sum, mx, sm);
     const float rstd = 1.0f / sqrtf(sum / (float)a.n + a.eps);
-    if (a.out_prec == LORES_FP32 || a.out_prec == LORES_BF16) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * rstd;
-        if (a.out_prec == LORES_FP32)
-            store_row<float, TPR, VPT, VEC>((float *)a.y + row * a.n, t, a.n, h);
-        else
-            store_row<uint16_t, TPR, VPT, VEC>((uint16_t *)a.y + row * a.n, t, a.n, h);
-        return;
-    }
-    const float top = a.out_prec == LORES_INT8 ? 127.0f : 448.0f;
-    // a row with a z that is not finite, or with squares beyond fp32, has the
-    // scale NaN and the codes 0
-    const bool lost = !(mx < inf) || !(sum < inf);
-    const float nan = __builtin_nanf("");
-    // a maximum under 2^-119 (top / m would leave fp32's range) counts as
-    // 2^-119, in the codes and in the scale: such a row uses fewer codes
-    const float m = fmaxf(mx, 0x1p-119f);
-    const float inv = lost ? nan : top * (1.0f / m);
-    uint8_t c[VPT][8];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float x = h[i][e] * inv;
-            if (a.out_prec == LORES_INT8) {
-                const float q = rintf(fminf(fmaxf(x, -127.0f), 127.0f));
-                c[i][e] = x == x ? (uint8_t)(int8_t)(int)q : (uint8_t)0;
-            } else {
-                const float q = fminf(fmaxf(x, -448.0f), 448.0f);
-                c[i][e] = x == x ? (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false)
-                                 : (uint8_t)0;
-            }
-        }
-    store_bytes<TPR, VPT, VEC>((uint8_t *)a.y + row * a.n, t, a.n, c);
-    // (without an epsilon the r of a row of zeros is an infinity)
-    if (t == 0) a.scales[row] = lost ? nan : mx == 0.0f ? 0.0f : m / top * rstd;
+    norm_store<TPR, VPT, VEC, false>(a.y, a.scales, a.out_prec, row, t, a.n, sum, mx, rstd, h);
 }
 
 template <typename T, int TPR, int VPT, bool VEC>
@@ -256,7 +72,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_backward_ker
     __shared__ __attribute__((aligned(16))) float sums[ROWS > 1 ? ROWS : 1][ROWS > 1 ? TPR * VPT * 8 : 1];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     float w[VPT][8], dw[VPT][8];
-    load_weight<T, TPR, VPT, VEC>(a, t, w);
+    load_either<TPR, VPT, VEC>(a.w, a.w_bf16, t, a.n, w);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -309,21 +125,26 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_norm_backward_ker
     }
 }
 
-// dw = the groups' sums added up: 16 columns per work-group, 64 slices of the
-// groups in parallel, the slices joined in LDS.
-__global__ void __launch_bounds__(1024) lores_norm_dw_kernel(const NormArgs a) {
+// The groups' sums added up: 16 columns per work-group, 64 slices of the
+// groups in parallel, the slices joined in LDS.  Columns from `split` on go to
+// `out1`.
+__global__ void __launch_bounds__(1024) lores_norm_dw_kernel(const float *part, int groups, int cols, int split,
+                                                             float *out0, float *out1) {
     __shared__ float sm[64][17];
     const int c = blockIdx.x * 16 + (threadIdx.x & 15), sl = threadIdx.x >> 4;
     float s = 0.0f;
-    if (c < a.n)
-        for (int g = sl; g < a.groups; g += 64) s += a.part[(int64_t)g * a.n + c];
+    if (c < cols)
+        for (int g = sl; g < groups; g += 64) s += part[(int64_t)g * cols + c];
     sm[sl][threadIdx.x & 15] = s;
     __syncthreads();
     for (int d = 32; d >= 1; d >>= 1) {
         if (sl < d) sm[sl][threadIdx.x & 15] += sm[sl + d][threadIdx.x & 15];
         __syncthreads();
     }
-    if (sl == 0 && c < a.n) a.dw[c] = sm[0][threadIdx.x];
+    if (sl == 0 && c < cols) {
+        if (c < split) out0[c] = sm[0][threadIdx.x];
+        else out1[c - split] = sm[0][threadIdx.x];
+    }
 }
 
 template <typename T, int TPR, int VPT>
@@ -383,7 +204,12 @@ hipError_t launch_norm_backward(bool in_bf16, bool vec, const NormArgs &a, hipSt
         const hipError_t e = in_bf16 ? by_width<uint16_t>(vec, true, a, s) : by_width<float>(vec, true, a, s);
         if (e != hipSuccess) return e;
     }
-    lores_norm_dw_kernel<<<dim3((unsigned)((a.n + 15) / 16)), 1024, 0, s>>>(a);
+    return launch_group_sums(a.part, a.groups, a.n, a.n, a.dw, nullptr, s);
+}
+
+hipError_t launch_group_sums(const float *part, int groups, int cols, int split, float *out0, float *out1,
+                             hipStream_t s) {
+    lores_norm_dw_kernel<<<dim3((unsigned)((cols + 15) / 16)), 1024, 0, s>>>(part, groups, cols, split, out0, out1);
     return hipGetLastError();
 }
 

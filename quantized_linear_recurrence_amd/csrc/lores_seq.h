@@ -47,6 +47,13 @@ int norm_groups(int64_t rows, int32_t n);
 hipError_t launch_norm(bool in_bf16, bool vec, const NormArgs &a, hipStream_t s);
 hipError_t launch_norm_backward(bool in_bf16, bool vec, const NormArgs &a, hipStream_t s);
 
+// `cols` columns summed over `groups` rows of `part`; columns from `split` on go to out1.
+hipError_t launch_group_sums(const float *part, int groups, int cols, int split, float *out0, float *out1,
+                             hipStream_t s);
+
+// Bytes between the scales of rows of 4-bit blocks: whole words of 4 blocks.
+__host__ __device__ constexpr int mx_scale_stride(int64_t n) { return (int)((n + 127) / 128 * 4); }
+
 // ------------------------------------------------------------ the recurrence
 
 struct ScanArgs {
