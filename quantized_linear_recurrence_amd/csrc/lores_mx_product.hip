@@ -6,6 +6,7 @@
 // ends with 4 neighbouring outputs of one row.  E4M3 rows lie otherwise: lane l
 // holds 16 neighbours from 16 (l / 16) and 16 from 64 + 16 (l / 16); their one
 // factor per row is multiplied in at the end.
+#include "lores_direct.h"
 #include "lores_layer.h"
 
 namespace lores {
@@ -110,10 +111,191 @@ hipError_t go_few(const MxProduct &p, hipStream_t s) {
     return hipGetLastError();
 }
 
+// ------------------------------------------------------------ many rows
+//
+// A work-group has WM x WN wavefronts, each with 16 MI rows and 16 NI columns in
+// registers.  Steps of 128 k go from memory straight to LDS, S steps deep; a
+// wavefront reads the next step's operands while it multiplies this one's.
+// A 4-bit row of a step is 64 bytes: pieces of 16 bytes, whose places are turned by
+// the row so that 8 neighbouring rows read their like pieces from different banks;
+// an E4M3 row is 128 bytes of 8 pieces, turned alike.
+template <bool FP8, int TM, int TN>
+struct Stage {
+    uint8_t w[TN * 64], a[TM * (FP8 ? 128 : 64)];
+    uint8_t ws[TN * 4], as[FP8 ? 16 : TM * 4];
+};
+
+// A wavefront's operands of a step: its rows, and half of its columns at a time.
+template <bool FP8, int MI>
+struct Rows {
+    i32x4 x[MI][FP8 ? 2 : 1];
+    int s[MI];
+};
+template <int NH>
+struct Columns {
+    i32x4 x[NH];
+    int s[NH];
+};
+
+// The work-group's tile: each of the 8 XCDs (work-groups go to them in turn) takes a
+// run of tiles, and a run goes over 8 rows of tiles before the next column.
+__device__ __forceinline__ void tile_of(int64_t b, int64_t tiles_m, int64_t tiles_n, int64_t &m, int64_t &n) {
+    const int64_t all = tiles_m * tiles_n, each = all / 8, more = all % 8, x = b % 8;
+    const int64_t t = x * each + (x < more ? x : more) + b / 8;
+    const int64_t band = t / (8 * tiles_n), first = band * 8;
+    const int64_t high = tiles_m - first < 8 ? tiles_m - first : 8, in = t - band * 8 * tiles_n;
+    m = first + in % high;
+    n = in / high;
+}
+
+template <bool FP8, bool BF16, int MI, int NI, int WM, int WN, int S>
+__global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxProduct p) {
+    constexpr int TM = 16 * MI * WM, TN = 16 * NI * WN, NW = WM * WN;
+    constexpr int AB = FP8 ? 128 : 64, AR = 1024 / AB;          // bytes of a row, rows of a load
+    constexpr int LW = TN / 16 / NW, LA = TM / AR / NW;         // a wavefront's loads of a step
+    constexpr int PW = TN / 64, PA = FP8 ? 0 : TM / 64;         // scales: 64 rows a load
+    constexpr int LS = (PW + PA + NW - 1) / NW;
+    constexpr int L = LW + LA + LS;
+    static_assert(LW * NW * 16 == TN && LA * NW * AR == TM && TN % 64 == 0 && TM % 64 == 0, "loads");
+    __shared__ __attribute__((aligned(1024))) Stage<FP8, TM, TN> st[S];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int wm = wv % WM, wn = wv / WM;
+    int64_t tm, tn;
+    tile_of(block_at(blockIdx.x, blockIdx.y), (p.M + TM - 1) / TM, (p.N + TN - 1) / TN, tm, tn);
+    const int64_t m0 = tm * TM, n0 = tn * TN;
+    if (m0 >= p.M || n0 >= p.N) return;
+    const int steps = (p.K + 127) / 128, per = mx_scale_stride(p.K);
+    const int64_t wrow = p.K / 2, arow = FP8 ? p.K : p.K / 2;
+    const int last_m = (int)min(p.M - 1 - m0, (int64_t)TM - 1), last_n = (int)min(p.N - 1 - n0, (int64_t)TN - 1);
+    const uint8_t *wb = p.w + n0 * wrow, *ab = p.a + m0 * arow;
+    const uint8_t *wsb = p.w_scales + n0 * per, *asb = FP8 ? nullptr : p.a_scales + m0 * per;
+    // a lane's piece of its row, the same in all its loads; rows behind the end are the last one
+    const int wpiece = (lane & 3) ^ ((lane >> 3) & 3), apiece = FP8 ? (lane & 7) ^ ((lane >> 3) & 7) : wpiece;
+    uint32_t wat[LW], aat[LA], sat[LS];
+#pragma unroll
+    for (int i = 0; i < LW; ++i)
+        wat[i] = (uint32_t)min((wv + i * NW) * 16 + (lane >> 2), last_n) * (uint32_t)wrow + wpiece * 16;
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+        aat[i] = (uint32_t)min((wv + i * NW) * AR + lane / (AB / 16), last_m) * (uint32_t)arow + apiece * 16;
+    int spart[LS];
+#pragma unroll
+    for (int i = 0; i < LS; ++i) {                   // (a wavefront without a part of its own repeats another's)
+        spart[i] = __builtin_amdgcn_readfirstlane((wv + i * NW) % (PW + PA));
+        sat[i] = spart[i] < PW ? (uint32_t)min(spart[i] * 64 + lane, last_n) * (uint32_t)per
+                               : (uint32_t)min((spart[i] - PW) * 64 + lane, last_m) * (uint32_t)per;
+    }
+    const int wv_ = __builtin_amdgcn_readfirstlane(wv);
+    auto load = [&](int k) {
+        Stage<FP8, TM, TN> &s = st[k % S];
+        // k behind a row's end: zeros
+        const bool win = 128 * k + 32 * wpiece < p.K, ain = FP8 ? 128 * k + 16 * apiece < p.K : win;
+        const i32x4 zero = {};
+#pragma unroll
+        for (int i = 0; i < LW; ++i) {
+            uint8_t *to = s.w + (wv_ + i * NW) * 1024;
+            if (win) direct16(wb + (int64_t)k * 64, wat[i], to);
+            else *(i32x4 *)(to + lane * 16) = zero;
+        }
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            uint8_t *to = s.a + (wv_ + i * NW) * 1024;
+            if (ain) direct16(ab + (int64_t)k * AB, aat[i], to);
+            else *(i32x4 *)(to + lane * 16) = zero;
+        }
+#pragma unroll
+        for (int i = 0; i < LS; ++i) {
+            if (FP8 || spart[i] < PW) direct4(wsb + (int64_t)k * 4, sat[i], s.ws + spart[i] * 256);
+            else direct4(asb + (int64_t)k * 4, sat[i], s.as + (spart[i] - PW) * 256);
+        }
+    };
+    // places in a stage, but for constants: like pieces of rows 16 apart are turned alike
+    const int wplace = (wn * NI * 16 + r) * 64 + (g ^ ((r >> 1) & 3)) * 16, wsplace = (wn * NI * 16 + r) * 4 + g;
+    const int aplace = FP8 ? (wm * MI * 16 + r) * 128 + (g ^ (r & 7)) * 16 : (wm * MI * 16 + r) * 64 + (g ^ ((r >> 1) & 3)) * 16;
+    const int aplace2 = (wm * MI * 16 + r) * 128 + ((4 + g) ^ (r & 7)) * 16, asplace = (wm * MI * 16 + r) * 4 + g;
+    constexpr int NH = NI / 2;
+    auto read_rows = [&](int k, Rows<FP8, MI> &o) {
+        const Stage<FP8, TM, TN> &s = st[k % S];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            o.x[i][0] = *(const i32x4 *)(s.a + aplace + i * 16 * AB);
+            if constexpr (FP8) o.x[i][1] = *(const i32x4 *)(s.a + aplace2 + i * 16 * AB);
+            o.s[i] = FP8 ? 127 : s.as[asplace + i * 64];
+        }
+    };
+    auto read_columns = [&](int k, int half, Columns<NH> &o) {
+        const Stage<FP8, TM, TN> &s = st[k % S];
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+            o.x[i] = *(const i32x4 *)(s.w + wplace + (half * NH + i) * 1024);
+            o.s[i] = s.ws[wsplace + (half * NH + i) * 64];
+        }
+    };
+    f32x4 c[MI][NI] = {};
+    auto multiply = [&](const Rows<FP8, MI> &a, const Columns<NH> &w, int half) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            i32x8 x = {a.x[i][0][0], a.x[i][0][1], a.x[i][0][2], a.x[i][0][3], 0, 0, 0, 0};
+            if constexpr (FP8)
+                x = i32x8{a.x[i][0][0], a.x[i][0][1], a.x[i][0][2], a.x[i][0][3],
+                          a.x[i][1][0], a.x[i][1][1], a.x[i][1][2], a.x[i][1][3]};
+#pragma unroll
+            for (int j = 0; j < NH; ++j) {
+                const i32x8 y = {w.x[j][0], w.x[j][1], w.x[j][2], w.x[j][3], 0, 0, 0, 0};
+                c[i][half * NH + j] = product<FP8>(y, x, c[i][half * NH + j], w.s[j], a.s[i]);
+            }
+        }
+    };
+    const int ahead = min(S, steps);
+    for (int k = 0; k < ahead; ++k) load(k);
+    if (steps >= S) arrived_but<L * (S - 1)>();
+    else arrived();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    Rows<FP8, MI> a[2];
+    Columns<NH> w[2];
+    read_rows(0, a[0]);
+    read_columns(0, 0, w[0]);
+    auto step = [&](int k, const Rows<FP8, MI> &now, Rows<FP8, MI> &next) {
+        read_columns(k, 1, w[1]);
+        multiply(now, w[0], 0);
+        if (k + 1 < steps) {
+            // this wavefront's reads of step k are done and its loads of step k + 1 have
+            // landed; behind the barrier that holds for all of them, so step k's place
+            // takes step k + S
+            if (k + S <= steps) arrived_but<L * (S - 2)>();
+            else arrived();
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            if (k + S < steps) load(k + S);
+            read_rows(k + 1, next);
+            read_columns(k + 1, 0, w[0]);
+        }
+        multiply(now, w[1], 1);
+    };
+    for (int k = 0; k < steps; k += 2) {
+        step(k, a[0], a[1]);
+        if (k + 1 < steps) step(k + 1, a[1], a[0]);
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+            put<FP8, BF16>(p, m0 + (wm * MI + i) * 16 + r, (int)n0 + (wn * NI + j) * 16 + 4 * g, c[i][j]);
+}
+
+template <bool FP8, bool BF16, int MI, int NI, int WM, int WN, int S>
+hipError_t go_tile(const MxProduct &p, hipStream_t s) {
+    constexpr int TM = 16 * MI * WM, TN = 16 * NI * WN;
+    const int64_t groups = (p.M + TM - 1) / TM * ((p.N + TN - 1) / TN);
+    lores_mx_tile_kernel<FP8, BF16, MI, NI, WM, WN, S><<<grid_of(groups), 64 * WM * WN, 0, s>>>(p);
+    return hipGetLastError();
+}
+
 template <bool FP8, bool BF16>
 hipError_t go(const MxProduct &p, hipStream_t s) {
     if (p.M <= 16) return go_few<FP8, BF16, 1>(p, s);
-    return go_few<FP8, BF16, 4>(p, s);
+    if (p.M <= 64) return go_few<FP8, BF16, 4>(p, s);
+    if (p.M * p.N >= (int64_t)256 * 256 * 128) return go_tile<FP8, BF16, 4, 8, 4, 2, 3>(p, s);
+    return go_tile<FP8, BF16, 4, 4, 2, 2, 3>(p, s);
 }
 
 }  // namespace

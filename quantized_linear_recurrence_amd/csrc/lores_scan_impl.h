@@ -20,6 +20,7 @@
 // instructions.  ORD = 2 leaves out 2^-17, for sums that end in bf16.
 #pragma once
 
+#include "lores_direct.h"
 #include "lores_seq.h"
 
 namespace lores {
@@ -427,22 +428,6 @@ struct TriWords {
         *(f32x4 *)&x[tri_block(I, J)][at_(row, c >> 2)] = f32x4{v[0], v[1], v[2], v[3]};
     }
 };
-
-// 16 bytes per lane from memory (`src`, the same in all lanes, plus the lane's
-// offset in bytes) straight to LDS, lane i's to `lds` + 16 i (`lds` the same in
-// all lanes).  The compiler does not count these loads: arrived() waits for
-// all of the wavefront's, and a barrier behind it makes them the
-// work-group's.  (Written as the instruction because the builtin's wait
-// before every LDS read that might alias would undo the prefetch; there is
-// no output register to be overwritten in flight.)
-__device__ __forceinline__ void direct16(const void *src, uint32_t lane_at, void *lds) {
-    // the low half of a generic LDS address is its offset; nothing else in these
-    // kernels uses m0
-    const uint32_t at = (uint32_t)(uintptr_t)lds;
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                 :: "v"(lane_at), "s"(src), "s"(at) : "memory");
-}
-__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Contiguous bytes (a multiple of 16) to LDS, by the work-group's NW wavefronts.
 template <int BYTES, int NW>
