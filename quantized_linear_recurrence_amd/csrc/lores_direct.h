@@ -26,12 +26,5 @@ __device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::
 template <int N>
 __device__ __forceinline__ void arrived_but() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
 
-// 4 bytes per lane, lane i's to `lds` + 4 i.
-__device__ __forceinline__ void direct4(const void *src, uint32_t lane_at, void *lds) {
-    const uint32_t at = (uint32_t)(uintptr_t)lds;
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
-                 :: "v"(lane_at), "s"(src), "s"(at) : "memory");
-}
-
 }  // namespace
 }  // namespace lores

@@ -6,6 +6,8 @@
 // ends with 4 neighbouring outputs of one row.  E4M3 rows lie otherwise: lane l
 // holds 16 neighbours from 16 (l / 16) and 16 from 64 + 16 (l / 16); their one
 // factor per row is multiplied in at the end.
+#include <type_traits>
+
 #include "lores_direct.h"
 #include "lores_layer.h"
 
@@ -28,15 +30,20 @@ __device__ __forceinline__ f32x4 product(const i32x8 &w, const i32x8 &a, f32x4 c
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, FP8 ? 0 : 4, 0, ws, 0, as);
 }
 
-// 4 outputs of row m from column j on
+template <bool BF16>
+__device__ __forceinline__ void put4(const MxProduct &p, int64_t at, f32x4 c) {
+    if constexpr (BF16) *(u16x4 *)((uint16_t *)p.out + at) = u16x4{to_bf16(c[0]), to_bf16(c[1]), to_bf16(c[2]), to_bf16(c[3])};
+    else *(f32x4 *)((float *)p.out + at) = c;
+}
+
+// 4 outputs of row m from column j on, as far as there are any
 template <bool FP8, bool BF16>
 __device__ __forceinline__ void put(const MxProduct &p, int64_t m, int j, f32x4 c) {
     if (m >= p.M) return;
     if constexpr (FP8) c *= p.a_rows[m];
     const int64_t at = m * p.N + j;
     if ((p.N & 3) == 0 && j + 3 < p.N) {
-        if constexpr (BF16) *(u16x4 *)((uint16_t *)p.out + at) = u16x4{to_bf16(c[0]), to_bf16(c[1]), to_bf16(c[2]), to_bf16(c[3])};
-        else *(f32x4 *)((float *)p.out + at) = c;
+        put4<BF16>(p, at, c);
         return;
     }
 #pragma unroll
@@ -122,10 +129,15 @@ hipError_t go_few(const MxProduct &p, hipStream_t s) {
 template <bool FP8, int TM, int TN>
 struct Stage {
     uint8_t w[TN * 64], a[TM * (FP8 ? 128 : 64)];
-    uint8_t ws[TN * 4], as[FP8 ? 16 : TM * 4];
+};
+// The scales of 4 steps, 16 bytes a row: the columns', the rows' behind them.  (4 bytes
+// a step and row would be as many requests to the cache as the codes are.)
+template <bool FP8, int TM, int TN>
+struct Scales {
+    uint8_t s[TN * 16 + (FP8 ? 0 : TM * 16)];
 };
 
-// A wavefront's operands of a step: its rows, and half of its columns at a time.
+// A wavefront's operands of a step: its rows, and a part of its columns at a time.
 template <bool FP8, int MI>
 struct Rows {
     i32x4 x[MI][FP8 ? 2 : 1];
@@ -155,9 +167,10 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     constexpr int LW = TN / 16 / NW, LA = TM / AR / NW;         // a wavefront's loads of a step
     constexpr int PW = TN / 64, PA = FP8 ? 0 : TM / 64;         // scales: 64 rows a load
     constexpr int LS = (PW + PA + NW - 1) / NW;
-    constexpr int L = LW + LA + LS;
+    constexpr int L = LW + LA;
     static_assert(LW * NW * 16 == TN && LA * NW * AR == TM && TN % 64 == 0 && TM % 64 == 0, "loads");
     __shared__ __attribute__((aligned(1024))) Stage<FP8, TM, TN> st[S];
+    __shared__ __attribute__((aligned(1024))) Scales<FP8, TM, TN> sc[2];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     const int wm = wv % WM, wn = wv / WM;
     int64_t tm, tn;
@@ -179,17 +192,20 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     for (int i = 0; i < LA; ++i)
         aat[i] = (uint32_t)min((wv + i * NW) * AR + lane / (AB / 16), last_m) * (uint32_t)arow + apiece * 16;
     int spart[LS];
+    const uint8_t *sbase[LS];
 #pragma unroll
     for (int i = 0; i < LS; ++i) {                   // (a wavefront without a part of its own repeats another's)
         spart[i] = __builtin_amdgcn_readfirstlane((wv + i * NW) % (PW + PA));
         sat[i] = spart[i] < PW ? (uint32_t)min(spart[i] * 64 + lane, last_n) * (uint32_t)per
                                : (uint32_t)min((spart[i] - PW) * 64 + lane, last_m) * (uint32_t)per;
+        sbase[i] = spart[i] < PW ? wsb : asb;
     }
     const int wv_ = __builtin_amdgcn_readfirstlane(wv);
-    auto load = [&](int k) {
+    // (whole: no k of the step lies behind the rows' end; the others get zeros there)
+    auto load = [&](int k, auto whole) {
         Stage<FP8, TM, TN> &s = st[k % S];
-        // k behind a row's end: zeros
-        const bool win = 128 * k + 32 * wpiece < p.K, ain = FP8 ? 128 * k + 16 * apiece < p.K : win;
+        const bool win = whole || 128 * k + 32 * wpiece < p.K;
+        const bool ain = whole || (FP8 ? 128 * k + 16 * apiece < p.K : win);
         const i32x4 zero = {};
 #pragma unroll
         for (int i = 0; i < LW; ++i) {
@@ -203,36 +219,50 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
             if (ain) direct16(ab + (int64_t)k * AB, aat[i], to);
             else *(i32x4 *)(to + lane * 16) = zero;
         }
+    };
+    // the scales of steps 4 b .. 4 b + 3; the last 16 bytes of a row where it ends before
+    auto scales_from = [&](int b) { return min(16 * b, max(per - 16, 0)); };
+    auto load_scales = [&](int b) {
+        uint8_t *to = sc[b & 1].s;
+        const int from = scales_from(b);
+        if (per >= 16) {
 #pragma unroll
-        for (int i = 0; i < LS; ++i) {
-            if (FP8 || spart[i] < PW) direct4(wsb + (int64_t)k * 4, sat[i], s.ws + spart[i] * 256);
-            else direct4(asb + (int64_t)k * 4, sat[i], s.as + (spart[i] - PW) * 256);
+            for (int i = 0; i < LS; ++i) direct16(sbase[i] + from, sat[i], to + spart[i] * 1024);
+        } else {
+#pragma unroll
+            for (int i = 0; i < LS; ++i)
+                for (int j = 0; j < per; j += 4)
+                    *(uint32_t *)(to + spart[i] * 1024 + lane * 16 + j) = *(const uint32_t *)(sbase[i] + sat[i] + j);
         }
     };
     // places in a stage, but for constants: like pieces of rows 16 apart are turned alike
-    const int wplace = (wn * NI * 16 + r) * 64 + (g ^ ((r >> 1) & 3)) * 16, wsplace = (wn * NI * 16 + r) * 4 + g;
+    const int wplace = (wn * NI * 16 + r) * 64 + (g ^ ((r >> 1) & 3)) * 16, wsplace = (wn * NI * 16 + r) * 16 + g;
     const int aplace = FP8 ? (wm * MI * 16 + r) * 128 + (g ^ (r & 7)) * 16 : (wm * MI * 16 + r) * 64 + (g ^ ((r >> 1) & 3)) * 16;
-    const int aplace2 = (wm * MI * 16 + r) * 128 + ((4 + g) ^ (r & 7)) * 16, asplace = (wm * MI * 16 + r) * 4 + g;
-    constexpr int NH = NI / 2;
+    const int aplace2 = (wm * MI * 16 + r) * 128 + ((4 + g) ^ (r & 7)) * 16, asplace = (TN + wm * MI * 16 + r) * 16 + g;
+    // columns are taken in parts, E4M3 rows with their wider operands in smaller ones
+    constexpr int PARTS = FP8 && NI == 8 ? 4 : 2, NH = NI / PARTS;
+    auto scales_at = [&](int k) { return sc[(k >> 2) & 1].s + (4 * k - scales_from(k >> 2)); };
     auto read_rows = [&](int k, Rows<FP8, MI> &o) {
         const Stage<FP8, TM, TN> &s = st[k % S];
+        const uint8_t *q = scales_at(k);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             o.x[i][0] = *(const i32x4 *)(s.a + aplace + i * 16 * AB);
             if constexpr (FP8) o.x[i][1] = *(const i32x4 *)(s.a + aplace2 + i * 16 * AB);
-            o.s[i] = FP8 ? 127 : s.as[asplace + i * 64];
+            o.s[i] = FP8 ? 127 : q[asplace + i * 256];
         }
     };
-    auto read_columns = [&](int k, int half, Columns<NH> &o) {
+    auto read_columns = [&](int k, int part, Columns<NH> &o) {
         const Stage<FP8, TM, TN> &s = st[k % S];
+        const uint8_t *q = scales_at(k);
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
-            o.x[i] = *(const i32x4 *)(s.w + wplace + (half * NH + i) * 1024);
-            o.s[i] = s.ws[wsplace + (half * NH + i) * 64];
+            o.x[i] = *(const i32x4 *)(s.w + wplace + (part * NH + i) * 1024);
+            o.s[i] = q[wsplace + (part * NH + i) * 256];
         }
     };
     f32x4 c[MI][NI] = {};
-    auto multiply = [&](const Rows<FP8, MI> &a, const Columns<NH> &w, int half) {
+    auto multiply = [&](const Rows<FP8, MI> &a, const Columns<NH> &w, int part) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             i32x8 x = {a.x[i][0][0], a.x[i][0][1], a.x[i][0][2], a.x[i][0][3], 0, 0, 0, 0};
@@ -242,12 +272,13 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
 #pragma unroll
             for (int j = 0; j < NH; ++j) {
                 const i32x8 y = {w.x[j][0], w.x[j][1], w.x[j][2], w.x[j][3], 0, 0, 0, 0};
-                c[i][half * NH + j] = product<FP8>(y, x, c[i][half * NH + j], w.s[j], a.s[i]);
+                c[i][part * NH + j] = product<FP8>(y, x, c[i][part * NH + j], w.s[j], a.s[i]);
             }
         }
     };
-    const int ahead = min(S, steps);
-    for (int k = 0; k < ahead; ++k) load(k);
+    const int ahead = min(S, steps), wholes = p.K / 128;
+    load_scales(0);
+    for (int k = 0; k < ahead; ++k) load(k, false);
     if (steps >= S) arrived_but<L * (S - 1)>();
     else arrived();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -255,31 +286,79 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     Columns<NH> w[2];
     read_rows(0, a[0]);
     read_columns(0, 0, w[0]);
-    auto step = [&](int k, const Rows<FP8, MI> &now, Rows<FP8, MI> &next) {
-        read_columns(k, 1, w[1]);
-        multiply(now, w[0], 0);
+    // one step: a part's products run while the next part's operands are read.  Before
+    // the last part this wavefront's reads of step k are done and its loads of step
+    // k + 1 have landed; behind the barrier that holds for all wavefronts, so step k's
+    // place takes step k + S.  Every fourth step (Q = k % 4 = 0) loads the next four's
+    // scales first, into the place of those that step k - 1 has read; the loads that
+    // may still be on their way are those of steps k + 2 .. k + S - 1, and scales that
+    // were asked for among them.
+    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+    auto step = [&](int k, auto Q, const Rows<FP8, MI> &now, Rows<FP8, MI> &next) {
+#pragma unroll
+        for (int q = 0; q < PARTS - 1; ++q) {
+            read_columns(k, q + 1, w[(q + 1) & 1]);
+            fence();
+            multiply(now, w[q & 1], q);
+            fence();
+        }
+        constexpr bool among = Q() >= 1 && Q() <= S - 2;
+        arrived_but<L * (S - 2) + (among ? LS : 0)>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (Q() == 0) load_scales((k >> 2) + 1);
+        load(k + S, std::true_type());
+        read_rows(k + 1, next);
+        read_columns(k + 1, 0, w[0]);
+        fence();
+        multiply(now, w[1], PARTS - 1);
+        fence();
+    };
+    // the steps at the end, where loads run out
+    auto last = [&](int k, const Rows<FP8, MI> &now, Rows<FP8, MI> &next) {
+#pragma unroll
+        for (int q = 0; q < PARTS - 1; ++q) {
+            read_columns(k, q + 1, w[(q + 1) & 1]);
+            multiply(now, w[q & 1], q);
+        }
         if (k + 1 < steps) {
-            // this wavefront's reads of step k are done and its loads of step k + 1 have
-            // landed; behind the barrier that holds for all of them, so step k's place
-            // takes step k + S
-            if (k + S <= steps) arrived_but<L * (S - 2)>();
+            if (S >= 4 && k + 4 <= steps) arrived_but<2 * L>();
+            else if (k + 3 <= steps) arrived_but<L>();
             else arrived();
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            if (k + S < steps) load(k + S);
+            if (k % 4 == 0 && k + 4 < steps) load_scales((k >> 2) + 1);
+            if (k + S < steps) load(k + S, false);
             read_rows(k + 1, next);
             read_columns(k + 1, 0, w[0]);
         }
-        multiply(now, w[1], 1);
+        multiply(now, w[1], PARTS - 1);
     };
-    for (int k = 0; k < steps; k += 2) {
-        step(k, a[0], a[1]);
-        if (k + 1 < steps) step(k + 1, a[1], a[0]);
+    static_assert(S == 3 || S == 4, "the waits");
+    int k = 0;
+    for (; k + 3 + S < wholes; k += 4) {
+        step(k, std::integral_constant<int, 0>(), a[0], a[1]);
+        step(k + 1, std::integral_constant<int, 1>(), a[1], a[0]);
+        step(k + 2, std::integral_constant<int, 2>(), a[0], a[1]);
+        step(k + 3, std::integral_constant<int, 3>(), a[1], a[0]);
+    }
+    for (; k < steps; k += 2) {
+        last(k, a[0], a[1]);
+        if (k + 1 < steps) last(k + 1, a[1], a[0]);
+    }
+    const int64_t m = m0 + wm * MI * 16 + r;
+    const int n = (int)n0 + wn * NI * 16 + 4 * g;
+    if (last_m == TM - 1 && last_n == TN - 1 && (p.N & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const float f = FP8 ? p.a_rows[m + 16 * i] : 1.0f;
+#pragma unroll
+            for (int j = 0; j < NI; ++j) put4<BF16>(p, (m + 16 * i) * p.N + n + 16 * j, FP8 ? c[i][j] * f : c[i][j]);
+        }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
-            put<FP8, BF16>(p, m0 + (wm * MI + i) * 16 + r, (int)n0 + (wn * NI + j) * 16 + 4 * g, c[i][j]);
+        for (int j = 0; j < NI; ++j) put<FP8, BF16>(p, m + 16 * i, n + 16 * j, c[i][j]);
 }
 
 template <bool FP8, bool BF16, int MI, int NI, int WM, int WN, int S>
@@ -294,7 +373,7 @@ template <bool FP8, bool BF16>
 hipError_t go(const MxProduct &p, hipStream_t s) {
     if (p.M <= 16) return go_few<FP8, BF16, 1>(p, s);
     if (p.M <= 64) return go_few<FP8, BF16, 4>(p, s);
-    if (p.M * p.N >= (int64_t)256 * 256 * 128) return go_tile<FP8, BF16, 4, 8, 4, 2, 3>(p, s);
+    if (p.M * p.N >= (int64_t)256 * 256 * 128) return go_tile<FP8, BF16, 4, 8, 4, 2, FP8 ? 3 : 4>(p, s);
     return go_tile<FP8, BF16, 4, 4, 2, 2, 3>(p, s);
 }
 
