@@ -17,17 +17,21 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+
+struct Words4 { uint32_t w[4]; };
 
 __device__ __forceinline__ uint16_t to_bf16(float f) {
     const __bf16 b = (__bf16)f;
     return __builtin_bit_cast(uint16_t, b);
 }
 
-template <bool FP8>
+// ws, as: the scales are byte Q of the registers
+template <bool FP8, int Q>
 __device__ __forceinline__ f32x4 product(const i32x8 &w, const i32x8 &a, f32x4 c, int ws, int as) {
     // format 4: E2M1, 0: E4M3
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, FP8 ? 0 : 4, 0, ws, 0, as);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, FP8 ? 0 : 4, Q, ws, Q, as);
 }
 
 template <bool BF16>
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(64 * W) lores_mx_few_kernel(const MxProduct p)
                 a = i32x8{x[0], x[1], x[2], x[3], 0, 0, 0, 0};
                 as = p.a_scales[ar[i] * per + blk];
             }
-            c[i] = product<FP8>(w, a, c[i], ws, as);
+            c[i] = product<FP8, 0>(w, a, c[i], ws, as);
         }
     }
 #pragma unroll
@@ -121,148 +125,181 @@ hipError_t go_few(const MxProduct &p, hipStream_t s) {
 // ------------------------------------------------------------ many rows
 //
 // A work-group has WM x WN wavefronts, each with 16 MI rows and 16 NI columns in
-// registers.  Steps of 128 k go from memory straight to LDS, S steps deep; a
-// wavefront reads the next step's operands while it multiplies this one's.
-// A 4-bit row of a step is 64 bytes: pieces of 16 bytes, whose places are turned by
-// the row so that 8 neighbouring rows read their like pieces from different banks;
-// an E4M3 row is 128 bytes of 8 pieces, turned alike.
-template <bool FP8, int TM, int TN>
-struct Stage {
-    uint8_t w[TN * 64], a[TM * (FP8 ? 128 : 64)];
-};
-// The scales of 4 steps, 16 bytes a row: the columns', the rows' behind them.  (4 bytes
-// a step and row would be as many requests to the cache as the codes are.)
-template <bool FP8, int TM, int TN>
-struct Scales {
-    uint8_t s[TN * 16 + (FP8 ? 0 : TM * 16)];
-};
-
-// A wavefront's operands of a step: its rows, and a part of its columns at a time.
-template <bool FP8, int MI>
-struct Rows {
-    i32x4 x[MI][FP8 ? 2 : 1];
-    int s[MI];
-};
-template <int NH>
-struct Columns {
-    i32x4 x[NH];
-    int s[NH];
+// registers.  Stages of 256 k go from memory straight to LDS, two stages deep:
+// 128 bytes of a 4-bit row, a whole line of the cache (64 bytes at a time, loads alone
+// took 93 instead of 67 us of 8192 x 8192 x 4096).  E4M3 rows have 128 bytes in each of
+// the stage's two steps of 128 k.  A row's 8 pieces of 16 bytes are turned by the row, so
+// that 8 neighbouring rows read their like pieces from different banks.  Scales
+// come through registers, 4 steps of a row in a thread, and are turned over in LDS so
+// that a lane has its block's of 4 steps in one register, where the instruction
+// selects one (read byte by byte from LDS they took 26 of the 65 us of all its reads).
+//
+// A work-group goes through several tiles as one stream of stages: while a tile's
+// outputs are written, the next one's first stages are on their way.
+template <bool FP8, int TM, int TN, int NW>
+struct Shared {
+    uint8_t w[2][TN * 128], a[2][FP8 ? 2 : 1][TM * 128];        // (a place's offset fits a read's own field)
+    uint32_t sc[TN + (FP8 ? 0 : TM)][4];
+    uint8_t out[NW][2048];
 };
 
-// The work-group's tile: each of the 8 XCDs (work-groups go to them in turn) takes a
+// The n-th tile of `all`: each of the 8 XCDs (work-groups go to them in turn) takes a
 // run of tiles, and a run goes over 8 rows of tiles before the next column.
-__device__ __forceinline__ void tile_of(int64_t b, int64_t tiles_m, int64_t tiles_n, int64_t &m, int64_t &n) {
-    const int64_t all = tiles_m * tiles_n, each = all / 8, more = all % 8, x = b % 8;
-    const int64_t t = x * each + (x < more ? x : more) + b / 8;
-    const int64_t band = t / (8 * tiles_n), first = band * 8;
-    const int64_t high = tiles_m - first < 8 ? tiles_m - first : 8, in = t - band * 8 * tiles_n;
-    m = first + in % high;
-    n = in / high;
+__device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t &m, uint32_t &n) {
+    asm volatile("" : "+s"(tiles_n));                // (a reciprocal kept over the loop would cost registers)
+    const uint32_t band = __builtin_amdgcn_readfirstlane(t / (8 * tiles_n)), first = band * 8, in = t - band * 8 * tiles_n;
+    const uint32_t high = min(tiles_m - first, 8u);
+    n = __builtin_amdgcn_readfirstlane(in / high);
+    m = first + in - n * high;
 }
 
-template <bool FP8, bool BF16, int MI, int NI, int WM, int WN, int S>
-__global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxProduct p) {
+// the same pointer in every lane, in scalar registers
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *q) {
+    const uint64_t x = (uint64_t)q;
+    return (const uint8_t *)(((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32) |
+                             (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x));
+}
+
+// X4: a row's scales come in whole pieces of 16 bytes (a request for 4 costs what one
+// for 16 does).  FULL: there are at least as many rows and columns as a tile has.  Then the last
+// tiles end with the last row and column, over part of their neighbours' (whose outputs
+// they write again, with the same values), and a lane's place in its rows is the same for
+// all its loads; else rows behind the end are read as the last one.
+//
+// K goes in groups of 512, two at least.  Behind a row's end its first bytes are read,
+// with scales of 0 on both sides: 36 2^-254 is below any fp32, so they add nothing (and
+// an E4M3 NaN there is the row's own).  So the loop has no branch.
+template <bool FP8, bool BF16, bool FULL, bool X4, int MI, int NI, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxProduct p, const uint32_t tiles_m, const uint32_t tiles_n) {
     constexpr int TM = 16 * MI * WM, TN = 16 * NI * WN, NW = WM * WN;
-    constexpr int AB = FP8 ? 128 : 64, AR = 1024 / AB;          // bytes of a row, rows of a load
-    constexpr int LW = TN / 16 / NW, LA = TM / AR / NW;         // a wavefront's loads of a step
-    constexpr int PW = TN / 64, PA = FP8 ? 0 : TM / 64;         // scales: 64 rows a load
-    constexpr int LS = (PW + PA + NW - 1) / NW;
-    constexpr int L = LW + LA;
-    static_assert(LW * NW * 16 == TN && LA * NW * AR == TM && TN % 64 == 0 && TM % 64 == 0, "loads");
-    __shared__ __attribute__((aligned(1024))) Stage<FP8, TM, TN> st[S];
-    __shared__ __attribute__((aligned(1024))) Scales<FP8, TM, TN> sc[2];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    constexpr int LW = TN / 8 / NW, LA = TM / 8 / NW;           // a wavefront's loads of 8 rows
+    constexpr int SR = TN + (FP8 ? 0 : TM);                     // rows of scales: the columns', the rows'
+    constexpr int PARTS = NI == 8 ? 4 : 2, NH = NI / PARTS;     // columns are taken in parts
+    static_assert(LW * NW * 8 == TN && LA * NW * 8 == TM && SR <= 64 * NW, "every load and scale has its lane");
+    static_assert(TN % 64 == 0, "a wavefront has scales of rows or of columns");
+    __shared__ __attribute__((aligned(1024))) Shared<FP8, TM, TN, NW> sh;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int wm = wv % WM, wn = wv / WM;
-    int64_t tm, tn;
-    tile_of(block_at(blockIdx.x, blockIdx.y), (p.M + TM - 1) / TM, (p.N + TN - 1) / TN, tm, tn);
-    const int64_t m0 = tm * TM, n0 = tn * TN;
-    if (m0 >= p.M || n0 >= p.N) return;
-    const int steps = (p.K + 127) / 128, per = mx_scale_stride(p.K);
-    const int64_t wrow = p.K / 2, arow = FP8 ? p.K : p.K / 2;
-    const int last_m = (int)min(p.M - 1 - m0, (int64_t)TM - 1), last_n = (int)min(p.N - 1 - n0, (int64_t)TN - 1);
-    const uint8_t *wb = p.w + n0 * wrow, *ab = p.a + m0 * arow;
-    const uint8_t *wsb = p.w_scales + n0 * per, *asb = FP8 ? nullptr : p.a_scales + m0 * per;
-    // a lane's piece of its row, the same in all its loads; rows behind the end are the last one
-    const int wpiece = (lane & 3) ^ ((lane >> 3) & 3), apiece = FP8 ? (lane & 7) ^ ((lane >> 3) & 7) : wpiece;
-    uint32_t wat[LW], aat[LA], sat[LS];
-#pragma unroll
-    for (int i = 0; i < LW; ++i)
-        wat[i] = (uint32_t)min((wv + i * NW) * 16 + (lane >> 2), last_n) * (uint32_t)wrow + wpiece * 16;
-#pragma unroll
-    for (int i = 0; i < LA; ++i)
-        aat[i] = (uint32_t)min((wv + i * NW) * AR + lane / (AB / 16), last_m) * (uint32_t)arow + apiece * 16;
-    int spart[LS];
-    const uint8_t *sbase[LS];
-#pragma unroll
-    for (int i = 0; i < LS; ++i) {                   // (a wavefront without a part of its own repeats another's)
-        spart[i] = __builtin_amdgcn_readfirstlane((wv + i * NW) % (PW + PA));
-        sat[i] = spart[i] < PW ? (uint32_t)min(spart[i] * 64 + lane, last_n) * (uint32_t)per
-                               : (uint32_t)min((spart[i] - PW) * 64 + lane, last_m) * (uint32_t)per;
-        sbase[i] = spart[i] < PW ? wsb : asb;
-    }
-    const int wv_ = __builtin_amdgcn_readfirstlane(wv);
-    // (whole: no k of the step lies behind the rows' end; the others get zeros there)
-    auto load = [&](int k, auto whole) {
-        Stage<FP8, TM, TN> &s = st[k % S];
-        const bool win = whole || 128 * k + 32 * wpiece < p.K;
-        const bool ain = whole || (FP8 ? 128 * k + 16 * apiece < p.K : win);
-        const i32x4 zero = {};
-#pragma unroll
-        for (int i = 0; i < LW; ++i) {
-            uint8_t *to = s.w + (wv_ + i * NW) * 1024;
-            if (win) direct16(wb + (int64_t)k * 64, wat[i], to);
-            else *(i32x4 *)(to + lane * 16) = zero;
+    // this work-group's tiles: of its XCD's run, every one that lies a round further
+    const uint32_t all = tiles_m * tiles_n, x8 = blockIdx.x % 8, each = all / 8, more = all % 8;
+    const uint32_t run = x8 * each + min(x8, more), run_end = run + each + (x8 < more), round = gridDim.x / 8;
+    uint32_t tile = run + blockIdx.x / 8;
+    if (tile >= run_end) return;
+    const int groups = max((p.K + 511) / 512, 2), per = mx_scale_stride(p.K);
+    const uint32_t wrow = p.K / 2, arow = FP8 ? p.K : p.K / 2;
+    const int piece = (lane & 7) ^ (lane >> 3);      // a lane's of its row, the same in all its loads
+
+    // ---- where a tile's operands lie; the tile that is multiplied and the next one
+    const int srow = SR == 64 * NW ? threadIdx.x : min((int)threadIdx.x, SR - 1);
+    const bool of_w = FP8 || wv < TN / 64;
+    struct Aim {
+        int64_t m0;
+        int n0;
+        const uint8_t *w, *a, *s;                    // FULL: the wavefront's rows, else the tile's; scales
+        uint32_t wat[FULL ? 1 : LW], aat[FULL ? 1 : LA], sat;
+    };
+    auto aim = [&](uint32_t t, Aim &x) {
+        uint32_t tm, tn;
+        tile_of(t, tiles_m, tiles_n, tm, tn);
+        x.m0 = (int64_t)tm * TM;
+        int64_t n0 = (int64_t)tn * TN;
+        if constexpr (FULL) {
+            x.m0 = min(x.m0, p.M - TM);
+            n0 = min(n0, (int64_t)p.N - TN);
         }
+        x.n0 = (int)n0;
+        x.w = uniform(p.w + (n0 + (FULL ? wv * 8 : 0)) * wrow);
+        x.a = uniform(p.a + (x.m0 + (FULL ? wv * 8 : 0)) * arow);
+        x.s = uniform(of_w ? p.w_scales + n0 * per : p.a_scales + x.m0 * per);
+        x.sat = srow - (of_w ? 0 : TN);
+        if constexpr (FULL) {
+            x.wat[0] = (lane >> 3) * wrow;
+            x.aat[0] = (lane >> 3) * arow;
+        } else {                                     // (a lane's offset is unsigned: from the tile's first row)
+            const uint32_t last_m = (uint32_t)min(p.M - 1 - x.m0, (int64_t)TM - 1), last_n = (uint32_t)min(p.N - 1 - n0, (int64_t)TN - 1);
 #pragma unroll
-        for (int i = 0; i < LA; ++i) {
-            uint8_t *to = s.a + (wv_ + i * NW) * 1024;
-            if (ain) direct16(ab + (int64_t)k * AB, aat[i], to);
-            else *(i32x4 *)(to + lane * 16) = zero;
+            for (int i = 0; i < LW; ++i) x.wat[i] = min((uint32_t)((wv + i * NW) * 8 + (lane >> 3)), last_n) * wrow;
+#pragma unroll
+            for (int i = 0; i < LA; ++i) x.aat[i] = min((uint32_t)((wv + i * NW) * 8 + (lane >> 3)), last_m) * arow;
+            x.sat = min(x.sat, of_w ? last_n : last_m);
+        }
+        x.sat *= per;
+    };
+    Aim now, then;
+    // stage j of a tile into place j & 1
+    auto load = [&](int j, const Aim &x) {
+        uint8_t *const tw = sh.w[j & 1], *const ta = sh.a[j & 1][0];
+        const uint32_t kw = 256 * j + 32 * piece < p.K ? j * 128 + piece * 16 : 0;
+#pragma unroll
+        for (int i = 0; i < LW; ++i)
+            direct16(uniform(x.w + (FULL ? (int64_t)(i * NW * 8) * wrow : 0)), x.wat[FULL ? 0 : i] + kw, tw + (wv + i * NW) * 1024);
+#pragma unroll
+        for (int h = 0; h < (FP8 ? 2 : 1); ++h) {
+            const uint32_t ka = !FP8 ? kw : 256 * j + 128 * h + 16 * piece < p.K ? 256 * j + 128 * h + 16 * piece : 0;
+#pragma unroll
+            for (int i = 0; i < LA; ++i)
+                direct16(uniform(x.a + (FULL ? (int64_t)(i * NW * 8) * arow : 0)), x.aat[FULL ? 0 : i] + ka,
+                         ta + (h * TM / 8 + wv + i * NW) * 1024);
         }
     };
-    // the scales of steps 4 b .. 4 b + 3; the last 16 bytes of a row where it ends before
-    auto scales_from = [&](int b) { return min(16 * b, max(per - 16, 0)); };
-    auto load_scales = [&](int b) {
-        uint8_t *to = sc[b & 1].s;
-        const int from = scales_from(b);
-        if (per >= 16) {
+    // a row's scales in a thread: steps 4 b .. 4 b + 3, 0 behind the row's end
+    uint32_t sq[4];
+    auto fetch_scales = [&](int b, const Aim &x) {
+        if constexpr (X4) {
+            const uint32_t in = 0u - (uint32_t)(16 * b < per);
+            const Words4 v = *(const Words4 *)(x.s + (16 * b & in) + x.sat);
 #pragma unroll
-            for (int i = 0; i < LS; ++i) direct16(sbase[i] + from, sat[i], to + spart[i] * 1024);
+            for (int i = 0; i < 4; ++i) sq[i] = v.w[i] & in;
         } else {
 #pragma unroll
-            for (int i = 0; i < LS; ++i)
-                for (int j = 0; j < per; j += 4)
-                    *(uint32_t *)(to + spart[i] * 1024 + lane * 16 + j) = *(const uint32_t *)(sbase[i] + sat[i] + j);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t in = 0u - (uint32_t)(16 * b + 4 * i < per);
+                sq[i] = *(const uint32_t *)(x.s + ((16 * b + 4 * i) & in) + x.sat) & in;
+            }
         }
     };
+    // byte s of word g is the scale of block g of step s
+    auto turn_scales = [&] {
+        const uint32_t lo0 = __builtin_amdgcn_perm(sq[1], sq[0], 0x05010400u), hi0 = __builtin_amdgcn_perm(sq[1], sq[0], 0x07030602u);
+        const uint32_t lo1 = __builtin_amdgcn_perm(sq[3], sq[2], 0x05010400u), hi1 = __builtin_amdgcn_perm(sq[3], sq[2], 0x07030602u);
+        const u32x4 t = {__builtin_amdgcn_perm(lo1, lo0, 0x05040100u), __builtin_amdgcn_perm(lo1, lo0, 0x07060302u),
+                         __builtin_amdgcn_perm(hi1, hi0, 0x05040100u), __builtin_amdgcn_perm(hi1, hi0, 0x07060302u)};
+        if (SR == 64 * NW || (int)threadIdx.x < SR) *(u32x4 *)sh.sc[srow] = t;
+    };
+    int rs[MI], cs[NI];
+    auto read_row_scales = [&](int (&x)[MI], int b) {
+        // E4M3: 1, but 0 behind K (byte s: block 16 b + 4 s + g)
+        const int left = p.K / 32 - 16 * b - g;
+        const int one = left > 12 ? 0x7f7f7f7f : left > 8 ? 0x7f7f7f : left > 4 ? 0x7f7f : left > 0 ? 0x7f : 0;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) x[i] = FP8 ? one : sh.sc[(FP8 ? 0 : TN) + (wm * MI + i) * 16 + r][g];
+    };
+    auto read_column_scales = [&](int part) {
+#pragma unroll
+        for (int i = part * NH; i < (part + 1) * NH; ++i) cs[i] = sh.sc[(wn * NI + i) * 16 + r][g];
+    };
+
+    // ---- operands: a wavefront's rows of a step, and a part of its columns at a time
+    struct Rows { i32x4 x[MI][FP8 ? 2 : 1]; };
+    struct Columns { i32x4 x[NH]; };
     // places in a stage, but for constants: like pieces of rows 16 apart are turned alike
-    const int wplace = (wn * NI * 16 + r) * 64 + (g ^ ((r >> 1) & 3)) * 16, wsplace = (wn * NI * 16 + r) * 16 + g;
-    const int aplace = FP8 ? (wm * MI * 16 + r) * 128 + (g ^ (r & 7)) * 16 : (wm * MI * 16 + r) * 64 + (g ^ ((r >> 1) & 3)) * 16;
-    const int aplace2 = (wm * MI * 16 + r) * 128 + ((4 + g) ^ (r & 7)) * 16, asplace = (TN + wm * MI * 16 + r) * 16 + g;
-    // columns are taken in parts, E4M3 rows with their wider operands in smaller ones
-    constexpr int PARTS = FP8 && NI == 8 ? 4 : 2, NH = NI / PARTS;
-    auto scales_at = [&](int k) { return sc[(k >> 2) & 1].s + (4 * k - scales_from(k >> 2)); };
-    auto read_rows = [&](int k, Rows<FP8, MI> &o) {
-        const Stage<FP8, TM, TN> &s = st[k % S];
-        const uint8_t *q = scales_at(k);
+    const int turn = r & 7, wplace = (wn * NI * 16 + r) * 128, aplace = (wm * MI * 16 + r) * 128;
+    auto read_rows = [&](auto Q, Rows &o) {          // of step Q of 4
+        const uint8_t *a = sh.a[Q() >> 1][FP8 ? Q() & 1 : 0] + aplace;
+        const int at = FP8 ? g : 4 * (Q() & 1) + g;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            o.x[i][0] = *(const i32x4 *)(s.a + aplace + i * 16 * AB);
-            if constexpr (FP8) o.x[i][1] = *(const i32x4 *)(s.a + aplace2 + i * 16 * AB);
-            o.s[i] = FP8 ? 127 : q[asplace + i * 256];
+            o.x[i][0] = *(const i32x4 *)(a + (at ^ turn) * 16 + i * 2048);
+            if constexpr (FP8) o.x[i][1] = *(const i32x4 *)(a + ((4 + g) ^ turn) * 16 + i * 2048);
         }
     };
-    auto read_columns = [&](int k, int part, Columns<NH> &o) {
-        const Stage<FP8, TM, TN> &s = st[k % S];
-        const uint8_t *q = scales_at(k);
+    auto read_columns = [&](auto Q, int part, Columns &o) {
+        const uint8_t *w = sh.w[Q() >> 1] + wplace + ((4 * (Q() & 1) + g) ^ turn) * 16;
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
-            o.x[i] = *(const i32x4 *)(s.w + wplace + (part * NH + i) * 1024);
-            o.s[i] = q[wsplace + (part * NH + i) * 256];
-        }
+        for (int i = 0; i < NH; ++i) o.x[i] = *(const i32x4 *)(w + (part * NH + i) * 2048);
     };
-    f32x4 c[MI][NI] = {};
-    auto multiply = [&](const Rows<FP8, MI> &a, const Columns<NH> &w, int part) {
+    f32x4 c[MI][NI];
+    auto multiply = [&](auto Q, const Rows &a, const Columns &w, int part) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             i32x8 x = {a.x[i][0][0], a.x[i][0][1], a.x[i][0][2], a.x[i][0][3], 0, 0, 0, 0};
@@ -272,109 +309,153 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
 #pragma unroll
             for (int j = 0; j < NH; ++j) {
                 const i32x8 y = {w.x[j][0], w.x[j][1], w.x[j][2], w.x[j][3], 0, 0, 0, 0};
-                c[i][part * NH + j] = product<FP8>(y, x, c[i][part * NH + j], w.s[j], a.s[i]);
+                c[i][part * NH + j] = product<FP8, Q()>(y, x, c[i][part * NH + j], cs[part * NH + j], rs[i]);
             }
         }
     };
-    const int ahead = min(S, steps), wholes = p.K / 128;
-    load_scales(0);
-    for (int k = 0; k < ahead; ++k) load(k, false);
-    if (steps >= S) arrived_but<L * (S - 1)>();
-    else arrived();
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    Rows<FP8, MI> a[2];
-    Columns<NH> w[2];
-    read_rows(0, a[0]);
-    read_columns(0, 0, w[0]);
-    // one step: a part's products run while the next part's operands are read.  Before
-    // the last part this wavefront's reads of step k are done and its loads of step
-    // k + 1 have landed; behind the barrier that holds for all wavefronts, so step k's
-    // place takes step k + S.  Every fourth step (Q = k % 4 = 0) loads the next four's
-    // scales first, into the place of those that step k - 1 has read; the loads that
-    // may still be on their way are those of steps k + 2 .. k + S - 1, and scales that
-    // were asked for among them.
     auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
-    auto step = [&](int k, auto Q, const Rows<FP8, MI> &now, Rows<FP8, MI> &next) {
-#pragma unroll
-        for (int q = 0; q < PARTS - 1; ++q) {
-            read_columns(k, q + 1, w[(q + 1) & 1]);
-            fence();
-            multiply(now, w[q & 1], q);
-            fence();
-        }
-        constexpr bool among = Q() >= 1 && Q() <= S - 2;
-        arrived_but<L * (S - 2) + (among ? LS : 0)>();
+    // the end of a stage: this wavefront's reads of it are done and its loads of the next
+    // one have landed; behind the barrier that holds for all wavefronts
+    auto meet = [] {
+        arrived();
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (Q() == 0) load_scales((k >> 2) + 1);
-        load(k + S, std::true_type());
-        read_rows(k + 1, next);
-        read_columns(k + 1, 0, w[0]);
-        fence();
-        multiply(now, w[1], PARTS - 1);
-        fence();
     };
-    // the steps at the end, where loads run out
-    auto last = [&](int k, const Rows<FP8, MI> &now, Rows<FP8, MI> &next) {
+    Rows a[2];
+    Columns w[2];
+    // step Q of 4: a part's products run while the next part's operands are read.  Every
+    // second step ends a stage, whose place takes the stage after the next one of the
+    // stream.  Scales of the next four steps: turned over into LDS at Q = 1, where those
+    // of these four have been read; read, and the following ones asked for, at Q = 3.
+    auto step = [&](auto Q, int b, const Rows &cur, Rows &next) {
+        constexpr std::integral_constant<int, (Q() + 1) & 3> N{};
+        int nr[MI];
 #pragma unroll
         for (int q = 0; q < PARTS - 1; ++q) {
-            read_columns(k, q + 1, w[(q + 1) & 1]);
-            multiply(now, w[q & 1], q);
+            read_columns(Q, q + 1, w[(q + 1) & 1]);
+            fence();
+            multiply(Q, cur, w[q & 1], q);
+            fence();
         }
-        if (k + 1 < steps) {
-            if (S >= 4 && k + 4 <= steps) arrived_but<2 * L>();
-            else if (k + 3 <= steps) arrived_but<L>();
-            else arrived();
-            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            if (k % 4 == 0 && k + 4 < steps) load_scales((k >> 2) + 1);
-            if (k + S < steps) load(k + S, false);
-            read_rows(k + 1, next);
-            read_columns(k + 1, 0, w[0]);
+        if constexpr ((Q() & 1) != 0) {
+            meet();
+            const int j = 2 * b + (Q() >> 1) + 2;
+            load(j < 2 * groups ? j : j - 2 * groups, j < 2 * groups ? now : then);
+            if constexpr (Q() == 1) turn_scales();
+            if constexpr (Q() == 3) {
+                read_row_scales(nr, b + 1 < groups ? b + 1 : 0);
+#pragma unroll
+                for (int q = 0; q < PARTS - 1; ++q) read_column_scales(q);
+            }
         }
-        multiply(now, w[1], PARTS - 1);
+        read_rows(N, next);
+        read_columns(N, 0, w[0]);
+        if constexpr (Q() == 3) fetch_scales(b + 2 < groups ? b + 2 : b + 2 - groups, b + 2 < groups ? now : then);
+        fence();
+        multiply(Q, cur, w[1], PARTS - 1);
+        fence();
+        if constexpr (Q() == 3) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) rs[i] = nr[i];
+            read_column_scales(PARTS - 1);           // (their first use is some parts away)
+        }
     };
-    static_assert(S == 3 || S == 4, "the waits");
-    int k = 0;
-    for (; k + 3 + S < wholes; k += 4) {
-        step(k, std::integral_constant<int, 0>(), a[0], a[1]);
-        step(k + 1, std::integral_constant<int, 1>(), a[1], a[0]);
-        step(k + 2, std::integral_constant<int, 2>(), a[0], a[1]);
-        step(k + 3, std::integral_constant<int, 3>(), a[1], a[0]);
-    }
-    for (; k < steps; k += 2) {
-        last(k, a[0], a[1]);
-        if (k + 1 < steps) last(k + 1, a[1], a[0]);
-    }
-    const int64_t m = m0 + wm * MI * 16 + r;
-    const int n = (int)n0 + wn * NI * 16 + 4 * g;
-    if (last_m == TM - 1 && last_n == TN - 1 && (p.N & 3) == 0) {
+
+    aim(tile, now);
+    fetch_scales(0, now);
+    load(0, now);
+    arrived();
+    turn_scales();
+    load(1, now);
+    fetch_scales(1, now);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    read_row_scales(rs, 0);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const float f = FP8 ? p.a_rows[m + 16 * i] : 1.0f;
+    for (int q = 0; q < PARTS; ++q) read_column_scales(q);
+    read_rows(std::integral_constant<int, 0>(), a[0]);
+    read_columns(std::integral_constant<int, 0>(), 0, w[0]);
+    for (; tile < run_end; tile += round) {
+        aim(tile + round < run_end ? tile + round : tile, then);     // (behind the last one: itself, loaded in vain)
 #pragma unroll
-            for (int j = 0; j < NI; ++j) put4<BF16>(p, (m + 16 * i) * p.N + n + 16 * j, FP8 ? c[i][j] * f : c[i][j]);
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) c[i][j] = f32x4{};
+        for (int b = 0; b < groups; ++b) {           // (behind K: zeros)
+            step(std::integral_constant<int, 0>(), b, a[0], a[1]);
+            step(std::integral_constant<int, 1>(), b, a[1], a[0]);
+            step(std::integral_constant<int, 2>(), b, a[0], a[1]);
+            step(std::integral_constant<int, 3>(), b, a[1], a[0]);
         }
-        return;
+        const int64_t m = now.m0 + wm * MI * 16;
+        const int n = now.n0 + wn * NI * 16;
+        // outputs in pieces of 16 bytes, if rows of them are whole: 16 rows of 128 bytes at a
+        // time through the wavefront's own place in LDS, so that lines are written whole
+        // (stored as they stand in the registers they took 45 us of 183)
+        constexpr int E = BF16 ? 8 : 4, FR = BF16 ? 4 : 2;       // outputs of a piece, tiles of 16 columns
+        // (what follows from the lane is made anew: kept over the loop it would cost registers)
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        const int lr = l & 15, lg = l >> 4, row = l >> 3, ch = l & 7;
+        if (p.N % E == 0) {
+            uint8_t *own = sh.out[wv];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const float f = FP8 ? p.a_rows[min(m + lr + 16 * i, p.M - 1)] : 1.0f;
+#pragma unroll
+                for (int h = 0; h < NI; h += FR) {
+#pragma unroll
+                    for (int j = 0; j < FR; ++j) {
+                        const f32x4 x = FP8 ? c[i][h + j] * f : c[i][h + j];
+                        if constexpr (BF16)
+                            *(u16x4 *)(own + (lr * 8 + ((2 * j + (lg >> 1)) ^ (lr & 7))) * 16 + (lg & 1) * 8) =
+                                u16x4{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
+                        else
+                            *(f32x4 *)(own + (lr * 8 + ((4 * j + lg) ^ (lr & 7))) * 16) = x;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const u32x4 x = *(const u32x4 *)(own + ((q * 8 + row) * 8 + (ch ^ row)) * 16);
+                        const int64_t mm = m + 16 * i + q * 8 + row;
+                        const int nn = n + 16 * h + ch * E;
+                        if (FULL || (mm < p.M && nn < p.N)) *(u32x4 *)((uint8_t *)p.out + (mm * p.N + nn) * (16 / E)) = x;
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) put<FP8, BF16>(p, m + lr + 16 * i, n + 16 * j + 4 * lg, c[i][j]);
+        }
+        now = then;
     }
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j) put<FP8, BF16>(p, m + 16 * i, n + 16 * j, c[i][j]);
+    arrived();                                       // nothing may land in LDS that is another's
 }
 
-template <bool FP8, bool BF16, int MI, int NI, int WM, int WN, int S>
-hipError_t go_tile(const MxProduct &p, hipStream_t s) {
+// `residents`: work-groups that run at once, a multiple of 8
+template <bool FP8, bool BF16, bool FULL, bool X4, int MI, int NI, int WM, int WN>
+hipError_t go_tile(const MxProduct &p, int residents, hipStream_t s) {
     constexpr int TM = 16 * MI * WM, TN = 16 * NI * WN;
-    const int64_t groups = (p.M + TM - 1) / TM * ((p.N + TN - 1) / TN);
-    lores_mx_tile_kernel<FP8, BF16, MI, NI, WM, WN, S><<<grid_of(groups), 64 * WM * WN, 0, s>>>(p);
+    const int64_t tm = (p.M + TM - 1) / TM, tn = (p.N + TN - 1) / TN;
+    const int64_t groups = (tm * tn + 7) / 8 * 8;
+    lores_mx_tile_kernel<FP8, BF16, FULL, X4, MI, NI, WM, WN><<<dim3((uint32_t)(groups < residents ? groups : residents)), 64 * WM * WN, 0, s>>>(
+        p, (uint32_t)tm, (uint32_t)tn);
     return hipGetLastError();
+}
+
+template <bool FP8, bool BF16, bool X4>
+hipError_t go_tiles(const MxProduct &p, hipStream_t s) {
+    if (p.M >= 256 && p.N >= 256 && p.M * p.N >= (int64_t)256 * 256 * 128) {
+        if constexpr (FP8) return go_tile<FP8, BF16, true, X4, 4, 4, 2, 4>(p, 256, s);
+        else return go_tile<FP8, BF16, true, X4, 4, 8, 4, 2>(p, 256, s);
+    }
+    return go_tile<FP8, BF16, false, X4, 4, 4, 2, 2>(p, FP8 ? 256 : 512, s);
 }
 
 template <bool FP8, bool BF16>
 hipError_t go(const MxProduct &p, hipStream_t s) {
     if (p.M <= 16) return go_few<FP8, BF16, 1>(p, s);
     if (p.M <= 64) return go_few<FP8, BF16, 4>(p, s);
-    if (p.M * p.N >= (int64_t)256 * 256 * 128) return go_tile<FP8, BF16, 4, 8, 4, 2, FP8 ? 3 : 4>(p, s);
-    return go_tile<FP8, BF16, 4, 4, 2, 2, 3>(p, s);
+    return mx_scale_stride(p.K) % 16 == 0 ? go_tiles<FP8, BF16, true>(p, s) : go_tiles<FP8, BF16, false>(p, s);
 }
 
 }  // namespace

@@ -115,7 +115,8 @@ def test_product(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(512, 512, 512), (700, 1000, 1056), (1025, 777, 288), (256, 4096, 256),
-                                   (4096, 256, 1024), (2048, 2304, 2080), (40, 3000, 8192)])
+                                   (4096, 256, 1024), (2048, 2304, 2080), (40, 3000, 8192), (3001, 4100, 544),
+                                   (5000, 2200, 416), (2304, 5000, 384), (12000, 1000, 1536)])
 def test_larger_products(M, N, K):
     w, ws, wv = mx((N, K), 4)
     a, as_, av = mx((M, K), 5)
@@ -140,6 +141,21 @@ def test_one_product_at_a_time():
     e, r = a.to(torch.float8_e4m3fn), torch.ones(K, device=dev())
     got = lores.lores_mx_matmul(e, r, wc, ws)
     assert torch.equal(got, torch.from_numpy(a.double().cpu().numpy() @ wv.T).to(BF16).to(dev()))
+
+
+@pytest.mark.parametrize("M,N", [(5, 40), (100, 200), (3000, 3400)])
+@pytest.mark.parametrize("K", [32, 96, 416, 544, 1056])
+def test_nothing_is_added_behind_a_row(M, N, K):
+    """Zeros times anything: every output is 0, whatever the lanes behind a row's end hold."""
+    w, ws, _ = mx((N, K), 16)
+    a, as_ = lores.lores_mx_quant(torch.zeros(M, K, device=dev()))
+    for prec in (lores.LORES_BF16, lores.LORES_FP32):
+        assert (lores.lores_mx_matmul(a, as_, w, ws, out_prec=prec) == 0).all()
+    x = torch.zeros(M, K, device=dev())
+    x[:, 0] = 448.0                                  # the row's first values are what such lanes read
+    w[:, 0] &= 0xf0                                  # and their partners here are 0
+    out = lores.lores_mx_matmul(x.to(torch.float8_e4m3fn), torch.ones(M, device=dev()), w, ws)
+    assert (out == 0).all()
 
 
 @pytest.mark.parametrize("M", [3, 200])
