@@ -20,7 +20,9 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 
-struct Words4 { uint32_t w[4]; };
+typedef uint32_t Words4 __attribute__((ext_vector_type(4), aligned(4)));
+// (a pointer put together from scalar registers is not known to be one to memory)
+template <typename T> using Global = __attribute__((address_space(1))) T;
 
 __device__ __forceinline__ uint16_t to_bf16(float f) {
     const __bf16 b = (__bf16)f;
@@ -166,7 +168,7 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *q) {
 // they write again, with the same values), and a lane's place in its rows is the same for
 // all its loads; else rows behind the end are read as the last one.
 //
-// K goes in groups of 512, two at least.  Behind a row's end its first bytes are read,
+// K goes in groups of 512.  Behind a row's end its first bytes are read,
 // with scales of 0 on both sides: 36 2^-254 is below any fp32, so they add nothing (and
 // an E4M3 NaN there is the row's own).  So the loop has no branch.
 template <bool FP8, bool BF16, bool FULL, bool X4, int MI, int NI, int WM, int WN>
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     const uint32_t run = x8 * each + min(x8, more), run_end = run + each + (x8 < more), round = gridDim.x / 8;
     uint32_t tile = run + blockIdx.x / 8;
     if (tile >= run_end) return;
-    const int groups = max((p.K + 511) / 512, 2), per = mx_scale_stride(p.K);
+    const int groups = (p.K + 511) / 512, per = mx_scale_stride(p.K);
     const uint32_t wrow = p.K / 2, arow = FP8 ? p.K : p.K / 2;
     const int piece = (lane & 7) ^ (lane >> 3);      // a lane's of its row, the same in all its loads
 
@@ -242,24 +244,27 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
                          ta + (h * TM / 8 + wv + i * NW) * 1024);
         }
     };
-    // a row's scales in a thread: steps 4 b .. 4 b + 3, 0 behind the row's end
-    uint32_t sq[4];
+    // a row's scales in a thread: steps 4 b .. 4 b + 3 (those behind the row's end are
+    // made 0 where they are used: used here they would be waited for)
+    uint32_t sq[4], sin[4];
     auto fetch_scales = [&](int b, const Aim &x) {
         if constexpr (X4) {
-            const uint32_t in = 0u - (uint32_t)(16 * b < per);
-            const Words4 v = *(const Words4 *)(x.s + (16 * b & in) + x.sat);
+            sin[0] = sin[1] = sin[2] = sin[3] = 0u - (uint32_t)(16 * b < per);
+            const Words4 v = *(const Global<Words4> *)(x.s + (16 * b & sin[0]) + x.sat);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sq[i] = v.w[i] & in;
+            for (int i = 0; i < 4; ++i) sq[i] = v[i];
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t in = 0u - (uint32_t)(16 * b + 4 * i < per);
-                sq[i] = *(const uint32_t *)(x.s + ((16 * b + 4 * i) & in) + x.sat) & in;
+                sin[i] = 0u - (uint32_t)(16 * b + 4 * i < per);
+                sq[i] = *(const Global<uint32_t> *)(x.s + ((16 * b + 4 * i) & sin[i]) + x.sat);
             }
         }
     };
     // byte s of word g is the scale of block g of step s
     auto turn_scales = [&] {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sq[i] &= sin[i];
         const uint32_t lo0 = __builtin_amdgcn_perm(sq[1], sq[0], 0x05010400u), hi0 = __builtin_amdgcn_perm(sq[1], sq[0], 0x07030602u);
         const uint32_t lo1 = __builtin_amdgcn_perm(sq[3], sq[2], 0x05010400u), hi1 = __builtin_amdgcn_perm(sq[3], sq[2], 0x07030602u);
         const u32x4 t = {__builtin_amdgcn_perm(lo1, lo0, 0x05040100u), __builtin_amdgcn_perm(lo1, lo0, 0x07060302u),
@@ -324,11 +329,13 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     Columns w[2];
     // step Q of 4: a part's products run while the next part's operands are read.  Every
     // second step ends a stage, whose place takes the stage after the next one of the
-    // stream.  Scales of the next four steps: turned over into LDS at Q = 1, where those
-    // of these four have been read; read, and the following ones asked for, at Q = 3.
+    // stream.  Scales of the next four steps: asked for at Q = 0 (in the same turn of the
+    // loop as their use: carried over its end they are copied, and waited for), turned
+    // over into LDS at Q = 1, where those of these four have been read, and read at Q = 3.
     auto step = [&](auto Q, int b, const Rows &cur, Rows &next) {
         constexpr std::integral_constant<int, (Q() + 1) & 3> N{};
         int nr[MI];
+        if constexpr (Q() == 0) fetch_scales(b + 1 < groups ? b + 1 : 0, b + 1 < groups ? now : then);
 #pragma unroll
         for (int q = 0; q < PARTS - 1; ++q) {
             read_columns(Q, q + 1, w[(q + 1) & 1]);
@@ -349,7 +356,6 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
         }
         read_rows(N, next);
         read_columns(N, 0, w[0]);
-        if constexpr (Q() == 3) fetch_scales(b + 2 < groups ? b + 2 : b + 2 - groups, b + 2 < groups ? now : then);
         fence();
         multiply(Q, cur, w[1], PARTS - 1);
         fence();
@@ -366,7 +372,6 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     arrived();
     turn_scales();
     load(1, now);
-    fetch_scales(1, now);
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     read_row_scales(rs, 0);
 #pragma unroll
