@@ -60,67 +60,119 @@ __device__ __forceinline__ void put(const MxProduct &p, int64_t m, int j, f32x4 
         }
 }
 
-// Few rows: a work-group has 16 columns and 16 MT rows, its wavefronts share k.
-template <bool FP8, bool BF16, int MT, int W>
+// ------------------------------------------------------------ few rows
+//
+// Bound by latency and the weights' way from memory.  A work-group has 16 NT columns and
+// 16 MT rows; its wavefronts share k, U steps of 128 at a time, and everything a
+// wavefront reads for them is on its way at once: of a row 64 U neighbouring bytes of codes
+// and 4 U of scales (a request for 4 bytes of scales costs what one for 16 does: 64 rows of
+// 8192 x 4096 took 20 us with single ones and 10 with four).  Behind K the row's first
+// bytes are read, with scales of 0 on both sides: 448 6 2^-254 is below any fp32.
+template <bool FP8, bool BF16, int MT, int NT, int U, int W>
 __global__ void __launch_bounds__(64 * W) lores_mx_few_kernel(const MxProduct p) {
-    __shared__ f32x4 sm[W][MT][64];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int tiles = (p.N + 15) / 16;
-    const int64_t b = block_at(blockIdx.x, blockIdx.y), mb = b / tiles;
-    const int j0 = (int)(b - mb * tiles) * 16;
-    const int64_t m0 = mb * (16 * MT);
-    if (m0 >= p.M) return;
-    const int blocks = p.K / 32, per = mx_scale_stride(p.K), steps = (p.K + 127) / 128;
-    const int64_t wr = min(j0 + r, p.N - 1);
-    const uint8_t *wc = p.w + wr * (p.K / 2), *wsc = p.w_scales + wr * per;
-    int64_t ar[MT];
+    typedef uint32_t Scales __attribute__((ext_vector_type(U), aligned(4)));
+    __shared__ f32x4 sm[W][MT * NT][64];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const int j0 = blockIdx.x * (16 * NT);
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+    const uint32_t blocks = p.K / 32, per = mx_scale_stride(p.K), wrow = p.K / 2, arow = FP8 ? p.K : p.K / 2;
+    const int steps = (p.K + 127) / 128;
+    // 32-bit places from the tile's first rows; rows behind the end are the last one
+    const uint8_t *wb = p.w + (int64_t)j0 * wrow, *wsb = p.w_scales + (int64_t)j0 * per;
+    const uint8_t *ab = p.a + m0 * arow, *asb = p.a_scales + m0 * per;
+    const uint32_t last_n = p.N - 1 - j0, last_m = (uint32_t)min(p.M - 1 - m0, (int64_t)(16 * MT - 1));
+    uint32_t wr[NT], ar[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) ar[i] = min(m0 + 16 * i + r, p.M - 1);
-    f32x4 c[MT] = {};
-    for (int k = wv; k < steps; k += W) {
-        const int blk = 4 * k + g;
-        const bool in = blk < blocks;
-        i32x8 w = {};
-        int ws = 0;
-        if (in) {
-            const i32x4 x = *(const i32x4 *)(wc + blk * 16);
-            w = i32x8{x[0], x[1], x[2], x[3], 0, 0, 0, 0};
-            ws = wsc[blk];
+    for (int j = 0; j < NT; ++j) wr[j] = min((uint32_t)(16 * j + r), last_n);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ar[i] = min((uint32_t)(16 * i + r), last_m);
+    f32x4 c[MT][NT] = {};
+    for (int k = wv * U; k < steps; k += W * U) {
+        i32x4 w[U][NT], a[U][MT][FP8 ? 2 : 1];
+        uint32_t sw[NT][U], sa[MT][U];
+        // places of the U steps in any row; E4M3: 16 neighbours from 16 g and 16 from 64 + 16 g
+        uint32_t at[U], at0[U], at1[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t e = 128 * (k + u) + 16 * g;
+            at[u] = 4 * (k + u) + g < blocks ? 64 * (k + u) + 16 * g : 0;
+            at0[u] = e < (uint32_t)p.K ? e : 0;
+            at1[u] = e + 64 < (uint32_t)p.K ? e + 64 : 0;
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            i32x8 a = {};
-            int as = 127;
-            if constexpr (FP8) {
-                const uint8_t *q = p.a + ar[i] * p.K;
-                const int at = k * 128 + 16 * g;
-                i32x4 x = {}, y = {};
-                if (at < p.K) x = *(const i32x4 *)(q + at);
-                if (at + 64 < p.K) y = *(const i32x4 *)(q + at + 64);
-                a = i32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            } else if (in) {
-                const i32x4 x = *(const i32x4 *)(p.a + ar[i] * (p.K / 2) + blk * 16);
-                a = i32x8{x[0], x[1], x[2], x[3], 0, 0, 0, 0};
-                as = p.a_scales[ar[i] * per + blk];
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[u][j] = *(const i32x4 *)(wb + (wr[j] * wrow + at[u]));
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if constexpr (FP8) {
+                    a[u][i][0] = *(const i32x4 *)(ab + (ar[i] * arow + at0[u]));
+                    a[u][i][1] = *(const i32x4 *)(ab + (ar[i] * arow + at1[u]));
+                } else {
+                    a[u][i][0] = *(const i32x4 *)(ab + (ar[i] * arow + at[u]));
+                }
             }
-            c[i] = product<FP8, 0>(w, a, c[i], ws, as);
+        auto scales = [&](auto whole) {
+            auto row = [&](const uint8_t *base, uint32_t row, uint32_t (&s)[U]) {
+                if constexpr (decltype(whole)::value) {
+                    const Scales v = *(const Scales *)(base + (row * per + 4 * k));
+#pragma unroll
+                    for (int u = 0; u < U; ++u) s[u] = v[u];
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) s[u] = *(const uint32_t *)(base + (row * per + (k + u < steps ? 4 * (k + u) : 0)));
+                }
+            };
+#pragma unroll
+            for (int j = 0; j < NT; ++j) row(wsb, wr[j], sw[j]);
+            if constexpr (!FP8) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) row(asb, ar[i], sa[i]);
+            }
+        };
+        if (k + U <= steps) scales(std::true_type());
+        else scales(std::false_type());
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = 4 * (k + u) + g < blocks;
+            int x[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) x[j] = in ? sw[j][u] >> (8 * g) : 0;      // (the lowest byte counts)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int y = !in ? 0 : FP8 ? 127 : sa[i][u] >> (8 * g);
+                i32x8 v = {a[u][i][0][0], a[u][i][0][1], a[u][i][0][2], a[u][i][0][3], 0, 0, 0, 0};
+                if constexpr (FP8)
+                    v = i32x8{a[u][i][0][0], a[u][i][0][1], a[u][i][0][2], a[u][i][0][3],
+                              a[u][i][1][0], a[u][i][1][1], a[u][i][1][2], a[u][i][1][3]};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const i32x8 q = {w[u][j][0], w[u][j][1], w[u][j][2], w[u][j][3], 0, 0, 0, 0};
+                    c[i][j] = product<FP8, 0>(q, v, c[i][j], x[j], y);
+                }
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) sm[wv][i][lane] = c[i];
-    __syncthreads();
-    for (int i = wv; i < MT; i += W) {               // the wavefronts' sums in their order
-        f32x4 s = sm[0][i][lane];
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int v = 1; v < W; ++v) s += sm[v][i][lane];
-        put<FP8, BF16>(p, m0 + 16 * i + r, j0 + 4 * g, s);
+        for (int j = 0; j < NT; ++j) sm[wv][i * NT + j][lane] = c[i][j];
+    __syncthreads();
+#pragma unroll 1
+    for (int t = wv; t < MT * NT; t += W) {          // the wavefronts' sums in their order
+        f32x4 s = sm[0][t][lane];
+#pragma unroll
+        for (int v = 1; v < W; ++v) s += sm[v][t][lane];
+        put<FP8, BF16>(p, m0 + 16 * (t / NT) + r, j0 + 16 * (t % NT) + 4 * g, s);
     }
 }
 
-template <bool FP8, bool BF16, int MT>
+template <bool FP8, bool BF16, int MT, int NT, int U, int W>
 hipError_t go_few(const MxProduct &p, hipStream_t s) {
-    const int64_t groups = (p.M + 16 * MT - 1) / (16 * MT) * ((p.N + 15) / 16);
-    lores_mx_few_kernel<FP8, BF16, MT, 8><<<grid_of(groups), 512, 0, s>>>(p);
+    const dim3 grid((uint32_t)((p.N + 16 * NT - 1) / (16 * NT)), (uint32_t)((p.M + 16 * MT - 1) / (16 * MT)));
+    lores_mx_few_kernel<FP8, BF16, MT, NT, U, W><<<grid, 64 * W, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -395,11 +447,12 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
         // outputs in pieces of 16 bytes, if rows of them are whole: 16 rows of 128 bytes at a
         // time through the wavefront's own place in LDS, so that lines are written whole
         // (stored as they stand in the registers they took 45 us of 183)
-        constexpr int E = BF16 ? 8 : 4, FR = BF16 ? 4 : 2;       // outputs of a piece, tiles of 16 columns
+        // outputs of a piece, tiles of 16 columns at a time, pieces of a row
+        constexpr int E = BF16 ? 8 : 4, FR = NI < E / 2 ? NI : E / 2, CH = FR * 16 / E;
         // (what follows from the lane is made anew: kept over the loop it would cost registers)
         int l = lane;
         asm volatile("" : "+v"(l));
-        const int lr = l & 15, lg = l >> 4, row = l >> 3, ch = l & 7;
+        const int lr = l & 15, lg = l >> 4, row = l / CH, ch = l % CH;
         if (p.N % E == 0) {
             uint8_t *own = sh.out[wv];
 #pragma unroll
@@ -411,15 +464,16 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
                     for (int j = 0; j < FR; ++j) {
                         const f32x4 x = FP8 ? c[i][h + j] * f : c[i][h + j];
                         if constexpr (BF16)
-                            *(u16x4 *)(own + (lr * 8 + ((2 * j + (lg >> 1)) ^ (lr & 7))) * 16 + (lg & 1) * 8) =
+                            *(u16x4 *)(own + (lr * CH + ((2 * j + (lg >> 1)) ^ (lr & (CH - 1)))) * 16 + (lg & 1) * 8) =
                                 u16x4{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
                         else
-                            *(f32x4 *)(own + (lr * 8 + ((4 * j + lg) ^ (lr & 7))) * 16) = x;
+                            *(f32x4 *)(own + (lr * CH + ((4 * j + lg) ^ (lr & (CH - 1)))) * 16) = x;
                     }
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const u32x4 x = *(const u32x4 *)(own + ((q * 8 + row) * 8 + (ch ^ row)) * 16);
-                        const int64_t mm = m + 16 * i + q * 8 + row;
+                    for (int q = 0; q < CH / 4; ++q) {           // 64 / CH rows at once
+                        const int at = q * (64 / CH) + row;
+                        const u32x4 x = *(const u32x4 *)(own + (at * CH + (ch ^ (at & (CH - 1)))) * 16);
+                        const int64_t mm = m + 16 * i + at;
                         const int nn = n + 16 * h + ch * E;
                         if (FULL || (mm < p.M && nn < p.N)) *(u32x4 *)((uint8_t *)p.out + (mm * p.N + nn) * (16 / E)) = x;
                     }
@@ -447,19 +501,33 @@ hipError_t go_tile(const MxProduct &p, int residents, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Tiles of 64 x 64 while they run at once (three of 4-bit rows on a CU), of 128 x 128 while
+// those do (two; one of E4M3 rows), else the largest that LDS and registers hold.  us at
+// K = 4096, 64 x 64 / 128 x 128 / largest:
+//   outputs         512 x 4096        512 x 8192       1024 x 8192       2048 x 8192
+//   4-bit rows   14.4 14.9 29.2    25.6 17.2 30.4    40.9 26.4 33.0    73.3 48.7 40.5
+//   E4M3 rows    17.7 24.4 30.5    31.6 27.6 31.6    57.5 49.8 37.4   103.2 92.1 67.2
 template <bool FP8, bool BF16, bool X4>
 hipError_t go_tiles(const MxProduct &p, hipStream_t s) {
-    if (p.M >= 256 && p.N >= 256 && p.M * p.N >= (int64_t)256 * 256 * 128) {
+    const int64_t cells = p.M * p.N;
+    if (p.M >= 256 && p.N >= 256 && cells > (FP8 ? 1 << 22 : 1 << 23)) {
         if constexpr (FP8) return go_tile<FP8, BF16, true, X4, 4, 4, 2, 4>(p, 256, s);
         else return go_tile<FP8, BF16, true, X4, 4, 8, 4, 2>(p, 256, s);
     }
+    if (cells <= 1 << 21) return go_tile<FP8, BF16, false, X4, 2, 2, 2, 2>(p, FP8 ? 512 : 768, s);
     return go_tile<FP8, BF16, false, X4, 4, 4, 2, 2>(p, FP8 ? 256 : 512, s);
 }
 
+// Few rows: the fewest rows a work-group (16, 32 or 64) with which there are at most 256
+// work-groups; us at K = 4096, 16 / 32 / 64 rows / tiles of 64 x 64:
+//   48 x 1024  5.4 6.7 8.3 11.6    48 x 4096  8.8 6.9 8.4 11.8    48 x 8192  12.2 10.7 8.7 12.2
+//   256 x 1024  8.9 6.9 9.2 8.9    96 x 4096  12.0 11.1 9.3 11.9   256 x 4096  28.6 20.5 16.4 12.9
 template <bool FP8, bool BF16>
 hipError_t go(const MxProduct &p, hipStream_t s) {
-    if (p.M <= 16) return go_few<FP8, BF16, 1>(p, s);
-    if (p.M <= 64) return go_few<FP8, BF16, 4>(p, s);
+    const int64_t columns = (p.N + 31) / 32;
+    if (columns * ((p.M + 15) / 16) <= 256 || p.M <= 16) return go_few<FP8, BF16, 1, 2, 4, 8>(p, s);
+    if (columns * ((p.M + 31) / 32) <= 256 || p.M <= 32) return go_few<FP8, BF16, 2, 2, 4, 8>(p, s);
+    if (columns * ((p.M + 63) / 64) <= 256 || p.M <= 64) return go_few<FP8, BF16, 4, 2, 4, 8>(p, s);
     return mx_scale_stride(p.K) % 16 == 0 ? go_tiles<FP8, BF16, true>(p, s) : go_tiles<FP8, BF16, false>(p, s);
 }
 
