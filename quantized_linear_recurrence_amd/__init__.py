@@ -540,32 +540,48 @@ def lores_rmsnorm_backward(h, weight, dy, eps, dresidual=None, stream=None):
 
 
 # ------------------------------------------------------------------- layers
+#
+# For a decode batch these calls cost the host more than the GPU (a launch 3.8 us of
+# some 8), so the checks touch every property once, take the usual shapes first, and
+# enter no context where the current device and stream are the ones to use.
 
-def _current(device):
-    """Launches inside go to `device`, where the tensors are."""
+def _context(stream, device):
+    """What makes `device` and `stream` the current ones; None if they are."""
     import torch
-    return _NOTHING if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    if torch._C._cuda_getDevice() != device.index:
+        return torch.cuda.device(device)
+    return None
 
 
-def _strided(t, name, like, kept):
-    """A tensor of like's shape, type and device whose last dimension is
-    contiguous and whose dimensions before the last `kept` have one stride: its
-    address, that stride and those of the kept dimensions but the last."""
+def _queue(device):
+    """The current stream of `device`."""
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t is not like:
-        if t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, x is on {like.device}")
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must be {list(like.shape)}, got {list(t.shape)}")
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _in(context, call, *args):
+    if context is None:
+        return call(*args)
+    with context:
+        return call(*args)
+
+
+def _rows_of(t, name, kept):
+    """A tensor whose last dimension is contiguous and whose dimensions before the
+    last `kept` lie one stride apart: that stride (None if there is one row) and
+    those of the kept dimensions but the last."""
     shape, st = t.shape, t.stride()
     if st[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
+    lead = len(shape) - kept
+    if lead == 1:
+        return st[0] if shape[0] != 1 else None, st[1:-1]
     step, size = None, 1
-    for d in range(len(shape) - kept - 1, -1, -1):
+    for d in range(lead - 1, -1, -1):
         if shape[d] == 1:
             continue
         if step is None:
@@ -573,59 +589,75 @@ def _strided(t, name, like, kept):
         elif st[d] != step * size:
             raise ValueError(f"the leading dimensions of {name} must lie one stride apart")
         size *= shape[d]
-    return t.data_ptr(), step, st[len(shape) - kept:-1]
+    return step, st[lead:-1]
+
+
+def _same(t, name, x):
+    """Refuses a tensor that is not of x's device, type and shape."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != x.device:
+        raise ValueError(f"{name} is on {t.device}, x is on {x.device}")
+    if t.dtype is not x.dtype:
+        raise TypeError(f"{name} must be {x.dtype}, got {t.dtype}")
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must be {list(x.shape)}, got {list(t.shape)}")
 
 
 def _layer_types(x, weight, name):
     import torch
     if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
         raise TypeError(f"x and {name} must be torch tensors")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"x must be on the GPU, got {x.device}")
-    bf, f32 = torch.bfloat16, torch.float32
-    for t, what in ((x, "x"), (weight, name)):
-        if t.dtype is not bf and t.dtype is not f32:
-            raise TypeError(f"{what} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    return int(x.dtype is bf), int(weight.dtype is bf)
+    bf, f32, xt, wt = torch.bfloat16, torch.float32, x.dtype, weight.dtype
+    if xt is not bf and xt is not f32:
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {xt}")
+    if wt is not bf and wt is not f32:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {wt}")
+    return int(xt is bf), int(wt is bf)
 
 
-def _needs_grad(*ts):
+def _warn_graph(what, *ts):
     import torch
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts):
+        _no_graph(what)
 
 
 def _mx_pair(t, lead, n):
     """Tensors for rows of n 4-bit values: codes and scales."""
     import torch
-    return (t.new_empty((*lead, n // 2), dtype=torch.uint8),
-            t.new_empty((*lead, (n + 127) // 128 * 4), dtype=torch.uint8))
+    u8 = torch.uint8
+    return (t.new_empty((*lead, n // 2), dtype=u8), t.new_empty((*lead, (n + 127) // 128 * 4), dtype=u8))
 
 
-def _row_out(x, out_prec, in_bf16, allowed):
-    """The output precision and its torch type (None: 4-bit blocks)."""
+def _out_prec(out_prec, in_bf16, allowed):
+    """The output precision, its torch type (None: 4-bit blocks) and whether that is x's."""
     import torch
-    if out_prec is None:
-        out_prec = LORES_BF16 if in_bf16 else LORES_FP32
+    if out_prec is None or out_prec == (LORES_BF16 if in_bf16 else LORES_FP32):
+        return (LORES_BF16 if in_bf16 else LORES_FP32), None, True
     if out_prec not in allowed:
         raise ValueError("out_prec must be one of " + ", ".join(allowed.values()))
     return out_prec, {LORES_FP32: torch.float32, LORES_BF16: torch.bfloat16, LORES_INT8: torch.int8,
-                      LORES_FP8: torch.float8_e4m3fn}.get(out_prec)
+                      LORES_FP8: torch.float8_e4m3fn}.get(out_prec), False
 
 
 def _gated_dims(x, gate, weight, eps, act, gate_first):
     in_bf16, w_bf16 = _layer_types(x, weight, "weight")
-    if x.dim() < 2 or x.shape[-1] < 1 or x.shape[-2] < 1:
-        raise ValueError(f"x must be [..., heads, n], got {list(x.shape)}")
-    heads, n = x.shape[-2:]
-    xp, xt, (xh,) = _strided(x, "x", x, 2)
-    gp, gt, (gh,) = _strided(gate, "gate", x, 2)
+    _same(gate, "gate", x)
+    shape = x.shape
+    if len(shape) < 2 or shape[-1] < 1 or shape[-2] < 1:
+        raise ValueError(f"x must be [..., heads, n], got {list(shape)}")
+    heads, n = shape[-2], shape[-1]
+    xt, xh = _rows_of(x, "x", 2)
+    gt, gh = _rows_of(gate, "gate", 2)
     per_head = weight.dim() == 2
     wp = _need(weight, "weight", weight.dtype, (heads, n) if per_head else (n,), x.device)
-    d = _lib.LoresGatedDims(x.numel() // (heads * n), heads, n, in_bf16, w_bf16, int(per_head), int(act),
-                            int(gate_first), eps)
-    d.x_stride[:] = (xt or 0, xh)
-    d.gate_stride[:] = (gt or 0, gh)
-    return d, xp, gp, wp
+    d = _lib.LoresGatedDims(x.numel() // (heads * n), heads, n, in_bf16, w_bf16, per_head, act, gate_first, eps)
+    d.x_stride[:] = (xt or 0, xh[0])
+    d.gate_stride[:] = (gt or 0, gh[0])
+    return d, x.data_ptr(), gate.data_ptr(), wp
 
 
 _GATED_OUT = {LORES_FP32: "LORES_FP32", LORES_BF16: "LORES_BF16", LORES_MXFP4: "LORES_MXFP4"}
@@ -647,20 +679,23 @@ def lores_gated_norm(x, gate, weight, eps, act=LORES_ACT_SILU, gate_first=False,
     No autograd graph is recorded (lores_gated_norm_backward has the gradients).
     """
     d, xp, gp, wp = _gated_dims(x, gate, weight, eps, act, gate_first)
-    if _needs_grad(x, gate, weight):
-        _no_graph("lores_gated_norm")
-    out_prec, dt = _row_out(x, out_prec, d.in_bf16, _GATED_OUT)
-    scales = None
-    with _current(x.device):
-        with _on(stream):
-            if dt is None:
-                y, scales = _mx_pair(x, x.shape[:-2], d.heads * d.n)
-            else:
-                y = x.new_empty(x.shape, dtype=dt)
-        _check(_lib.lib().lores_gated_norm(ctypes.byref(d), xp, gp, wp, out_prec, y.data_ptr(),
-                                           None if scales is None else scales.data_ptr(),
-                                           _raw_stream(stream, x.device)))
-    return y, scales
+    if x.requires_grad or gate.requires_grad or weight.requires_grad:
+        _warn_graph("lores_gated_norm", x, gate, weight)
+    prec, dt, same = _out_prec(out_prec, d.in_bf16, _GATED_OUT)
+
+    def call():
+        scales = sp = None
+        if same:
+            y = x.new_empty(x.shape)
+        elif dt is None:
+            y, scales = _mx_pair(x, x.shape[:-2], d.heads * d.n)
+            sp = scales.data_ptr()
+        else:
+            y = x.new_empty(x.shape, dtype=dt)
+        _check(_lib.lib().lores_gated_norm(d, xp, gp, wp, prec, y.data_ptr(), sp, _queue(x.device)))
+        return y, scales
+
+    return _in(_context(stream, x.device), call)
 
 
 def lores_gated_norm_backward(x, gate, weight, dy, eps, act=LORES_ACT_SILU, gate_first=False,
@@ -671,32 +706,40 @@ def lores_gated_norm_backward(x, gate, weight, dy, eps, act=LORES_ACT_SILU, gate
     d, xp, gp, wp = _gated_dims(x, gate, weight, eps, act, gate_first)
     dyp = _need(dy, "dy", x.dtype, x.shape, x.device)
     size = ctypes.c_size_t(0)
-    _check(_lib.lib().lores_gated_norm_workspace(ctypes.byref(d), ctypes.byref(size)))
-    with _current(x.device):
-        with _on(stream):
-            dx, dgate = x.new_empty(x.shape), x.new_empty(x.shape)
-            dw = x.new_empty(weight.shape, dtype=torch.float32)
-            work = x.new_empty(size.value, dtype=torch.uint8)
-        _check(_lib.lib().lores_gated_norm_backward(
-            ctypes.byref(d), xp, gp, wp, dyp, dx.data_ptr(), dgate.data_ptr(), dw.data_ptr(),
-            work.data_ptr(), size.value, _raw_stream(stream, x.device)))
-    return dx, dgate, dw
+    _check(_lib.lib().lores_gated_norm_workspace(d, ctypes.byref(size)))
+
+    def call():
+        dx, dgate = x.new_empty(x.shape), x.new_empty(x.shape)
+        dw = x.new_empty(weight.shape, dtype=torch.float32)
+        work = x.new_empty(size.value, dtype=torch.uint8)
+        _check(_lib.lib().lores_gated_norm_backward(d, xp, gp, wp, dyp, dx.data_ptr(), dgate.data_ptr(),
+                                                    dw.data_ptr(), work.data_ptr(), size.value,
+                                                    _queue(x.device)))
+        return dx, dgate, dw
+
+    return _in(_context(stream, x.device), call)
 
 
 def _block_dims(x, residual, weight, weight_next, eps, scale, gate, act):
     in_bf16, w_bf16 = _layer_types(x, weight_next, "weight_next")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError(f"x must be [..., n] with n >= 1, got {list(x.shape)}")
-    n = x.shape[-1]
-    ptrs, strides = [], []
-    for t, name in ((x, "x"), (residual, "residual"), (gate, "gate")):
-        p, s, _ = (None, None, None) if t is None else _strided(t, name, x, 1)
-        ptrs.append(p)
-        strides.append(n if s is None else s)
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError(f"x must be [..., n] with n >= 1, got {list(shape)}")
+    n = shape[-1]
+    xs = _rows_of(x, "x", 1)[0]
+    rp = gp = None
+    rs = gs = n
+    if residual is not None:
+        _same(residual, "residual", x)
+        rs, rp = _rows_of(residual, "residual", 1)[0], residual.data_ptr()
+    if gate is not None:
+        _same(gate, "gate", x)
+        gs, gp = _rows_of(gate, "gate", 1)[0], gate.data_ptr()
     wn = _need(weight_next, "weight_next", weight_next.dtype, (n,), x.device)
-    w = _whole(weight, "weight", weight_next.dtype, (n,), x.device)
-    d = _lib.LoresBlockDims(x.numel() // n, n, in_bf16, w_bf16, int(act), eps, scale, *strides)
-    return d, ptrs, w, wn
+    w = None if weight is None else _whole(weight, "weight", weight_next.dtype, (n,), x.device)
+    d = _lib.LoresBlockDims(x.numel() // n, n, in_bf16, w_bf16, act, eps, scale, n if xs is None else xs,
+                            n if rs is None else rs, n if gs is None else gs)
+    return d, x.data_ptr(), rp, gp, w, wn
 
 
 def lores_block_norm(x, residual, weight, weight_next, eps, scale=1.0, gate=None, act=LORES_ACT_NONE,
@@ -713,24 +756,28 @@ def lores_block_norm(x, residual, weight, weight_next, eps, scale=1.0, gate=None
     (lores_block_norm_backward has the gradients).
     """
     import torch
-    d, (xp, rp, gp), w, wn = _block_dims(x, residual, weight, weight_next, eps, scale, gate, act)
-    if _needs_grad(x, residual, weight, weight_next, gate):
-        _no_graph("lores_block_norm")
-    out_prec, dt = _row_out(x, out_prec, d.in_bf16, _BLOCK_OUT)
-    scales = None
-    with _current(x.device):
-        with _on(stream):
-            if dt is None:
-                y, scales = _mx_pair(x, x.shape[:-1], d.n)
-            else:
-                y = x.new_empty(x.shape, dtype=dt)
-                if out_prec in (LORES_INT8, LORES_FP8):
-                    scales = x.new_empty(x.shape[:-1], dtype=torch.float32)
-            h = x.new_empty(x.shape)
-        _check(_lib.lib().lores_block_norm(ctypes.byref(d), xp, rp, gp, w, wn, out_prec, y.data_ptr(),
-                                           None if scales is None else scales.data_ptr(), h.data_ptr(),
-                                           _raw_stream(stream, x.device)))
-    return y, scales, h
+    d, xp, rp, gp, w, wn = _block_dims(x, residual, weight, weight_next, eps, scale, gate, act)
+    _warn_graph("lores_block_norm", x, residual, weight, weight_next, gate)
+    prec, dt, same = _out_prec(out_prec, d.in_bf16, _BLOCK_OUT)
+
+    def call():
+        scales = sp = None
+        h = x.new_empty(x.shape)
+        if same:
+            y = x.new_empty(x.shape)
+        elif dt is None:
+            y, scales = _mx_pair(x, x.shape[:-1], d.n)
+            sp = scales.data_ptr()
+        else:
+            y = x.new_empty(x.shape, dtype=dt)
+            if prec == LORES_INT8 or prec == LORES_FP8:
+                scales = x.new_empty(x.shape[:-1], dtype=torch.float32)
+                sp = scales.data_ptr()
+        _check(_lib.lib().lores_block_norm(d, xp, rp, gp, w, wn, prec, y.data_ptr(), sp, h.data_ptr(),
+                                           _queue(x.device)))
+        return y, scales, h
+
+    return _in(_context(stream, x.device), call)
 
 
 def lores_block_norm_backward(x, h, weight, weight_next, dy, eps, scale=1.0, gate=None,
@@ -740,24 +787,26 @@ def lores_block_norm_backward(x, h, weight, weight_next, dy, eps, scale=1.0, gat
     None).  h is the sum that lores_block_norm returned.  dgate and dw are None
     without a gate or a weight; the weights' gradients are fp32."""
     import torch
-    d, (xp, _, gp), w, wn = _block_dims(x, None, weight, weight_next, eps, scale, gate, act)
+    d, xp, _, gp, w, wn = _block_dims(x, None, weight, weight_next, eps, scale, gate, act)
     hp = _need(h, "h", x.dtype, x.shape, x.device)
     dyp = _need(dy, "dy", x.dtype, x.shape, x.device)
     dhp = _whole(dh, "dh", x.dtype, x.shape, x.device)
     size = ctypes.c_size_t(0)
-    _check(_lib.lib().lores_block_norm_workspace(ctypes.byref(d), ctypes.byref(size)))
-    with _current(x.device):
-        with _on(stream):
-            dx, dres = x.new_empty(x.shape), x.new_empty(x.shape)
-            dgate = None if gate is None else x.new_empty(x.shape)
-            dwn = x.new_empty(d.n, dtype=torch.float32)
-            dw = None if weight is None else torch.empty_like(dwn)
-            work = x.new_empty(size.value, dtype=torch.uint8)
+    _check(_lib.lib().lores_block_norm_workspace(d, ctypes.byref(size)))
+
+    def call():
+        dx, dres = x.new_empty(x.shape), x.new_empty(x.shape)
+        dgate = None if gate is None else x.new_empty(x.shape)
+        dwn = x.new_empty(d.n, dtype=torch.float32)
+        dw = None if weight is None else torch.empty_like(dwn)
+        work = x.new_empty(size.value, dtype=torch.uint8)
         _check(_lib.lib().lores_block_norm_backward(
-            ctypes.byref(d), xp, hp, gp, w, wn, dyp, dhp, dx.data_ptr(), dres.data_ptr(),
+            d, xp, hp, gp, w, wn, dyp, dhp, dx.data_ptr(), dres.data_ptr(),
             None if dgate is None else dgate.data_ptr(), None if dw is None else dw.data_ptr(),
-            dwn.data_ptr(), work.data_ptr(), size.value, _raw_stream(stream, x.device)))
-    return dx, dres, dgate, dw, dwn
+            dwn.data_ptr(), work.data_ptr(), size.value, _queue(x.device)))
+        return dx, dres, dgate, dw, dwn
+
+    return _in(_context(stream, x.device), call)
 
 
 def lores_mx_quant(x, stream=None):
@@ -770,37 +819,46 @@ def lores_mx_quant(x, stream=None):
     import torch
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch tensor")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"x must be on the GPU, got {x.device}")
-    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
-        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
-    if x.dim() < 1 or x.shape[-1] < 32 or x.shape[-1] % 32:
-        raise ValueError(f"x must be [..., n] with n a multiple of 32, got {list(x.shape)}")
-    n = x.shape[-1]
-    xp, step, _ = _strided(x, "x", x, 1)
-    with _current(x.device):
-        with _on(stream):
-            codes, scales = _mx_pair(x, x.shape[:-1], n)
-        _check(_lib.lib().lores_mx_quant(xp, n if step is None else step, x.numel() // n, n,
-                                         int(x.dtype is torch.bfloat16), codes.data_ptr(),
-                                         scales.data_ptr(), _raw_stream(stream, x.device)))
-    return codes, scales
+    dt, shape = x.dtype, x.shape
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {dt}")
+    if len(shape) < 1 or shape[-1] < 32 or shape[-1] % 32:
+        raise ValueError(f"x must be [..., n] with n a multiple of 32, got {list(shape)}")
+    n = shape[-1]
+    step = _rows_of(x, "x", 1)[0]
+
+    def call():
+        codes, scales = _mx_pair(x, shape[:-1], n)
+        _check(_lib.lib().lores_mx_quant(x.data_ptr(), n if step is None else step, x.numel() // n, n,
+                                         dt is torch.bfloat16, codes.data_ptr(), scales.data_ptr(),
+                                         _queue(x.device)))
+        return codes, scales
+
+    return _in(_context(stream, x.device), call)
 
 
 def _mx_rows(codes, scales, name):
-    """Checks a pair of lores_mx_quant's: rows and their length."""
+    """Checks a pair of lores_mx_quant's: addresses, rows and their length."""
     import torch
     if not isinstance(codes, torch.Tensor) or not isinstance(scales, torch.Tensor):
         raise TypeError(f"{name} and its scales must be torch tensors")
-    if codes.device.type != "cuda":
+    if not codes.is_cuda:
         raise ValueError(f"{name} must be on the GPU, got {codes.device}")
-    if codes.dim() < 1 or codes.shape[-1] < 16 or codes.shape[-1] % 16:
-        raise ValueError(f"{name} must be [..., n / 2] with n a multiple of 32, got {list(codes.shape)}")
-    n = 2 * codes.shape[-1]
-    u8, lead = torch.uint8, codes.shape[:-1]
-    return (_need(codes, name, u8, codes.shape, codes.device),
-            _need(scales, f"{name}'s scales", u8, (*lead, (n + 127) // 128 * 4), codes.device),
-            codes.numel() // (n // 2), n)
+    shape = codes.shape
+    if len(shape) < 1 or shape[-1] < 16 or shape[-1] % 16:
+        raise ValueError(f"{name} must be [..., n / 2] with n a multiple of 32, got {list(shape)}")
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+        raise TypeError(f"{name} and its scales must be torch.uint8, got {codes.dtype}, {scales.dtype}")
+    if scales.device != codes.device:
+        raise ValueError(f"{name}'s scales are on {scales.device}, {name} is on {codes.device}")
+    n = 2 * shape[-1]
+    if scales.shape != (*shape[:-1], (n + 127) // 128 * 4):
+        raise ValueError(f"{name}'s scales must be {[*shape[:-1], (n + 127) // 128 * 4]}, got {list(scales.shape)}")
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError(f"{name} and its scales must be contiguous")
+    return codes.data_ptr(), scales.data_ptr(), codes.numel() // (n // 2), n
 
 
 def lores_mx_dequant(codes, scales, dtype=None, stream=None):
@@ -811,12 +869,14 @@ def lores_mx_dequant(codes, scales, dtype=None, stream=None):
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
     cp, sp, rows, n = _mx_rows(codes, scales, "codes")
-    with _current(codes.device):
-        with _on(stream):
-            out = codes.new_empty((*codes.shape[:-1], n), dtype=dtype)
-        _check(_lib.lib().lores_mx_dequant(cp, sp, rows, n, int(dtype is torch.bfloat16), out.data_ptr(),
-                                           _raw_stream(stream, codes.device)))
-    return out
+
+    def call():
+        out = codes.new_empty((*codes.shape[:-1], n), dtype=dtype)
+        _check(_lib.lib().lores_mx_dequant(cp, sp, rows, n, dtype is torch.bfloat16, out.data_ptr(),
+                                           _queue(codes.device)))
+        return out
+
+    return _in(_context(stream, codes.device), call)
 
 
 def lores_mx_matmul(a, a_scales, w, w_scales, out_prec=LORES_BF16, out=None, stream=None):
@@ -836,28 +896,33 @@ def lores_mx_matmul(a, a_scales, w, w_scales, out_prec=LORES_BF16, out=None, str
         raise ValueError(f"w must be [N, K / 2], got {list(w.shape)}")
     if not isinstance(a, torch.Tensor):
         raise TypeError("a must be a torch tensor")
-    if a.device != w.device:
-        raise ValueError(f"a is on {a.device}, w is on {w.device}")
+    device = w.device
+    if a.device != device:
+        raise ValueError(f"a is on {a.device}, w is on {device}")
+    lead = a.shape[:-1]
     if a.dtype is torch.float8_e4m3fn:
         prec = LORES_FP8
         if a.dim() < 1 or a.shape[-1] != K:
             raise ValueError(f"a must be [..., {K}], got {list(a.shape)}")
         if out_prec != LORES_BF16:
             raise ValueError("E4M3 rows give LORES_BF16")
-        ap = _need(a, "a", a.dtype, a.shape, w.device)
-        asp = _need(a_scales, "a_scales", torch.float32, a.shape[:-1], w.device)
+        ap = _need(a, "a", a.dtype, a.shape, device)
+        asp = _need(a_scales, "a_scales", torch.float32, lead, device)
+        M = a.numel() // K
     else:
         prec = LORES_MXFP4
-        ap, asp, _, ka = _mx_rows(a, a_scales, "a")
+        ap, asp, M, ka = _mx_rows(a, a_scales, "a")
         if ka != K:
             raise ValueError(f"a has rows of {ka}, w of {K}")
-    lead = a.shape[:-1]
     dt = torch.bfloat16 if out_prec == LORES_BF16 else torch.float32
-    with _current(w.device):
-        with _on(stream):
-            if out is None:
-                out = w.new_empty((*lead, N), dtype=dt)
-        op = _need(out, "out", dt, (*lead, N), w.device)
-        _check(_lib.lib().lores_mx_matmul(ap, asp, prec, wp, wsp, lead.numel(), N, K, out_prec, op,
-                                          _raw_stream(stream, w.device)))
-    return out
+
+    def call():
+        if out is None:
+            y = w.new_empty((*lead, N), dtype=dt)
+            yp = y.data_ptr()
+        else:
+            y, yp = out, _need(out, "out", dt, (*lead, N), device)
+        _check(_lib.lib().lores_mx_matmul(ap, asp, prec, wp, wsp, M, N, K, out_prec, yp, _queue(device)))
+        return y
+
+    return _in(_context(stream, device), call)
