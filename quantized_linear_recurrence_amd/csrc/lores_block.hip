@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_kernel(cons
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(h[i][e], h[i][e], sum);
+            for (int e = 0; e < 8; ++e) sum = fmaf(e >= own_from<TPR, VEC>(t, i, a.n) ? h[i][e] : 0.0f, h[i][e], sum);
         sum = row_sum<TPR>(sum, sm);
         const float r1 = 1.0f / sqrtf(sum / (float)a.n + a.eps);
 #pragma unroll
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_kernel(cons
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            sum = fmaf(h[i][e], h[i][e], sum);
+            sum = fmaf(e >= own_from<TPR, VEC>(t, i, a.n) ? h[i][e] : 0.0f, h[i][e], sum);
             h[i][e] = h[i][e] * w[i][e];
             bits = max(bits, __float_as_uint(fabsf(h[i][e])));
         }
@@ -73,38 +73,61 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_kernel(cons
 // The weights' gradients are summed as the plain norm's: by each work-group over
 // its rows, then over the work-groups in a fixed order.  Both stand side by
 // side in a work-group's part: dwn, then (with a weight) dw.
+//
+// 1024 threads leave a thread 128 registers, which two vectors of five rows, two
+// weights and their sums do not fit (4096 x 16384 with all kept: 630 us).  LEAN
+// keeps the sums in LDS and reads the weights and the gate's row where they are used.
 template <typename T, int TPR, int VPT, int VEC>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_kernel(const BlockArgs a) {
     constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
+    constexpr bool LEAN = TPR * VPT > 1024;
     __shared__ float sm[TPR > 64 ? TPR / 64 : 1][2];
     __shared__ __attribute__((aligned(16))) float sums[ROWS > 1 ? ROWS : 1][ROWS > 1 ? TPR * VPT * 8 : 1];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    float w[VPT][8], wn[VPT][8], dw[VPT][8], dwn[VPT][8];
-    load_either<TPR, VPT, VEC>(a.wn, a.w_bf16, t, a.n, wn);
-    if (a.w) load_either<TPR, VPT, VEC>(a.w, a.w_bf16, t, a.n, w);
+    __shared__ float far[LEAN ? 2 : 1][LEAN ? VPT * 8 : 1][LEAN ? TPR : 1];
+    float w[VPT][8], wn[VPT][8], dw[LEAN ? 1 : VPT][8], dwn[LEAN ? 1 : VPT][8];
+    // the thread's sums of dwn (k = 0) and dw (1)
+    auto sum = [&](int k, int i, int e) -> float & {
+        if constexpr (LEAN) return far[k][i * 8 + e][t];
+        else return k ? dw[i][e] : dwn[i][e];
+    };
+    auto weight_next = [&] { load_either<TPR, VPT, VEC>(a.wn, a.w_bf16, t, a.n, wn); };
+    auto weight = [&] {
+        if (a.w) {
+            load_either<TPR, VPT, VEC>(a.w, a.w_bf16, t, a.n, w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[i][e] = 1.0f;
+        }
+    };
+    if constexpr (!LEAN) {
+        weight_next();
+        weight();
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (!a.w) w[i][e] = 1.0f;
-            dw[i][e] = dwn[i][e] = 0.0f;
-        }
+        for (int e = 0; e < 8; ++e) sum(0, i, e) = sum(1, i, e) = 0.0f;
     const float per = 1.0f / (float)a.n;
     for (int64_t row = (int64_t)blockIdx.x * ROWS + sub; row < a.rows; row += (int64_t)a.groups * ROWS) {
         Kept<T> kx[VPT], kh[VPT], kg[VPT], ky[VPT], kd[VPT];
         keep_row<T, TPR, VPT, VEC>((const T *)a.h + row * a.n, t, a.n, kh);
         keep_row<T, TPR, VPT, VEC>((const T *)a.dy + row * a.n, t, a.n, ky);
         keep_row<T, TPR, VPT, VEC>((const T *)a.x + row * a.xs, t, a.n, kx);
-        if (a.gate) keep_row<T, TPR, VPT, VEC>((const T *)a.gate + row * a.gs, t, a.n, kg);
+        if (a.gate && !LEAN) keep_row<T, TPR, VPT, VEC>((const T *)a.gate + row * a.gs, t, a.n, kg);
         if (a.dh) keep_row<T, TPR, VPT, VEC>((const T *)a.dh + row * a.n, t, a.n, kd);
+        if constexpr (LEAN) weight_next();
         float s2 = 0.0f, dot2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float h = kh[i].at(e);
-                s2 = fmaf(h, h, s2);
-                dot2 = fmaf(h, wn[i][e] * ky[i].at(e), dot2);
+                const float hc = e >= own_from<TPR, VEC>(t, i, a.n) ? h : 0.0f;
+                s2 = fmaf(hc, h, s2);
+                dot2 = fmaf(hc, wn[i][e] * ky[i].at(e), dot2);
             }
         reduce<TPR, false>(s2, dot2, sm);
         const float r2 = 1.0f / sqrtf(s2 / (float)a.n + a.eps);
@@ -115,26 +138,36 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_ke
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float n2 = kh[i].at(e) * r2, dy = ky[i].at(e);
-                dwn[i][e] = fmaf(dy, n2, dwn[i][e]);
+                sum(0, i, e) = fmaf(dy, n2, sum(0, i, e));
                 G[i][e] = fmaf(r2, fmaf(-n2, c2, wn[i][e] * dy), a.dh ? kd[i].at(e) : 0.0f);
             }
         store_row<T, TPR, VPT, VEC>((T *)a.dres + row * a.n, t, a.n, G);
-        // from here on G is sc G, and with a gate a and a' stand in registers
-        float ga[VPT][8], gs[VPT][8];
+        if constexpr (LEAN) {
+            weight();
+            if (a.gate) keep_row<T, TPR, VPT, VEC>((const T *)a.gate + row * a.gs, t, a.n, kg);
+        }
+        // from here on G is sc G
+        auto gate_of = [&](int i, int e, float &value, float &slope) {
+            value = slope = 1.0f;
+            if (a.gate) {
+                const float z = kg[i].at(e), sg = a.act ? sigmoid<T>(z) : 0.0f;
+                value = gate_value(a.act, z, sg);
+                slope = gate_slope(a.act, z, sg);
+            }
+        };
+        float ga[LEAN ? 1 : VPT][8], gs[LEAN ? 1 : VPT][8];
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 G[i][e] = a.scale * G[i][e];
-                ga[i][e] = gs[i][e] = 1.0f;
-                if (a.gate) {
-                    const float z = kg[i].at(e), sg = a.act ? sigmoid<T>(z) : 0.0f;
-                    ga[i][e] = gate_value(a.act, z, sg);
-                    gs[i][e] = gate_slope(a.act, z, sg);
-                }
+                float value, slope;
+                gate_of(i, e, value, slope);
+                if constexpr (!LEAN) { ga[i][e] = value; gs[i][e] = slope; }
                 const float x = kx[i].at(e);
-                s1 = fmaf(x, x, s1);
-                dot1 = fmaf(x, G[i][e] * ga[i][e] * w[i][e], dot1);
+                const float xc = e >= own_from<TPR, VEC>(t, i, a.n) ? x : 0.0f;
+                s1 = fmaf(xc, x, s1);
+                dot1 = fmaf(xc, G[i][e] * value * w[i][e], dot1);
             }
         float r1 = 1.0f, c1 = 0.0f;
         if (a.w) {
@@ -142,17 +175,23 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_ke
             r1 = 1.0f / sqrtf(s1 / (float)a.n + a.eps);
             c1 = dot1 * r1 * per;
         }
+        // G becomes dx
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+        for (int i = 0; i < VPT; ++i) {
+            float dz[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float n1 = kx[i].at(e) * r1, ge = G[i][e] * ga[i][e];
-                dw[i][e] = fmaf(ge, n1, dw[i][e]);
-                gs[i][e] = G[i][e] * n1 * w[i][e] * gs[i][e];
+                float value, slope;
+                if constexpr (LEAN) gate_of(i, e, value, slope);
+                else { value = ga[i][e]; slope = gs[i][e]; }
+                const float n1 = kx[i].at(e) * r1, ge = G[i][e] * value;
+                sum(1, i, e) = fmaf(ge, n1, sum(1, i, e));
+                dz[e] = G[i][e] * n1 * w[i][e] * slope;
                 G[i][e] = r1 * fmaf(-n1, c1, ge * w[i][e]);
             }
+            if (a.gate) store_vector<T, TPR, VEC>((T *)a.dgate + row * a.n, t, i, a.n, dz);
+        }
         store_row<T, TPR, VPT, VEC>((T *)a.dx + row * a.n, t, a.n, G);
-        if (a.gate) store_row<T, TPR, VPT, VEC>((T *)a.dgate + row * a.n, t, a.n, gs);
     }
     const int cols = a.w ? 2 * a.n : a.n;
     float *part = a.part + (int64_t)blockIdx.x * cols;
@@ -171,8 +210,16 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_ke
             }
         }
     } else {
-        store_row<float, TPR, VPT, VEC>(part, t, a.n, dwn);
-        if (a.w) store_row<float, TPR, VPT, VEC>(part + a.n, t, a.n, dw);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k && !a.w) return;
+            float x[VPT][8];
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[i][e] = sum(k, i, e);
+            store_row<float, TPR, VPT, VEC>(part + k * a.n, t, a.n, x);
+        }
     }
 }
 
@@ -182,19 +229,20 @@ hipError_t go(int mode, bool back, const BlockArgs &a, hipStream_t s) {
     if (back) {
         const dim3 grid((uint32_t)a.groups);
         if (mode == ROWS_VEC) lores_block_backward_kernel<T, TPR, VPT, ROWS_VEC><<<grid, TH, 0, s>>>(a);
-        else lores_block_backward_kernel<T, TPR, VPT, ROWS_ANY><<<grid, TH, 0, s>>>(a);
+        else lores_block_backward_kernel<T, TPR, VPT, ROWS_ODD><<<grid, TH, 0, s>>>(a);
         return hipGetLastError();
     }
     const dim3 grid = grid_of((a.rows + ROWS - 1) / ROWS);
     if (mode == ROWS_VEC) lores_block_kernel<T, TPR, VPT, ROWS_VEC><<<grid, TH, 0, s>>>(a);
-    else if (mode == ROWS_BLOCKS) lores_block_kernel<T, TPR, VPT, ROWS_BLOCKS><<<grid, TH, 0, s>>>(a);
-    else lores_block_kernel<T, TPR, VPT, ROWS_ANY><<<grid, TH, 0, s>>>(a);
+    else lores_block_kernel<T, TPR, VPT, ROWS_ODD><<<grid, TH, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t by_width(int mode, bool back, const BlockArgs &a, hipStream_t s) {
+    if (a.n <= 64) return go<T, 8, 1>(mode, back, a, s);
     if (a.n <= 128) return go<T, 16, 1>(mode, back, a, s);
+    if (a.n <= 256) return go<T, 32, 1>(mode, back, a, s);
     if (a.n <= 512) return go<T, 64, 1>(mode, back, a, s);
     if (a.n <= 1024) return go<T, 64, 2>(mode, back, a, s);
     if (a.n <= 2048) return go<T, 256, 1>(mode, back, a, s);
@@ -205,7 +253,14 @@ hipError_t by_width(int mode, bool back, const BlockArgs &a, hipStream_t s) {
 
 }  // namespace
 
-int block_groups(int64_t rows, int32_t n) { return norm_groups(rows, n); }
+// Work-groups that sum apart; us of the backward pass at 256 / 512 / 1024 of them, bf16, with a gate:
+//   8192 x 1024   42  34  40    16384 x 2048  190 115 115    16384 x 4096  295 209 213
+//   65536 x 128   46  34  40    8192 x 8192   248 254 271
+int block_groups(int64_t rows, int32_t n) {
+    const int side = n <= 64 ? 32 : n <= 128 ? 16 : n <= 256 ? 8 : n <= 1024 ? 4 : 1;     // rows of a work-group at once
+    const int64_t most = n <= 4096 ? 512 : 256, need = (rows + side - 1) / side;
+    return (int)(need < most ? need : most);
+}
 
 hipError_t launch_block(bool in_bf16, int mode, const BlockArgs &a, hipStream_t s) {
     return in_bf16 ? by_width<uint16_t>(mode, false, a, s) : by_width<float>(mode, false, a, s);

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_kernel(cons
         for (int e = 0; e < 8; ++e) {
             const float g = gate_value(a.act, z[i][e], a.act ? sigmoid<T>(z[i][e]) : 0.0f);
             if (a.gate_first) x[i][e] = x[i][e] * g;
-            sum = fmaf(x[i][e], x[i][e], sum);
+            sum = fmaf(e >= own_from<TPR, VEC>(t, i, a.n) ? x[i][e] : 0.0f, x[i][e], sum);
             w[i][e] = a.gate_first ? w[i][e] : w[i][e] * g;
         }
     sum = row_sum<TPR>(sum, sm);
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_kernel(cons
         store_row<float, TPR, VPT, VEC>((float *)a.y + row * a.n, t, a.n, x);
     } else if (a.out_prec == LORES_BF16) {
         store_row<uint16_t, TPR, VPT, VEC>((uint16_t *)a.y + row * a.n, t, a.n, x);
-    } else if constexpr (VEC != ROWS_ANY) {          // a token's heads are one row of blocks
+    } else {                                         // a token's heads are one row of blocks
         const int per = mx_scale_stride((int64_t)a.heads * a.n), blocks = a.n / 32;
         if (sum == 0.0f) {                           // (without an epsilon r is an infinity)
 #pragma unroll
@@ -69,23 +69,34 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_kernel(cons
 
 // dw is summed by each work-group over its rows (with weights per head, the
 // rows of one head), in registers and over the rows side by side in LDS; a
-// second kernel adds the work-groups' sums in a fixed order.
+// second kernel adds the work-groups' sums in a fixed order.  LEAN: 1024 threads leave
+// a thread 128 registers, so with two vectors the sums stand in LDS and the weights
+// are read where they are used.
 template <typename T, int TPR, int VPT, int VEC>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_backward_kernel(const GatedArgs a) {
     constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
     __shared__ float sm[TPR > 64 ? TPR / 64 : 1][2];
     __shared__ __attribute__((aligned(16))) float sums[ROWS > 1 ? ROWS : 1][ROWS > 1 ? TPR * VPT * 8 : 1];
+    constexpr bool LEAN = TPR * VPT > 1024;
+    __shared__ float far[LEAN ? VPT * 8 : 1][LEAN ? TPR : 1];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     // weights per head: the work-groups of neighbouring heads are neighbours
     const uint32_t own = a.per_head ? blockIdx.x % (uint32_t)a.heads : 0;
     const uint32_t group = a.per_head ? blockIdx.x / (uint32_t)a.heads : blockIdx.x;
     const int64_t count = a.per_head ? a.rows / a.heads : a.rows;    // rows the groups share out
-    float w[VPT][8], dw[VPT][8];
-    load_either<TPR, VPT, VEC>((const uint8_t *)a.w + (int64_t)own * a.n * (a.w_bf16 ? 2 : 4), a.w_bf16, t, a.n, w);
+    float w[VPT][8], dw[LEAN ? 1 : VPT][8];
+    auto sum = [&](int i, int e) -> float & {
+        if constexpr (LEAN) return far[i * 8 + e][t];
+        else return dw[i][e];
+    };
+    auto weight = [&] {
+        load_either<TPR, VPT, VEC>((const uint8_t *)a.w + (int64_t)own * a.n * (a.w_bf16 ? 2 : 4), a.w_bf16, t, a.n, w);
+    };
+    if constexpr (!LEAN) weight();
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+        for (int e = 0; e < 8; ++e) sum(i, e) = 0.0f;
     for (int64_t r = (int64_t)group * ROWS + sub; r < count; r += (int64_t)a.groups * ROWS) {
         uint32_t token = (uint32_t)r, head = own;
         if (!a.per_head) split_row(a, (uint32_t)r, token, head);
@@ -94,42 +105,49 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_backward_ke
         keep_row<T, TPR, VPT, VEC>((const T *)a.x + token * a.xs[0] + head * a.xs[1], t, a.n, kx);
         keep_row<T, TPR, VPT, VEC>((const T *)a.gate + token * a.gs[0] + head * a.gs[1], t, a.n, kz);
         keep_row<T, TPR, VPT, VEC>((const T *)a.dy + row * a.n, t, a.n, kg);
-        float s[VPT][8], ss = 0.0f, dot = 0.0f;
+        if constexpr (LEAN) weight();
+        float s[LEAN ? 1 : VPT][8], ss = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float z = kz[i].at(e), x = kx[i].at(e);
-                s[i][e] = a.act ? sigmoid<T>(z) : 0.0f;
-                const float g = gate_value(a.act, z, s[i][e]), u = a.gate_first ? x * g : x;
+                const float sg = a.act ? sigmoid<T>(z) : 0.0f;
+                if constexpr (!LEAN) s[i][e] = sg;
+                const float g = gate_value(a.act, z, sg), u = a.gate_first ? x * g : x;
                 const float d = kg[i].at(e) * w[i][e];
-                ss = fmaf(u, u, ss);
-                dot = fmaf(u, a.gate_first ? d : d * g, dot);
+                const float uc = e >= own_from<TPR, VEC>(t, i, a.n) ? u : 0.0f;
+                ss = fmaf(uc, u, ss);
+                dot = fmaf(uc, a.gate_first ? d : d * g, dot);
             }
         reduce<TPR, false>(ss, dot, sm);
         const float rstd = 1.0f / sqrtf(ss / (float)a.n + a.eps);
         const float c = dot * rstd / (float)a.n;     // mean(e n)
-        float dx[VPT][8], dz[VPT][8];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+        for (int i = 0; i < VPT; ++i) {
+            float dx[8], dz[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float z = kz[i].at(e), x = kx[i].at(e), dy = kg[i].at(e);
-                const float g = gate_value(a.act, z, s[i][e]), sl = gate_slope(a.act, z, s[i][e]);
+                float sg = 0.0f;                     // (LEAN makes it twice)
+                if constexpr (LEAN) sg = a.act ? sigmoid<T>(z) : 0.0f;
+                else sg = s[i][e];
+                const float g = gate_value(a.act, z, sg), sl = gate_slope(a.act, z, sg);
                 if (a.gate_first) {
                     const float n = x * g * rstd, du = rstd * fmaf(-n, c, dy * w[i][e]);
-                    dw[i][e] = fmaf(dy, n, dw[i][e]);
-                    dx[i][e] = du * g;
-                    dz[i][e] = du * x * sl;
+                    sum(i, e) = fmaf(dy, n, sum(i, e));
+                    dx[e] = du * g;
+                    dz[e] = du * x * sl;
                 } else {
                     const float n = x * rstd, d = dy * w[i][e];
-                    dw[i][e] = fmaf(dy * g, n, dw[i][e]);
-                    dx[i][e] = rstd * fmaf(-n, c, d * g);
-                    dz[i][e] = d * n * sl;
+                    sum(i, e) = fmaf(dy * g, n, sum(i, e));
+                    dx[e] = rstd * fmaf(-n, c, d * g);
+                    dz[e] = d * n * sl;
                 }
             }
-        store_row<T, TPR, VPT, VEC>((T *)a.dx + row * a.n, t, a.n, dx);
-        store_row<T, TPR, VPT, VEC>((T *)a.dgate + row * a.n, t, a.n, dz);
+            store_vector<T, TPR, VEC>((T *)a.dx + row * a.n, t, i, a.n, dx);
+            store_vector<T, TPR, VEC>((T *)a.dgate + row * a.n, t, i, a.n, dz);
+        }
     }
     float *part = a.part + ((int64_t)group * (a.per_head ? a.heads : 1) + own) * a.n;
     if constexpr (ROWS > 1) {                        // the rows side by side, in their order
@@ -142,7 +160,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_backward_ke
             part[c] = x;
         }
     } else {
-        store_row<float, TPR, VPT, VEC>(part, t, a.n, dw);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = sum(i, e);
+            store_vector<float, TPR, VEC>(part, t, i, a.n, x);
+        }
     }
 }
 
@@ -152,19 +176,20 @@ hipError_t go(int mode, bool back, const GatedArgs &a, hipStream_t s) {
     if (back) {
         const dim3 grid((uint32_t)a.groups * (a.per_head ? a.heads : 1));
         if (mode == ROWS_VEC) lores_gated_backward_kernel<T, TPR, VPT, ROWS_VEC><<<grid, TH, 0, s>>>(a);
-        else lores_gated_backward_kernel<T, TPR, VPT, ROWS_ANY><<<grid, TH, 0, s>>>(a);
+        else lores_gated_backward_kernel<T, TPR, VPT, ROWS_ODD><<<grid, TH, 0, s>>>(a);
         return hipGetLastError();
     }
     const dim3 grid = grid_of((a.rows + ROWS - 1) / ROWS);
     if (mode == ROWS_VEC) lores_gated_kernel<T, TPR, VPT, ROWS_VEC><<<grid, TH, 0, s>>>(a);
-    else if (mode == ROWS_BLOCKS) lores_gated_kernel<T, TPR, VPT, ROWS_BLOCKS><<<grid, TH, 0, s>>>(a);
-    else lores_gated_kernel<T, TPR, VPT, ROWS_ANY><<<grid, TH, 0, s>>>(a);
+    else lores_gated_kernel<T, TPR, VPT, ROWS_ODD><<<grid, TH, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t by_width(int mode, bool back, const GatedArgs &a, hipStream_t s) {
+    if (a.n <= 64) return go<T, 8, 1>(mode, back, a, s);
     if (a.n <= 128) return go<T, 16, 1>(mode, back, a, s);
+    if (a.n <= 256) return go<T, 32, 1>(mode, back, a, s);
     if (a.n <= 512) return go<T, 64, 1>(mode, back, a, s);
     if (a.n <= 1024) return go<T, 64, 2>(mode, back, a, s);
     if (a.n <= 2048) return go<T, 256, 1>(mode, back, a, s);
@@ -175,10 +200,16 @@ hipError_t by_width(int mode, bool back, const GatedArgs &a, hipStream_t s) {
 
 }  // namespace
 
+// Work-groups that sum dw apart (with weights per head: of all heads); us of the backward
+// pass at 512 / 1024 / 2048 of them, bf16:
+//   8192 x 32 x 128, one weight  84  76  77    per head  81  75  68
+//   8192 x 4 x 1024, per head    73  74  79    8192 x 1 x 4096  77  81  89    4096 x 1 x 8192  116 128 154 (256: 111)
 int gated_groups(int64_t tokens, int32_t heads, int32_t n, int32_t per_head) {
-    if (!per_head) return norm_groups(tokens * heads, n);
-    const int all = norm_groups(tokens, n), most = (1024 + heads - 1) / heads;
-    return all < most ? all : most;
+    const int side = n <= 64 ? 32 : n <= 128 ? 16 : n <= 256 ? 8 : n <= 1024 ? 4 : 1;     // rows of a work-group at once
+    const int64_t most = n <= 512 ? (per_head ? 2048 : 1024) : n <= 4096 ? 512 : 256;
+    const int64_t need = ((per_head ? tokens : tokens * heads) + side - 1) / side;
+    const int64_t share = per_head ? (most + heads - 1) / heads : most;
+    return (int)(need < share ? need : share);
 }
 
 hipError_t launch_gated(bool in_bf16, int mode, const GatedArgs &a, hipStream_t s) {

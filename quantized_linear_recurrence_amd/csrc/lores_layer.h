@@ -7,9 +7,9 @@
 
 namespace lores {
 
-// How a kernel reads its rows: single elements in any order, 16 bytes at a
-// time, or single elements in the order of the latter (4-bit output).
-enum { ROWS_ANY = 0, ROWS_VEC = 1, ROWS_BLOCKS = 2 };
+// How a kernel reads its rows (VEC of lores_rows.h): aligned rows of whole
+// vectors, or rows of any length and alignment.
+enum { ROWS_VEC = 1, ROWS_ODD = 2 };
 
 struct GatedArgs {
     int64_t rows;                      // tokens x heads

@@ -187,7 +187,7 @@ int lores_gated_norm(const lores_gated_dims *dims, const void *x, const void *ga
     a.scales = scales;
     const bool vec = gated_vec(dims, x, gate, weight) && aligned(y, 16);
     consume_stale_hip_error();
-    return hip_status(lores::launch_gated(dims->in_bf16, vec ? lores::ROWS_VEC : mx ? lores::ROWS_BLOCKS : lores::ROWS_ANY,
+    return hip_status(lores::launch_gated(dims->in_bf16, vec ? lores::ROWS_VEC : lores::ROWS_ODD,
                                           a, (hipStream_t)stream),
                       "gated norm");
 }
@@ -220,7 +220,7 @@ int lores_gated_norm_backward(const lores_gated_dims *dims, const void *x, const
     a.groups = lores::gated_groups(dims->tokens, dims->heads, dims->n, dims->per_head);
     const bool vec = gated_vec(dims, x, gate, weight) && aligned(dy, 16) && aligned(dx, 16) && aligned(dgate, 16);
     consume_stale_hip_error();
-    return hip_status(lores::launch_gated_backward(dims->in_bf16, vec ? lores::ROWS_VEC : lores::ROWS_ANY, a,
+    return hip_status(lores::launch_gated_backward(dims->in_bf16, vec ? lores::ROWS_VEC : lores::ROWS_ODD, a,
                                                    (hipStream_t)stream),
                       "gated norm backward");
 }
@@ -254,7 +254,7 @@ int lores_block_norm(const lores_block_dims *dims, const void *x, const void *re
     const bool vec = block_vec(dims, x, gate, weight, weight_next) && aligned(residual, 16) && aligned(h, 16) &&
                      (!residual || dims->res_stride * (int64_t)el % 16 == 0) && aligned(y, bytes ? 8 : 16);
     consume_stale_hip_error();
-    return hip_status(lores::launch_block(dims->in_bf16, vec ? lores::ROWS_VEC : mx ? lores::ROWS_BLOCKS : lores::ROWS_ANY,
+    return hip_status(lores::launch_block(dims->in_bf16, vec ? lores::ROWS_VEC : lores::ROWS_ODD,
                                           a, (hipStream_t)stream),
                       "block norm");
 }
@@ -295,7 +295,7 @@ int lores_block_norm_backward(const lores_block_dims *dims, const void *x, const
     const bool vec = block_vec(dims, x, gate, weight, weight_next) && aligned(h, 16) && aligned(dy, 16) &&
                      aligned(dh, 16) && aligned(dx, 16) && aligned(dresidual, 16) && aligned(dgate, 16);
     consume_stale_hip_error();
-    return hip_status(lores::launch_block_backward(dims->in_bf16, vec ? lores::ROWS_VEC : lores::ROWS_ANY, a,
+    return hip_status(lores::launch_block_backward(dims->in_bf16, vec ? lores::ROWS_VEC : lores::ROWS_ODD, a,
                                                    (hipStream_t)stream),
                       "block norm backward");
 }

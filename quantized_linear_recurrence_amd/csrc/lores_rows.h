@@ -33,6 +33,17 @@ template <> struct Elem<float> {
         *(f32x4 *)p = f32x4{x[0], x[1], x[2], x[3]};
         *(f32x4 *)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
     }
+    // at any multiple of an element: the hardware takes such addresses
+    typedef f32x4 Odd __attribute__((aligned(4)));
+    static __device__ __forceinline__ void get8_odd(const float *p, float *x) {
+        const f32x4 a = *(const Odd *)p, b = *(const Odd *)(p + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { x[e] = a[e]; x[4 + e] = b[e]; }
+    }
+    static __device__ __forceinline__ void put8_odd(float *p, const float *x) {
+        *(Odd *)p = f32x4{x[0], x[1], x[2], x[3]};
+        *(Odd *)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+    }
 };
 template <> struct Elem<uint16_t> {
     static __device__ __forceinline__ float get(const uint16_t *p) { return bf2f(*p); }
@@ -46,23 +57,44 @@ template <> struct Elem<uint16_t> {
             x[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ void put8(uint16_t *p, const float *x) {
+    static __device__ __forceinline__ u32x4 pack8(const float *x) {
         u32x4 a;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             a[e] = (uint32_t)f2bf(x[2 * e]) | ((uint32_t)f2bf(x[2 * e + 1]) << 16);
-        *(u32x4 *)p = a;
+        return a;
     }
+    static __device__ __forceinline__ void put8(uint16_t *p, const float *x) { *(u32x4 *)p = pack8(x); }
+    typedef u32x4 Odd __attribute__((aligned(2)));
+    static __device__ __forceinline__ void get8_odd(const uint16_t *p, float *x) {
+        const u32x4 a = *(const Odd *)p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(a[e] << 16);
+            x[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void put8_odd(uint16_t *p, const float *x) { *(Odd *)p = pack8(x); }
 };
 
 // One thread's elements of a row: VPT vectors of 8.  VEC 1: 8 neighbours per
 // vector and thread (16-byte accesses); 0: element e of vector i is 8 i + e
 // strides of TPR away, so that neighbouring threads read neighbouring
-// elements of rows at any alignment; 2: the columns of 1 by single elements,
-// for 4-bit blocks of rows at any alignment.
+// elements of rows at any alignment; 2: the columns of 1 in rows of any length
+// and alignment (of 8 elements or more), by vectors at odd addresses.  A row's last
+// vector then ends with the row, over part of its neighbour's: both compute the same
+// there, and only elements from own_from() on count in sums.
 template <int TPR, int VEC>
 __device__ __forceinline__ int col(int t, int i, int e) {
     return VEC ? (i * TPR + t) * 8 + e : (i * 8 + e) * TPR + t;
+}
+
+// vector i of a thread: its first column, and its first element that is not a neighbour's
+template <int TPR>
+__device__ __forceinline__ int odd_at(int t, int i, int n) { return min((i * TPR + t) * 8, n - 8); }
+template <int TPR, int VEC>
+__device__ __forceinline__ int own_from(int t, int i, int n) {
+    return VEC == 2 && n >= 8 ? (i * TPR + t) * 8 - odd_at<TPR>(t, i, n) : 0;
 }
 
 template <typename T, int TPR, int VPT, int VEC>
@@ -77,6 +109,13 @@ __device__ __forceinline__ void load_row(const T *p, int t, int n, float (&x)[VP
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
             }
+        } else if (VEC == 2 && n >= 8) {
+            if ((i * TPR + t) * 8 < n) {
+                Elem<T>::get8_odd(p + odd_at<TPR>(t, i, n), x[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -87,21 +126,29 @@ __device__ __forceinline__ void load_row(const T *p, int t, int n, float (&x)[VP
     }
 }
 
+// vector i of a thread's part of a row
+template <typename T, int TPR, int VEC>
+__device__ __forceinline__ void store_vector(T *p, int t, int i, int n, const float (&x)[8]) {
+    if constexpr (VEC == 1) {
+        const int c = (i * TPR + t) * 8;
+        if (c < n) Elem<T>::put8(p + c, x);
+    } else {
+        if (VEC == 2 && n >= 8) {
+            if ((i * TPR + t) * 8 < n) Elem<T>::put8_odd(p + odd_at<TPR>(t, i, n), x);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = col<TPR, VEC>(t, i, e);
+            if (c < n) Elem<T>::put(p + c, x[e]);
+        }
+    }
+}
+
 template <typename T, int TPR, int VPT, int VEC>
 __device__ __forceinline__ void store_row(T *p, int t, int n, const float (&x)[VPT][8]) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if constexpr (VEC == 1) {
-            const int c = (i * TPR + t) * 8;
-            if (c < n) Elem<T>::put8(p + c, x[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = col<TPR, VEC>(t, i, e);
-                if (c < n) Elem<T>::put(p + c, x[i][e]);
-            }
-        }
-    }
+    for (int i = 0; i < VPT; ++i) store_vector<T, TPR, VEC>(p, t, i, n, x[i]);
 }
 
 template <int TPR, int VPT, int VEC>
@@ -115,6 +162,14 @@ __device__ __forceinline__ void store_bytes(uint8_t *p, int t, int n, const uint
             for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)x[i][e] << (8 * (e & 3));
             if (c < n) *(u32x2 *)(p + c) = w;
         } else {
+            if (VEC == 2 && n >= 8) {
+                typedef u32x2 Odd __attribute__((aligned(1)));
+                u32x2 w = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)x[i][e] << (8 * (e & 3));
+                if ((i * TPR + t) * 8 < n) *(Odd *)(p + odd_at<TPR>(t, i, n)) = w;
+                continue;
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = col<TPR, VEC>(t, i, e);
@@ -185,6 +240,7 @@ template <> struct Kept<float> {
     }
     __device__ __forceinline__ float at(int e) const { return x[e]; }
     __device__ __forceinline__ void read(const float *p) { Elem<float>::get8(p, x); }
+    __device__ __forceinline__ void read_odd(const float *p) { Elem<float>::get8_odd(p, x); }
 };
 template <> struct Kept<uint16_t> {
     u32x4 x;
@@ -197,6 +253,7 @@ template <> struct Kept<uint16_t> {
         return __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
     }
     __device__ __forceinline__ void read(const uint16_t *p) { x = *(const u32x4 *)p; }
+    __device__ __forceinline__ void read_odd(const uint16_t *p) { x = *(const Elem<uint16_t>::Odd *)p; }
 };
 
 template <typename T, int TPR, int VPT, int VEC>
@@ -211,6 +268,13 @@ __device__ __forceinline__ void keep_row(const T *p, int t, int n, Kept<T> (&k)[
                 const float zero[8] = {};
                 k[i].set(zero);
             }
+        }
+    } else if (VEC == 2 && n >= 8) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const float zero[8] = {};
+            if ((i * TPR + t) * 8 < n) k[i].read_odd(p + odd_at<TPR>(t, i, n));
+            else k[i].set(zero);
         }
     } else {
         float x[VPT][8];

@@ -28,7 +28,7 @@ static hipError_t rec(const std::string &what) {
     g_next = hipSuccess;
     return e;
 }
-static std::string mode_name(int mode) { return mode == ROWS_VEC ? "vec" : mode == ROWS_BLOCKS ? "blocks" : "any"; }
+static std::string mode_name(int mode) { return mode == ROWS_VEC ? "vec" : "odd"; }
 int gated_groups(int64_t tokens, int32_t heads, int32_t, int32_t per_head) { return (int)(per_head ? tokens : tokens * heads); }
 int block_groups(int64_t rows, int32_t) { return (int)rows; }
 hipError_t launch_gated(bool, int mode, const GatedArgs &, hipStream_t) { return rec("gated " + mode_name(mode)); }
@@ -66,8 +66,8 @@ int main() {
         };
         fresh();
         OK(go(p, p, LORES_FP32, p, nullptr), "gated vec");
-        OK(go(p + 4, p, LORES_FP32, p, nullptr), "gated any");
-        OK(go(p, p + 4, LORES_MXFP4, p, u), "gated blocks");
+        OK(go(p + 4, p, LORES_FP32, p, nullptr), "gated odd");
+        OK(go(p, p + 4, LORES_MXFP4, p, u), "gated odd");
         OK(go(p, p, LORES_MXFP4, p, u + 1), "gated vec");
         BAD(go(p, p, LORES_MXFP4, p, nullptr));
         BAD(go(p, p, LORES_MXFP4, p + 4, u));
@@ -79,7 +79,7 @@ int main() {
         for (int prec : {(int)LORES_INT8, (int)LORES_FP8, (int)LORES_INT4, -1, 17}) BAD(go(p, p, prec, p, u));
         BAD(lores_gated_norm(nullptr, p, p, p, LORES_FP32, p, nullptr, nullptr));
         d.x_stride[0] = 257;
-        OK(go(p, p, LORES_FP32, p, nullptr), "gated any");
+        OK(go(p, p, LORES_FP32, p, nullptr), "gated odd");
         d.x_stride[0] = 0;
         OK(go(p, p, LORES_FP32, p, nullptr), "gated vec");
         d.x_stride[0] = -1;
@@ -111,7 +111,7 @@ int main() {
             return lores_gated_norm_backward(&d, p, p, p, dy, dx, dz, dw, work, bytes, nullptr);
         };
         OK(back(p, p, p, f, p, n), "gated back vec");
-        OK(back(p + 4, p, p, f, p, n), "gated back any");
+        OK(back(p + 4, p, p, f, p, n), "gated back odd");
         CHECK(back(p, p, p, f, p, n - 1) == LORES_ESIZE && g_log.empty());
         BAD(back(p, p, p, f, nullptr, n));
         BAD(back(p, p, p, f, p + 8, n));
@@ -141,8 +141,8 @@ int main() {
         fresh();
         OK(go(p, p, p, p, LORES_FP32, p, nullptr, p), "block vec");
         OK(go(p, nullptr, nullptr, nullptr, LORES_FP32, p, nullptr, p), "block vec");
-        OK(go(p, p + 4, nullptr, nullptr, LORES_FP32, p, nullptr, p), "block any");
-        OK(go(p, p + 4, nullptr, nullptr, LORES_MXFP4, p, u, p), "block blocks");
+        OK(go(p, p + 4, nullptr, nullptr, LORES_FP32, p, nullptr, p), "block odd");
+        OK(go(p, p + 4, nullptr, nullptr, LORES_MXFP4, p, u, p), "block odd");
         OK(go(p, p, p, p, LORES_INT8, p, f, p), "block vec");
         BAD(go(p, p, p, p, LORES_INT8, p, nullptr, p));
         BAD(go(p, p, p, p, LORES_FP8, p, p + 2, p));
@@ -156,7 +156,7 @@ int main() {
         d.gate_stride = 0;
         OK(go(p, p, p, p, LORES_FP32, p, nullptr, p), "block vec");
         d.gate_stride = 65;
-        OK(go(p, p, p, p, LORES_FP32, p, nullptr, p), "block any");
+        OK(go(p, p, p, p, LORES_FP32, p, nullptr, p), "block odd");
         d.gate_stride = 63; BAD(go(p, p, p, p, LORES_FP32, p, nullptr, p));
         fresh(); d.x_stride = (int64_t)1 << 41; BAD(go(p, p, p, p, LORES_FP32, p, nullptr, p));
         fresh(); d.scale = INFINITY; BAD(go(p, p, p, p, LORES_FP32, p, nullptr, p));
@@ -170,7 +170,7 @@ int main() {
         };
         OK(back(p, p, p, p, f, n), "block back vec");
         OK(back(p, nullptr, nullptr, nullptr, nullptr, n), "block back vec");
-        OK(back(p + 4, p, p, p, f, n), "block back any");
+        OK(back(p + 4, p, p, p, f, n), "block back odd");
         BAD(back(p, p, p, nullptr, f, n));
         BAD(back(p, p, p, p, nullptr, n));
         BAD(back(nullptr, p, p, p, f, n));
