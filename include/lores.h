@@ -513,8 +513,7 @@ int lores_rmsnorm_backward(const void *h, int64_t h_stride, const void *weight, 
  * computed.  Sums are fp32, results are rounded once, and do not depend on
  * scheduling.  The gradients are those of the formula before its rounding.  At
  * eps = 0 a row of zeros has an infinite r, and its y are NaN (4-bit rows: 0).
- * An input of a call may be one of its outputs where the two have the same
- * layout, for x (or h), the gate, the residual, dy and dh.
+ * No output may overlap an input or another output.
  */
 
 /* Shapes of a gated norm: rows (token, head) of n elements.  Strides are in
@@ -617,8 +616,8 @@ int lores_block_norm_backward(const lores_block_dims *dims, const void *x, const
  * scale 2^e, the smallest power of two (e >= -127) with max |x| < 7 2^e, and
  * each is x 2^-e rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to
  * the even code; the largest is rounded, never cut off).
- *   x       device [rows][n], in_bf16 ? bf16 : fp32, rows x_stride elements apart;
- *           n a multiple of 32 up to 2^24, 0 <= rows < 2^31, rows x n at most 2^38
+ *   x       device [rows][n], in_bf16 ? bf16 : fp32, rows x_stride (0 or at least n)
+ *           elements apart; n a multiple of 32 up to 2^24, 0 <= rows < 2^31, rows x n at most 2^38
  *   codes   device out [rows][n / 2], 16-byte aligned: code c of column j in bits
  *           4 (j & 1) .. of byte j / 2, its sign in bit 3
  *   scales  device out [rows][4 ceil(n / 128)]: e + 127 of block j / 32, 0 behind the

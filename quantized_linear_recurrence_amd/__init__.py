@@ -582,6 +582,8 @@ def _rows_of(t, name, kept):
         return st[0] if shape[0] != 1 else None, st[1:-1]
     step, size = None, 1
     for d in range(lead - 1, -1, -1):
+        if shape[d] == 0:
+            return None, st[lead:-1]
         if shape[d] == 1:
             continue
         if step is None:
@@ -625,11 +627,26 @@ def _warn_graph(what, *ts):
         _no_graph(what)
 
 
+def _like(x):
+    """An uninitialised contiguous tensor of x's shape and type (empty_like takes the host
+    1.1 us, new_empty 1.7)."""
+    import torch
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
+def _rows2(t, lead, n, dtype):
+    """An uninitialised contiguous tensor [*lead, n] on t's device (empty_strided: 1.3 us)."""
+    import torch
+    if len(lead) == 1:
+        return torch.empty_strided((lead[0], n), (n, 1), dtype=dtype, device=t.device)
+    return t.new_empty((*lead, n), dtype=dtype)
+
+
 def _mx_pair(t, lead, n):
     """Tensors for rows of n 4-bit values: codes and scales."""
     import torch
     u8 = torch.uint8
-    return (t.new_empty((*lead, n // 2), dtype=u8), t.new_empty((*lead, (n + 127) // 128 * 4), dtype=u8))
+    return _rows2(t, lead, n // 2, u8), _rows2(t, lead, (n + 127) // 128 * 4, u8)
 
 
 def _out_prec(out_prec, in_bf16, allowed):
@@ -686,7 +703,7 @@ def lores_gated_norm(x, gate, weight, eps, act=LORES_ACT_SILU, gate_first=False,
     def call():
         scales = sp = None
         if same:
-            y = x.new_empty(x.shape)
+            y = _like(x)
         elif dt is None:
             y, scales = _mx_pair(x, x.shape[:-2], d.heads * d.n)
             sp = scales.data_ptr()
@@ -709,7 +726,7 @@ def lores_gated_norm_backward(x, gate, weight, dy, eps, act=LORES_ACT_SILU, gate
     _check(_lib.lib().lores_gated_norm_workspace(d, ctypes.byref(size)))
 
     def call():
-        dx, dgate = x.new_empty(x.shape), x.new_empty(x.shape)
+        dx, dgate = _like(x), _like(x)
         dw = x.new_empty(weight.shape, dtype=torch.float32)
         work = x.new_empty(size.value, dtype=torch.uint8)
         _check(_lib.lib().lores_gated_norm_backward(d, xp, gp, wp, dyp, dx.data_ptr(), dgate.data_ptr(),
@@ -762,9 +779,9 @@ def lores_block_norm(x, residual, weight, weight_next, eps, scale=1.0, gate=None
 
     def call():
         scales = sp = None
-        h = x.new_empty(x.shape)
+        h = _like(x)
         if same:
-            y = x.new_empty(x.shape)
+            y = _like(x)
         elif dt is None:
             y, scales = _mx_pair(x, x.shape[:-1], d.n)
             sp = scales.data_ptr()
@@ -795,8 +812,8 @@ def lores_block_norm_backward(x, h, weight, weight_next, dy, eps, scale=1.0, gat
     _check(_lib.lib().lores_block_norm_workspace(d, ctypes.byref(size)))
 
     def call():
-        dx, dres = x.new_empty(x.shape), x.new_empty(x.shape)
-        dgate = None if gate is None else x.new_empty(x.shape)
+        dx, dres = _like(x), _like(x)
+        dgate = None if gate is None else _like(x)
         dwn = x.new_empty(d.n, dtype=torch.float32)
         dw = None if weight is None else torch.empty_like(dwn)
         work = x.new_empty(size.value, dtype=torch.uint8)
@@ -871,7 +888,7 @@ def lores_mx_dequant(codes, scales, dtype=None, stream=None):
     cp, sp, rows, n = _mx_rows(codes, scales, "codes")
 
     def call():
-        out = codes.new_empty((*codes.shape[:-1], n), dtype=dtype)
+        out = _rows2(codes, codes.shape[:-1], n, dtype)
         _check(_lib.lib().lores_mx_dequant(cp, sp, rows, n, dtype is torch.bfloat16, out.data_ptr(),
                                            _queue(codes.device)))
         return out
@@ -918,7 +935,7 @@ def lores_mx_matmul(a, a_scales, w, w_scales, out_prec=LORES_BF16, out=None, str
 
     def call():
         if out is None:
-            y = w.new_empty((*lead, N), dtype=dt)
+            y = _rows2(w, lead, N, dt)
             yp = y.data_ptr()
         else:
             y, yp = out, _need(out, "out", dt, (*lead, N), device)

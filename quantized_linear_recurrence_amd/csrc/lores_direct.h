@@ -22,9 +22,6 @@ __device__ __forceinline__ void direct16(const void *src, uint32_t lane_at, void
                  :: "v"(lane_at), "s"(src), "s"(at) : "memory");
 }
 __device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-// Waits until at most N of the wavefront's loads are on their way: they arrive in order.
-template <int N>
-__device__ __forceinline__ void arrived_but() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
 
 }  // namespace
 }  // namespace lores

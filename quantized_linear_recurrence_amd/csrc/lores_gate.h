@@ -20,7 +20,8 @@ __device__ __forceinline__ float sigmoid(float z) {
         const float t = m * log2e;
         const float lo = fmaf(m, 0x1.4ae0cp-26f, fmaf(m, log2e, -t));   // log2 e = log2e + 0x1.4ae0cp-26
         const float e = __builtin_amdgcn_exp2f(t);
-        const float s = __builtin_amdgcn_rcpf(1.0f + fmaf(e, lo * 0x1.62e43p-1f, e));
+        // (a product, whose infinite e stays one whatever lo's sign)
+        const float s = __builtin_amdgcn_rcpf(1.0f + e * fmaf(lo, 0x1.62e43p-1f, 1.0f));
         return z != z ? z : s;
     }
 }

@@ -44,7 +44,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_kernel(cons
             w[i][e] = a.gate_first ? w[i][e] : w[i][e] * g;
         }
     sum = row_sum<TPR>(sum, sm);
-    const float rstd = 1.0f / sqrtf(sum / (float)a.n + a.eps);
+    float rstd = 1.0f / sqrtf(sum / (float)a.n + a.eps);
+    // (without an epsilon the r of a row of zeros is an infinity: its codes are 0)
+    if (a.out_prec == LORES_MXFP4 && sum == 0.0f) rstd = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -55,12 +57,6 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_kernel(cons
         store_row<uint16_t, TPR, VPT, VEC>((uint16_t *)a.y + row * a.n, t, a.n, x);
     } else {                                         // a token's heads are one row of blocks
         const int per = mx_scale_stride((int64_t)a.heads * a.n), blocks = a.n / 32;
-        if (sum == 0.0f) {                           // (without an epsilon r is an infinity)
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
-        }
         store_mx<TPR, VPT>((uint8_t *)a.y + row * (a.n / 2), a.scales + (int64_t)token * per + head * blocks,
                            head + 1 == (uint32_t)a.heads ? per - a.heads * blocks : 0, t, a.n,
                            !(sum < __builtin_inff()), x);

@@ -310,7 +310,8 @@ int lores_mx_quant(const void *x, int64_t x_stride, int64_t rows, int32_t n, int
     if (!aligned(x, el)) return fail(LORES_EINVAL, "x must be aligned to its element size");
     if (!aligned(codes, 16) || !aligned(scales, 4))
         return fail(LORES_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
-    if (x_stride < n || x_stride > kMaxStride) return fail(LORES_EINVAL, "rows must be n to 2^40 elements apart");
+    if ((x_stride < n && x_stride != 0) || x_stride > kMaxStride)
+        return fail(LORES_EINVAL, "rows must be 0, or n to 2^40, elements apart");
     lores::MxRows a;
     std::memset(&a, 0, sizeof a);
     a.rows = rows;

@@ -186,7 +186,9 @@ int main() {
         OK(quant(p + 2, 64, 4, 64, 1, u, u), "quant");
         OK(quant(p, 65, 4, 64, 1, u, u), "quant");
         OK(quant(nullptr, 64, 0, 64, 0, nullptr, nullptr), "");
+        OK(quant(p, 0, 4, 64, 1, u, u), "quant vec");
         BAD(quant(p, 63, 4, 64, 0, u, u));
+        BAD(quant(p, -64, 4, 64, 0, u, u));
         BAD(quant(p, 64, 4, 48, 0, u, u));
         BAD(quant(p, 64, 4, 0, 0, u, u));
         BAD(quant(p, 64, -1, 64, 0, u, u));

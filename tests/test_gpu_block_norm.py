@@ -190,6 +190,16 @@ def test_streams_empty_calls_and_graph():
     assert dx.shape == dres.shape == dg.shape == (0, 512) and (dw == 0).all() and (dwn == 0).all()
 
 
+def test_batches_of_no_rows():
+    w = weight((96,), BF16, 1)
+    for shape in ((3, 0, 96), (0, 3, 96), (0, 96), (2, 3, 0, 96)):
+        e = torch.empty(shape, dtype=BF16, device=dev())
+        y, _, h = lores.lores_block_norm(e, e, w, w, EPS, gate=e)
+        assert y.shape == h.shape == shape
+        dx, dres, dgate, dw, dwn = lores.lores_block_norm_backward(e, e, w, w, e, EPS, gate=e)
+        assert dx.shape == dgate.shape == shape and (dw == 0).all() and (dwn == 0).all()
+
+
 def test_refusals():
     x, w = randn((4, 64), F32, 40), weight((64,), F32, 41)
     for bad in ((x.half(), None, w, w), (x, None, w.half(), w), (x, None, w, w.half()), (None, x, w, w), (x, x, w, None),

@@ -137,6 +137,32 @@ def test_far_gates(dtype):
         assert ((rz - dz.double().cpu()).abs() <= TOL[dtype] * rz.abs() + 2.0 ** -20).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_every_gate_has_a_value(dtype):
+    """Gates on both sides of where the exponential leaves fp32's range (88.7), densely."""
+    z = torch.linspace(-160.0, 160.0, 8192, device=dev()).to(dtype).view(64, 1, 128)
+    x, w, dy = randn((64, 1, 128), dtype, 64), weight((128,), dtype, 65), randn((64, 1, 128), dtype, 66)
+    for kind in ("silu", "sigmoid"):
+        for first in (False, True):
+            args = arr(x), arr(z), arr(w)
+            y, _ = lores.lores_gated_norm(x, z, w, EPS, act=ACTS[kind], gate_first=first, out_prec=lores.LORES_FP32)
+            want = torch.from_numpy(layer.gated_norm(*args, EPS, kind, first))
+            # gated first, a row of gates of 2^-100 is one that is scaled up by 2^10 (eps 2^-20)
+            assert ((want - y.double().cpu()).abs() <= TOL[dtype] * want.abs() + 2.0 ** -90).all()
+            dx, dz, _ = lores.lores_gated_norm_backward(x, z, w, dy, EPS, act=ACTS[kind], gate_first=first)
+            assert torch.isfinite(dx).all() and torch.isfinite(dz).all()
+
+
+def test_a_gate_without_a_value_in_a_row_of_zeros():
+    x, z, w = torch.zeros(2, 2, 64, device=dev()), randn((2, 2, 64), F32, 74), weight((64,), F32, 75)
+    z[1, 1, 40] = float("nan")                       # 0 times NaN
+    for eps in (EPS, 0.0):
+        c, s = lores.lores_gated_norm(x, z, w, eps, out_prec=lores.LORES_MXFP4)
+        assert s[1, 3] == 255 and (c & 0x77 == 0).all()
+        s[1, 3] = 0
+        assert (s == 0).all()
+
+
 def test_values_that_are_not_finite():
     x, z, w = randn((6, 1, 64), F32, 71), randn((6, 1, 64), F32, 72), weight((64,), F32, 73)
     z[0, 0, 3] = float("inf")                        # s = 1
@@ -179,6 +205,10 @@ def test_streams_empty_calls_and_inputs_left_alone():
         assert y.shape == (0, 256) and sc.shape == (0, 16)
         dx, dz, dw = lores.lores_gated_norm_backward(x[:0], z[:0], w0, x[:0], EPS)
         assert dx.shape == dz.shape == (0, 4, 128) and dw.shape == w0.shape and (dw == 0).all()
+    for shape in ((3, 0, 4, 128), (0, 3, 4, 128), (2, 3, 0, 4, 128)):
+        e = x.new_empty(shape)
+        assert lores.lores_gated_norm(e, e, w, EPS)[0].shape == shape
+        assert lores.lores_gated_norm_backward(e, e, w, e, EPS)[0].shape == shape
 
 
 def test_replayed_graph():

@@ -225,6 +225,32 @@ def test_streams_graph_and_empty_calls():
     assert a.shape == (0, 128) and s.shape == (0, 8)
     assert lores.lores_mx_dequant(a, s).shape == (0, 256)
     assert lores.lores_mx_matmul(a, s, wc, ws).shape == (0, 96)
+    a, s = lores.lores_mx_quant(x.new_empty(5, 0, 256))
+    assert a.shape == (5, 0, 128) and lores.lores_mx_matmul(a, s, wc, ws).shape == (5, 0, 96)
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls share nothing: interleaved on two streams they give what each gives alone."""
+    w = [mx((520, 1056), 40 + i)[:2] for i in range(2)]
+    x = [randn((m, 1056), BF16, 42 + i) for i, m in enumerate((300, 40))]
+    want = [lores.lores_mx_matmul(*lores.lores_mx_quant(x[i]), *w[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(side[i]):
+                got.append((i, lores.lores_mx_matmul(*lores.lores_mx_quant(x[i]), *w[i])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i, y in got)
+
+
+def test_one_row_for_all():
+    """Rows that lie no step apart are read as often as they stand there."""
+    x = randn((1, 320), BF16, 45)
+    a, s = lores.lores_mx_quant(x.expand(7, 320))
+    one = lores.lores_mx_quant(x)
+    assert torch.equal(a, one[0].expand(7, 160)) and torch.equal(s, one[1].expand(7, 12))
 
 
 def test_refusals():
