@@ -179,20 +179,25 @@ hipError_t go_few(const MxProduct &p, hipStream_t s) {
 // ------------------------------------------------------------ many rows
 //
 // A work-group has WM x WN wavefronts, each with 16 MI rows and 16 NI columns in
-// registers.  Stages of 256 k go from memory straight to LDS, two stages deep:
-// 128 bytes of a 4-bit row, a whole line of the cache (64 bytes at a time, loads alone
-// took 93 instead of 67 us of 8192 x 8192 x 4096).  E4M3 rows have 128 bytes in each of
-// the stage's two steps of 128 k.  A row's 8 pieces of 16 bytes are turned by the row, so
-// that 8 neighbouring rows read their like pieces from different banks.  Scales
-// come through registers, 4 steps of a row in a thread, and are turned over in LDS so
-// that a lane has its block's of 4 steps in one register, where the instruction
-// selects one (read byte by byte from LDS they took 26 of the 65 us of all its reads).
+// registers.  Stages of 128 bytes a row, a whole line of the cache, go from memory straight
+// to LDS, two stages deep (64 bytes at a time, loads alone took 93 instead of 67 us of
+// 8192 x 8192 x 4096): 256 k of 4-bit rows, 128 k of E4M3 rows.  A row's 8 pieces of 16
+// bytes are turned by the row, so that 8 neighbouring rows read their like pieces from
+// different banks.  Scales come through registers, 4 steps of 128 k of a row in a thread,
+// and are turned over in LDS so that a lane has its block's of 4 steps in one register,
+// where the instruction selects one (read byte by byte from LDS they took 26 of the 65 us
+// of all its reads).
+//
+// A step of the largest tile, 256 x 256, takes LDS 768 cycles of reads and 256 of writes for
+// 4-bit rows, as many as the matrix instructions take (1024 and 384 of 2048 for E4M3
+// rows; a tile of 128 x 256 takes 1024 of 1024): 8192 x 8192 x 16384 runs at 4.7, E4M3 rows
+// at 3.0 of the 6.7 and 4.3 PFLOP/s that the instructions reach alone.
 //
 // A work-group goes through several tiles as one stream of stages: while a tile's
 // outputs are written, the next one's first stages are on their way.
 template <bool FP8, int TM, int TN, int NW>
 struct Shared {
-    uint8_t w[2][TN * 128], a[2][FP8 ? 2 : 1][TM * 128];        // (a place's offset fits a read's own field)
+    uint8_t w[2][TN * 128], a[2][TM * 128];        // (a place's offset fits a read's own field)
     uint32_t sc[TN + (FP8 ? 0 : TM)][4];
     uint8_t out[NW][2048];
 };
@@ -228,9 +233,12 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     constexpr int TM = 16 * MI * WM, TN = 16 * NI * WN, NW = WM * WN;
     constexpr int LW = TN / 8 / NW, LA = TM / 8 / NW;           // a wavefront's loads of 8 rows
     constexpr int SR = TN + (FP8 ? 0 : TM);                     // rows of scales: the columns', the rows'
-    constexpr int PARTS = NI == 8 ? 4 : 2, NH = NI / PARTS;     // columns are taken in parts
+    constexpr int PARTS = NI < 8 ? 2 : FP8 ? 8 : 4, NH = NI / PARTS;      // columns are taken in parts
+    // Steps of rows in registers.  Two leave the next step's time to arrive, but E4M3 rows
+    // with 8 x 4 outputs do not fit (75 registers spilled); one costs 4-bit rows a quarter.
+    constexpr int RB = FP8 && NI == 8 ? 1 : 2;
     static_assert(LW * NW * 8 == TN && LA * NW * 8 == TM && SR <= 64 * NW, "every load and scale has its lane");
-    static_assert(TN % 64 == 0, "a wavefront has scales of rows or of columns");
+    static_assert(TN % 64 == 0 && TM % 64 == 0, "a wavefront has scales of rows or of columns");
     __shared__ __attribute__((aligned(1024))) Shared<FP8, TM, TN, NW> sh;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int wm = wv % WM, wn = wv / WM;
@@ -244,8 +252,8 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     const int piece = (lane & 7) ^ (lane >> 3);      // a lane's of its row, the same in all its loads
 
     // ---- where a tile's operands lie; the tile that is multiplied and the next one
-    const int srow = SR == 64 * NW ? threadIdx.x : min((int)threadIdx.x, SR - 1);
-    const bool of_w = FP8 || wv < TN / 64;
+    const int srow = threadIdx.x % SR;               // (with fewer rows than threads some come twice)
+    const bool of_w = FP8 || wv % (SR / 64) < TN / 64;
     struct Aim {
         int64_t m0;
         int n0;
@@ -280,21 +288,20 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
         x.sat *= per;
     };
     Aim now, then;
-    // stage j of a tile into place j & 1
-    auto load = [&](int j, const Aim &x) {
-        uint8_t *const tw = sh.w[j & 1], *const ta = sh.a[j & 1][0];
-        const uint32_t kw = 256 * j + 32 * piece < p.K ? j * 128 + piece * 16 : 0;
+    // stage j of a tile's columns, or of its rows, into place j & 1
+    auto load_columns = [&](int j, const Aim &x) {
+        const uint32_t k = 256 * j + 32 * piece < p.K ? j * 128 + piece * 16 : 0;
 #pragma unroll
         for (int i = 0; i < LW; ++i)
-            direct16(uniform(x.w + (FULL ? (int64_t)(i * NW * 8) * wrow : 0)), x.wat[FULL ? 0 : i] + kw, tw + (wv + i * NW) * 1024);
+            direct16(uniform(x.w + (FULL ? (int64_t)(i * NW * 8) * wrow : 0)), x.wat[FULL ? 0 : i] + k,
+                     sh.w[j & 1] + (wv + i * NW) * 1024);
+    };
+    auto load_rows = [&](int j, const Aim &x) {
+        const uint32_t k = (FP8 ? 128 : 256) * j + (FP8 ? 16 : 32) * piece < p.K ? j * 128 + piece * 16 : 0;
 #pragma unroll
-        for (int h = 0; h < (FP8 ? 2 : 1); ++h) {
-            const uint32_t ka = !FP8 ? kw : 256 * j + 128 * h + 16 * piece < p.K ? 256 * j + 128 * h + 16 * piece : 0;
-#pragma unroll
-            for (int i = 0; i < LA; ++i)
-                direct16(uniform(x.a + (FULL ? (int64_t)(i * NW * 8) * arow : 0)), x.aat[FULL ? 0 : i] + ka,
-                         ta + (h * TM / 8 + wv + i * NW) * 1024);
-        }
+        for (int i = 0; i < LA; ++i)
+            direct16(uniform(x.a + (FULL ? (int64_t)(i * NW * 8) * arow : 0)), x.aat[FULL ? 0 : i] + k,
+                     sh.a[j & 1] + (wv + i * NW) * 1024);
     };
     // a row's scales in a thread: steps 4 b .. 4 b + 3 (those behind the row's end are
     // made 0 where they are used: used here they would be waited for)
@@ -321,13 +328,13 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
         const uint32_t lo1 = __builtin_amdgcn_perm(sq[3], sq[2], 0x05010400u), hi1 = __builtin_amdgcn_perm(sq[3], sq[2], 0x07030602u);
         const u32x4 t = {__builtin_amdgcn_perm(lo1, lo0, 0x05040100u), __builtin_amdgcn_perm(lo1, lo0, 0x07060302u),
                          __builtin_amdgcn_perm(hi1, hi0, 0x05040100u), __builtin_amdgcn_perm(hi1, hi0, 0x07060302u)};
-        if (SR == 64 * NW || (int)threadIdx.x < SR) *(u32x4 *)sh.sc[srow] = t;
+        *(u32x4 *)sh.sc[srow] = t;
     };
     int rs[MI], cs[NI];
     auto read_row_scales = [&](int (&x)[MI], int b) {
         // E4M3: 1, but 0 behind K (byte s: block 16 b + 4 s + g)
-        const int left = p.K / 32 - 16 * b - g;
-        const int one = left > 12 ? 0x7f7f7f7f : left > 8 ? 0x7f7f7f : left > 4 ? 0x7f7f : left > 0 ? 0x7f : 0;
+        const int none = 16 - min(max(p.K / 32 - 16 * b - g + 3, 0) & ~3, 16);      // 4 bits for each half byte of 0
+        const int one = (0x7f7f7f7f >> none) >> none;
 #pragma unroll
         for (int i = 0; i < MI; ++i) x[i] = FP8 ? one : sh.sc[(FP8 ? 0 : TN) + (wm * MI + i) * 16 + r][g];
     };
@@ -336,19 +343,15 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
         for (int i = part * NH; i < (part + 1) * NH; ++i) cs[i] = sh.sc[(wn * NI + i) * 16 + r][g];
     };
 
-    // ---- operands: a wavefront's rows of a step, and a part of its columns at a time
-    struct Rows { i32x4 x[MI][FP8 ? 2 : 1]; };
+    // ---- operands: a wavefront's rows of a step or two, and a part of its columns at a time
+    i32x4 a[RB][MI][FP8 ? 2 : 1];
     struct Columns { i32x4 x[NH]; };
     // places in a stage, but for constants: like pieces of rows 16 apart are turned alike
     const int turn = r & 7, wplace = (wn * NI * 16 + r) * 128, aplace = (wm * MI * 16 + r) * 128;
-    auto read_rows = [&](auto Q, Rows &o) {          // of step Q of 4
-        const uint8_t *a = sh.a[Q() >> 1][FP8 ? Q() & 1 : 0] + aplace;
-        const int at = FP8 ? g : 4 * (Q() & 1) + g;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            o.x[i][0] = *(const i32x4 *)(a + (at ^ turn) * 16 + i * 2048);
-            if constexpr (FP8) o.x[i][1] = *(const i32x4 *)(a + ((4 + g) ^ turn) * 16 + i * 2048);
-        }
+    auto read_row = [&](auto Q, int i) {             // of step Q of 4
+        const uint8_t *p = sh.a[FP8 ? Q() & 1 : Q() >> 1] + aplace + i * 2048;
+        a[Q() % RB][i][0] = *(const i32x4 *)(p + ((FP8 ? g : 4 * (Q() & 1) + g) ^ turn) * 16);
+        if constexpr (FP8) a[Q() % RB][i][1] = *(const i32x4 *)(p + ((4 + g) ^ turn) * 16);
     };
     auto read_columns = [&](auto Q, int part, Columns &o) {
         const uint8_t *w = sh.w[Q() >> 1] + wplace + ((4 * (Q() & 1) + g) ^ turn) * 16;
@@ -356,35 +359,36 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
         for (int i = 0; i < NH; ++i) o.x[i] = *(const i32x4 *)(w + (part * NH + i) * 2048);
     };
     f32x4 c[MI][NI];
-    auto multiply = [&](auto Q, const Rows &a, const Columns &w, int part) {
+    auto multiply_row = [&](auto Q, int i, const Columns &w, int part) {
+        i32x8 x = {a[Q() % RB][i][0][0], a[Q() % RB][i][0][1], a[Q() % RB][i][0][2], a[Q() % RB][i][0][3], 0, 0, 0, 0};
+        if constexpr (FP8)
+            x = i32x8{a[Q() % RB][i][0][0], a[Q() % RB][i][0][1], a[Q() % RB][i][0][2], a[Q() % RB][i][0][3],
+                      a[Q() % RB][i][1][0], a[Q() % RB][i][1][1], a[Q() % RB][i][1][2], a[Q() % RB][i][1][3]};
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            i32x8 x = {a.x[i][0][0], a.x[i][0][1], a.x[i][0][2], a.x[i][0][3], 0, 0, 0, 0};
-            if constexpr (FP8)
-                x = i32x8{a.x[i][0][0], a.x[i][0][1], a.x[i][0][2], a.x[i][0][3],
-                          a.x[i][1][0], a.x[i][1][1], a.x[i][1][2], a.x[i][1][3]};
-#pragma unroll
-            for (int j = 0; j < NH; ++j) {
-                const i32x8 y = {w.x[j][0], w.x[j][1], w.x[j][2], w.x[j][3], 0, 0, 0, 0};
-                c[i][part * NH + j] = product<FP8, Q()>(y, x, c[i][part * NH + j], cs[part * NH + j], rs[i]);
-            }
+        for (int j = 0; j < NH; ++j) {
+            const i32x8 y = {w.x[j][0], w.x[j][1], w.x[j][2], w.x[j][3], 0, 0, 0, 0};
+            // (so that the sum stays in its registers: else spills; with two steps of rows it costs time)
+            if constexpr (RB == 1) asm("" : "+v"(c[i][part * NH + j]));
+            c[i][part * NH + j] = product<FP8, Q()>(y, x, c[i][part * NH + j], cs[part * NH + j], rs[i]);
         }
+    };
+    auto multiply = [&](auto Q, const Columns &w, int part) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) multiply_row(Q, i, w, part);
     };
     auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
     // the end of a stage: this wavefront's reads of it are done and its loads of the next
-    // one have landed; behind the barrier that holds for all wavefronts
-    auto meet = [] {
-        arrived();
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // one, all but the last `but`, have landed; behind the barrier that holds for all wavefronts
+    auto meet = [](auto but) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(but()) : "memory");
     };
-    Rows a[2];
     Columns w[2];
     // step Q of 4: a part's products run while the next part's operands are read.  Every
-    // second step ends a stage, whose place takes the stage after the next one of the
-    // stream.  Scales of the next four steps: asked for at Q = 0 (in the same turn of the
+    // second step (E4M3 rows: every one) ends a stage, whose place takes the stage after
+    // the next one of the stream.  Scales of the next four steps: asked for at Q = 0 (in the same turn of the
     // loop as their use: carried over its end they are copied, and waited for), turned
     // over into LDS at Q = 1, where those of these four have been read, and read at Q = 3.
-    auto step = [&](auto Q, int b, const Rows &cur, Rows &next) {
+    auto step = [&](auto Q, int b) {
         constexpr std::integral_constant<int, (Q() + 1) & 3> N{};
         int nr[MI];
         if constexpr (Q() == 0) fetch_scales(b + 1 < groups ? b + 1 : 0, b + 1 < groups ? now : then);
@@ -392,24 +396,42 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
         for (int q = 0; q < PARTS - 1; ++q) {
             read_columns(Q, q + 1, w[(q + 1) & 1]);
             fence();
-            multiply(Q, cur, w[q & 1], q);
+            multiply(Q, w[q & 1], q);
             fence();
         }
-        if constexpr ((Q() & 1) != 0) {
-            meet();
-            const int j = 2 * b + (Q() >> 1) + 2;
-            load(j < 2 * groups ? j : j - 2 * groups, j < 2 * groups ? now : then);
-            if constexpr (Q() == 1) turn_scales();
+        if constexpr (FP8 || (Q() & 1) != 0) {
+            // inside a stage of columns the next one, and at Q = 0 at least one load of
+            // scales, may be on their way still: they are behind the rows
+            constexpr bool COLS = (Q() & 1) != 0;
+            meet(std::integral_constant<int, COLS ? 0 : LW + (Q() == 0)>{});
+            if constexpr (Q() == 1) {                // (before the next loads, which its wait would take in)
+                turn_scales();
+                fence();
+            }
+            const int j = 2 * b + (Q() >> 1) + 2, all_j = 2 * groups;
+            const int jr = FP8 ? 4 * b + Q() + 2 : j, all_r = FP8 ? 4 * groups : all_j;
+            load_rows(jr < all_r ? jr : jr - all_r, jr < all_r ? now : then);
+            if constexpr (COLS) load_columns(j < all_j ? j : j - all_j, j < all_j ? now : then);
             if constexpr (Q() == 3) {
                 read_row_scales(nr, b + 1 < groups ? b + 1 : 0);
 #pragma unroll
                 for (int q = 0; q < PARTS - 1; ++q) read_column_scales(q);
             }
         }
-        read_rows(N, next);
+        if constexpr (RB == 2)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) read_row(N, i);
         read_columns(N, 0, w[0]);
         fence();
-        multiply(Q, cur, w[1], PARTS - 1);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            multiply_row(Q, i, w[1], PARTS - 1);
+            if constexpr (RB == 1) {                 // into the registers that the last products leave
+                fence();
+                read_row(N, i);
+                fence();
+            }
+        }
         fence();
         if constexpr (Q() == 3) {
 #pragma unroll
@@ -420,15 +442,18 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
 
     aim(tile, now);
     fetch_scales(0, now);
-    load(0, now);
+    load_rows(0, now);
+    load_columns(0, now);
     arrived();
     turn_scales();
-    load(1, now);
+    load_rows(1, now);
+    load_columns(1, now);
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     read_row_scales(rs, 0);
 #pragma unroll
     for (int q = 0; q < PARTS; ++q) read_column_scales(q);
-    read_rows(std::integral_constant<int, 0>(), a[0]);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) read_row(std::integral_constant<int, 0>(), i);
     read_columns(std::integral_constant<int, 0>(), 0, w[0]);
     for (; tile < run_end; tile += round) {
         aim(tile + round < run_end ? tile + round : tile, then);     // (behind the last one: itself, loaded in vain)
@@ -437,10 +462,10 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
 #pragma unroll
             for (int j = 0; j < NI; ++j) c[i][j] = f32x4{};
         for (int b = 0; b < groups; ++b) {           // (behind K: zeros)
-            step(std::integral_constant<int, 0>(), b, a[0], a[1]);
-            step(std::integral_constant<int, 1>(), b, a[1], a[0]);
-            step(std::integral_constant<int, 2>(), b, a[0], a[1]);
-            step(std::integral_constant<int, 3>(), b, a[1], a[0]);
+            step(std::integral_constant<int, 0>(), b);
+            step(std::integral_constant<int, 1>(), b);
+            step(std::integral_constant<int, 2>(), b);
+            step(std::integral_constant<int, 3>(), b);
         }
         const int64_t m = now.m0 + wm * MI * 16;
         const int n = now.n0 + wn * NI * 16;
@@ -501,21 +526,20 @@ hipError_t go_tile(const MxProduct &p, int residents, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Tiles of 64 x 64 while they run at once (three of 4-bit rows on a CU), of 128 x 128 while
-// those do (two; one of E4M3 rows), else the largest that LDS and registers hold.  us at
-// K = 4096, 64 x 64 / 128 x 128 / largest:
-//   outputs         512 x 4096        512 x 8192       1024 x 8192       2048 x 8192
-//   4-bit rows   14.4 14.9 29.2    25.6 17.2 30.4    40.9 26.4 33.0    73.3 48.7 40.5
-//   E4M3 rows    17.7 24.4 30.5    31.6 27.6 31.6    57.5 49.8 37.4   103.2 92.1 67.2
+// Tiles of 64 x 64 while they run at once (three on a CU), of 128 x 128 while those do
+// (two; of E4M3 rows while each has its CU), of E4M3 rows 128 x 256 while those do, else
+// 256 x 256.  us at K = 4096, 64 x 64 / 128 x 128 / 128 x 256 / 256 x 256:
+//   outputs           512 x 4096           512 x 8192          1024 x 8192          1536 x 8192
+//   4-bit rows   14.2 15.3 19.6 27.1  24.8 17.6 20.8 27.8  40.2 25.1 25.5 30.7  56.6 38.4 40.4 34.7
+//   E4M3 rows    18.2 21.8 26.5 42.1  31.2 24.2 28.2 42.8  53.7 45.0 34.1 45.9  73.9 63.1 55.7 50.8
 template <bool FP8, bool BF16, bool X4>
 hipError_t go_tiles(const MxProduct &p, hipStream_t s) {
     const int64_t cells = p.M * p.N;
-    if (p.M >= 256 && p.N >= 256 && cells > (FP8 ? 1 << 22 : 1 << 23)) {
-        if constexpr (FP8) return go_tile<FP8, BF16, true, X4, 4, 4, 2, 4>(p, 256, s);
-        else return go_tile<FP8, BF16, true, X4, 4, 8, 4, 2>(p, 256, s);
-    }
-    if (cells <= 1 << 21) return go_tile<FP8, BF16, false, X4, 2, 2, 2, 2>(p, FP8 ? 512 : 768, s);
-    return go_tile<FP8, BF16, false, X4, 4, 4, 2, 2>(p, FP8 ? 256 : 512, s);
+    if (p.M >= 256 && p.N >= 256 && cells > 1 << 23) return go_tile<FP8, BF16, true, X4, 4, 8, 4, 2>(p, 256, s);
+    if constexpr (FP8)
+        if (p.M >= 256 && p.N >= 256 && cells > 1 << 22) return go_tile<FP8, BF16, true, X4, 4, 4, 2, 4>(p, 256, s);
+    if (cells <= 1 << 21) return go_tile<FP8, BF16, false, X4, 2, 2, 2, 2>(p, 768, s);
+    return go_tile<FP8, BF16, false, X4, 4, 4, 2, 2>(p, 512, s);
 }
 
 // Few rows: the fewest rows a work-group (16, 32 or 64) with which there are at most 256
