@@ -190,7 +190,7 @@ hipError_t go_few(const MxProduct &p, hipStream_t s) {
 //
 // A step of the largest tile, 256 x 256, takes LDS 768 cycles of reads and 256 of writes for
 // 4-bit rows, as many as the matrix instructions take (1024 and 384 of 2048 for E4M3
-// rows; a tile of 128 x 256 takes 1024 of 1024): 8192 x 8192 x 16384 runs at 4.7, E4M3 rows
+// rows; a tile of 128 x 256 takes 1024 of 1024): 8192 x 8192 x 16384 runs at 4.8, E4M3 rows
 // at 3.0 of the 6.7 and 4.3 PFLOP/s that the instructions reach alone.
 //
 // A work-group goes through several tiles as one stream of stages: while a tile's
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     // with 8 x 4 outputs do not fit (75 registers spilled); one costs 4-bit rows a quarter.
     constexpr int RB = FP8 && NI == 8 ? 1 : 2;
     static_assert(LW * NW * 8 == TN && LA * NW * 8 == TM && SR <= 64 * NW, "every load and scale has its lane");
+    static_assert(FULL || NI < 8, "the largest tiles are whole");
     static_assert(TN % 64 == 0 && TM % 64 == 0, "a wavefront has scales of rows or of columns");
     __shared__ __attribute__((aligned(1024))) Shared<FP8, TM, TN, NW> sh;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -500,7 +501,11 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
                         const u32x4 x = *(const u32x4 *)(own + (at * CH + (ch ^ (at & (CH - 1)))) * 16);
                         const int64_t mm = m + 16 * i + at;
                         const int nn = n + 16 * h + ch * E;
-                        if (FULL || (mm < p.M && nn < p.N)) *(u32x4 *)((uint8_t *)p.out + (mm * p.N + nn) * (16 / E)) = x;
+                        Global<u32x4> *to = (Global<u32x4> *)((uint8_t *)p.out + (mm * p.N + nn) * (16 / E));
+                        // (4-bit rows, largest tiles: past the caches, which keep the operands instead,
+                        // 138 -> 130 us; E4M3 rows: 100 -> 103)
+                        if constexpr (!FP8 && NI == 8) __builtin_nontemporal_store(x, to);
+                        else if (FULL || (mm < p.M && nn < p.N)) *to = x;
                     }
                 }
             }

@@ -33,6 +33,11 @@ template <> struct Elem<float> {
         *(f32x4 *)p = f32x4{x[0], x[1], x[2], x[3]};
         *(f32x4 *)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
     }
+    // past the caches' recent lines: for rows that are not read again soon
+    static __device__ __forceinline__ void put8_far(float *p, const float *x) {
+        __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, (f32x4 *)p);
+        __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, (f32x4 *)(p + 4));
+    }
     // at any multiple of an element: the hardware takes such addresses
     typedef f32x4 Odd __attribute__((aligned(4)));
     static __device__ __forceinline__ void get8_odd(const float *p, float *x) {
@@ -65,6 +70,9 @@ template <> struct Elem<uint16_t> {
         return a;
     }
     static __device__ __forceinline__ void put8(uint16_t *p, const float *x) { *(u32x4 *)p = pack8(x); }
+    static __device__ __forceinline__ void put8_far(uint16_t *p, const float *x) {
+        __builtin_nontemporal_store(pack8(x), (u32x4 *)p);
+    }
     typedef u32x4 Odd __attribute__((aligned(2)));
     static __device__ __forceinline__ void get8_odd(const uint16_t *p, float *x) {
         const u32x4 a = *(const Odd *)p;
@@ -126,12 +134,15 @@ __device__ __forceinline__ void load_row(const T *p, int t, int n, float (&x)[VP
     }
 }
 
-// vector i of a thread's part of a row
-template <typename T, int TPR, int VEC>
+// vector i of a thread's part of a row (FAR: with VEC 1 by put8_far)
+template <typename T, int TPR, int VEC, bool FAR = false>
 __device__ __forceinline__ void store_vector(T *p, int t, int i, int n, const float (&x)[8]) {
     if constexpr (VEC == 1) {
         const int c = (i * TPR + t) * 8;
-        if (c < n) Elem<T>::put8(p + c, x);
+        if (c < n) {
+            if constexpr (FAR) Elem<T>::put8_far(p + c, x);
+            else Elem<T>::put8(p + c, x);
+        }
     } else {
         if (VEC == 2 && n >= 8) {
             if ((i * TPR + t) * 8 < n) Elem<T>::put8_odd(p + odd_at<TPR>(t, i, n), x);
@@ -145,10 +156,10 @@ __device__ __forceinline__ void store_vector(T *p, int t, int i, int n, const fl
     }
 }
 
-template <typename T, int TPR, int VPT, int VEC>
+template <typename T, int TPR, int VPT, int VEC, bool FAR = false>
 __device__ __forceinline__ void store_row(T *p, int t, int n, const float (&x)[VPT][8]) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) store_vector<T, TPR, VEC>(p, t, i, n, x[i]);
+    for (int i = 0; i < VPT; ++i) store_vector<T, TPR, VEC, FAR>(p, t, i, n, x[i]);
 }
 
 template <int TPR, int VPT, int VEC>
@@ -343,7 +354,7 @@ __device__ __forceinline__ void store_mx(uint8_t *codes, uint8_t *scales, int pa
 
 // A row of z = h w with the row's sum of h^2 and largest |z| (infinite for a
 // NaN): y in fp32 or bf16, 8-bit codes with a scale, or 4-bit blocks.
-template <int TPR, int VPT, int VEC, bool MX>
+template <int TPR, int VPT, int VEC, bool MX, bool FAR = false>
 __device__ __forceinline__ void norm_store(void *y, void *scales, int out_prec, int64_t row, int t, int n, float sum,
                                            float mx, float rstd, float (&z)[VPT][8]) {
     const float inf = __builtin_inff();
@@ -355,9 +366,9 @@ __device__ __forceinline__ void norm_store(void *y, void *scales, int out_prec, 
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[i][e] = z[i][e] * rstd;
         if (out_prec == LORES_FP32)
-            store_row<float, TPR, VPT, VEC>((float *)y + row * n, t, n, z);
+            store_row<float, TPR, VPT, VEC, FAR>((float *)y + row * n, t, n, z);
         else if (out_prec == LORES_BF16)
-            store_row<uint16_t, TPR, VPT, VEC>((uint16_t *)y + row * n, t, n, z);
+            store_row<uint16_t, TPR, VPT, VEC, FAR>((uint16_t *)y + row * n, t, n, z);
         else if constexpr (MX && VEC != 0) {
             const int per = mx_scale_stride(n);
             // (without an epsilon the r of a row of zeros is an infinity: its y are 0)
