@@ -250,7 +250,12 @@ template <> struct Kept<float> {
         for (int e = 0; e < 8; ++e) x[e] = v[e];
     }
     __device__ __forceinline__ float at(int e) const { return x[e]; }
-    __device__ __forceinline__ void read(const float *p) { Elem<float>::get8(p, x); }
+    template <bool FAR> __device__ __forceinline__ void read(const float *p) {
+        const f32x4 *q = (const f32x4 *)p;
+        const f32x4 a = FAR ? __builtin_nontemporal_load(q) : *q, b = FAR ? __builtin_nontemporal_load(q + 1) : q[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { x[e] = a[e]; x[4 + e] = b[e]; }
+    }
     __device__ __forceinline__ void read_odd(const float *p) { Elem<float>::get8_odd(p, x); }
 };
 template <> struct Kept<uint16_t> {
@@ -263,18 +268,21 @@ template <> struct Kept<uint16_t> {
     __device__ __forceinline__ float at(int e) const {
         return __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
     }
-    __device__ __forceinline__ void read(const uint16_t *p) { x = *(const u32x4 *)p; }
+    template <bool FAR> __device__ __forceinline__ void read(const uint16_t *p) {
+        x = FAR ? __builtin_nontemporal_load((const u32x4 *)p) : *(const u32x4 *)p;
+    }
     __device__ __forceinline__ void read_odd(const uint16_t *p) { x = *(const Elem<uint16_t>::Odd *)p; }
 };
 
-template <typename T, int TPR, int VPT, int VEC>
+// (FAR: with VEC 1 past the caches' recent lines, as put8_far)
+template <typename T, int TPR, int VPT, int VEC, bool FAR>
 __device__ __forceinline__ void keep_row(const T *p, int t, int n, Kept<T> (&k)[VPT]) {
     if constexpr (VEC == 1) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = (i * TPR + t) * 8;
             if (c < n) {
-                k[i].read(p + c);
+                k[i].template read<FAR>(p + c);
             } else {
                 const float zero[8] = {};
                 k[i].set(zero);
