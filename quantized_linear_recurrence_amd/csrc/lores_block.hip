@@ -9,16 +9,16 @@
 // Bound by memory: a row is read once, kept in registers through both norms
 // and written once, past the caches' recent lines (16384 x 4096 with a gate: forward
 // 128 -> 117 us, backward 206 -> 202; followed by a read of y, 1024 to 32768 rows take as
-// long or less).  16384 x 4096 with a gate: forward 116 us, 5.8 TB/s, backward 198, 5.4 TB/s.
+// long or less).  16384 x 4096 with a gate: forward 118 us, 5.7 TB/s, backward 202, 5.3 TB/s.
 #include "lores_gate.h"
 #include "lores_layer.h"
 
 namespace lores {
 namespace {
 
-// Whether rows are read past the caches' recent lines too: long ones (backward of 4096 x 16384
-// 324 -> 278 us, of 16384 x 4096 202 -> 198), not short ones (8192 x 1024 32 -> 34).
-template <int TPR> constexpr bool kFar = TPR >= 256;
+// Whether rows are read past the caches' recent lines too: the longest ones (4096 x 16384 forward
+// and backward 426 -> 379 us), not the others (1024 x 4096 37 -> 39, 16384 x 4096 297 -> 293).
+template <int TPR, int VPT> constexpr bool kFar = TPR * VPT > 1024;
 
 template <typename T, int TPR, int VPT, int VEC>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_kernel(const BlockArgs a) {
@@ -30,8 +30,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_kernel(cons
     float h[VPT][8], w[VPT][8];
     load_row<T, TPR, VPT, VEC>((const T *)a.x + row * a.xs, t, a.n, h);
     Kept<T> kr[VPT], kg[VPT];
-    if (a.res) keep_row<T, TPR, VPT, VEC, kFar<TPR>>((const T *)a.res + row * a.rs, t, a.n, kr);
-    if (a.gate) keep_row<T, TPR, VPT, VEC, kFar<TPR>>((const T *)a.gate + row * a.gs, t, a.n, kg);
+    if (a.res) keep_row<T, TPR, VPT, VEC, kFar<TPR, VPT>>((const T *)a.res + row * a.rs, t, a.n, kr);
+    if (a.gate) keep_row<T, TPR, VPT, VEC, kFar<TPR, VPT>>((const T *)a.gate + row * a.gs, t, a.n, kg);
     float f = a.scale;
     if (a.w) {
         load_either<TPR, VPT, VEC>(a.w, a.w_bf16, t, a.n, w);
@@ -119,11 +119,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_ke
     const float per = 1.0f / (float)a.n;
     for (int64_t row = (int64_t)blockIdx.x * ROWS + sub; row < a.rows; row += (int64_t)a.groups * ROWS) {
         Kept<T> kx[VPT], kh[VPT], kg[VPT], ky[VPT], kd[VPT];
-        keep_row<T, TPR, VPT, VEC, kFar<TPR>>((const T *)a.h + row * a.n, t, a.n, kh);
-        keep_row<T, TPR, VPT, VEC, kFar<TPR>>((const T *)a.dy + row * a.n, t, a.n, ky);
-        keep_row<T, TPR, VPT, VEC, kFar<TPR>>((const T *)a.x + row * a.xs, t, a.n, kx);
-        if (a.gate && !LEAN) keep_row<T, TPR, VPT, VEC, kFar<TPR>>((const T *)a.gate + row * a.gs, t, a.n, kg);
-        if (a.dh) keep_row<T, TPR, VPT, VEC, kFar<TPR>>((const T *)a.dh + row * a.n, t, a.n, kd);
+        keep_row<T, TPR, VPT, VEC, kFar<TPR, VPT>>((const T *)a.h + row * a.n, t, a.n, kh);
+        keep_row<T, TPR, VPT, VEC, kFar<TPR, VPT>>((const T *)a.dy + row * a.n, t, a.n, ky);
+        keep_row<T, TPR, VPT, VEC, kFar<TPR, VPT>>((const T *)a.x + row * a.xs, t, a.n, kx);
+        if (a.gate && !LEAN) keep_row<T, TPR, VPT, VEC, kFar<TPR, VPT>>((const T *)a.gate + row * a.gs, t, a.n, kg);
+        if (a.dh) keep_row<T, TPR, VPT, VEC, kFar<TPR, VPT>>((const T *)a.dh + row * a.n, t, a.n, kd);
         if constexpr (LEAN) weight_next();
         float s2 = 0.0f, dot2 = 0.0f;
 #pragma unroll
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_ke
         store_row<T, TPR, VPT, VEC, true>((T *)a.dres + row * a.n, t, a.n, G);
         if constexpr (LEAN) {
             weight();
-            if (a.gate) keep_row<T, TPR, VPT, VEC, kFar<TPR>>((const T *)a.gate + row * a.gs, t, a.n, kg);
+            if (a.gate) keep_row<T, TPR, VPT, VEC, kFar<TPR, VPT>>((const T *)a.gate + row * a.gs, t, a.n, kg);
         }
         // from here on G is sc G
         auto gate_of = [&](int i, int e, float &value, float &slope) {

@@ -65,8 +65,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_kernel(cons
 
 // dw is summed by each work-group over its rows (with weights per head, the
 // rows of one head), in registers and over the rows side by side in LDS; a
-// second kernel adds the work-groups' sums in a fixed order.  Rows are read past the caches'
-// recent lines (8192 x 32 x 128: 74 -> 68 us, 4.9 TB/s).  LEAN: 1024 threads leave
+// second kernel adds the work-groups' sums in a fixed order.  (Rows read past the
+// caches' recent lines: 8192 x 32 x 128 alone 74 -> 68 us, but behind its forward pass, whose
+// rows the last cache still holds, 110 -> 121 for both.)  LEAN: 1024 threads leave
 // a thread 128 registers, so with two vectors the sums stand in LDS and the weights
 // are read where they are used.
 template <typename T, int TPR, int VPT, int VEC>
@@ -99,9 +100,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_backward_ke
         if (!a.per_head) split_row(a, (uint32_t)r, token, head);
         const int64_t row = (int64_t)token * a.heads + head;
         Kept<T> kx[VPT], kz[VPT], kg[VPT];
-        keep_row<T, TPR, VPT, VEC, true>((const T *)a.x + token * a.xs[0] + head * a.xs[1], t, a.n, kx);
-        keep_row<T, TPR, VPT, VEC, true>((const T *)a.gate + token * a.gs[0] + head * a.gs[1], t, a.n, kz);
-        keep_row<T, TPR, VPT, VEC, true>((const T *)a.dy + row * a.n, t, a.n, kg);
+        keep_row<T, TPR, VPT, VEC>((const T *)a.x + token * a.xs[0] + head * a.xs[1], t, a.n, kx);
+        keep_row<T, TPR, VPT, VEC>((const T *)a.gate + token * a.gs[0] + head * a.gs[1], t, a.n, kz);
+        keep_row<T, TPR, VPT, VEC>((const T *)a.dy + row * a.n, t, a.n, kg);
         if constexpr (LEAN) weight();
         float s[LEAN ? 1 : VPT][8], ss = 0.0f, dot = 0.0f;
 #pragma unroll

@@ -275,7 +275,7 @@ template <> struct Kept<uint16_t> {
 };
 
 // (FAR: with VEC 1 past the caches' recent lines, as put8_far)
-template <typename T, int TPR, int VPT, int VEC, bool FAR>
+template <typename T, int TPR, int VPT, int VEC, bool FAR = false>
 __device__ __forceinline__ void keep_row(const T *p, int t, int n, Kept<T> (&k)[VPT]) {
     if constexpr (VEC == 1) {
 #pragma unroll
