@@ -5,7 +5,10 @@
 //   norm first: e = dy w a,  dx = r (e - n mean(e n)),  dz = dy w n s,  dw = sum dy a n
 //   gate first: e = dy w,  du = r (e - n mean(e n)),  dx = du a,  dz = du x s,  dw = sum dy n
 //
-// Bound by memory: a row is read once, kept in registers and written once.
+// Bound by memory: a row is read once, kept in registers and written once.  8192 x 32 x 128
+// bf16: forward 39 us, 5.2 TB/s, backward 74, 4.5 TB/s (with 33 M elements of fp32 35 and 74);
+// heads of 100: 38 and 69.  A row takes the fewest threads that hold it in two vectors each
+// (heads of 64 with 16 threads instead of 8: forward 62 instead of 38).
 #include "lores_gate.h"
 #include "lores_layer.h"
 

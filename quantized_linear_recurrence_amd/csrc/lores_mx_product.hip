@@ -62,7 +62,8 @@ __device__ __forceinline__ void put(const MxProduct &p, int64_t m, int j, f32x4 
 
 // ------------------------------------------------------------ few rows
 //
-// Bound by latency and the weights' way from memory.  A work-group has 16 NT columns and
+// Bound by latency and the weights' way from memory: 8192 x 4096 take 5.5 us with one row,
+// 9.8 with 64.  A work-group has 16 NT columns and
 // 16 MT rows; its wavefronts share k, U steps of 128 at a time, and everything a
 // wavefront reads for them is on its way at once: of a row 64 U neighbouring bytes of codes
 // and 4 U of scales (a request for 4 bytes of scales costs what one for 16 does: 64 rows of

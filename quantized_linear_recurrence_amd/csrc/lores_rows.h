@@ -1,6 +1,7 @@
 // Rows in registers, as the norms hold them: element access in bf16 or fp32, a
 // thread's columns of a row, loads and stores of them, sums over a row's
-// threads, and a norm's output in any of its forms.  A row takes TPR threads (16, 64, 256 or 1024) of VPT vectors of 8.
+// threads, and a norm's output in any of its forms.  A row takes TPR threads (8 to 64,
+// 256 or 1024) of VPT vectors of 8.
 #pragma once
 
 #include "lores_seq.h"
