@@ -548,16 +548,20 @@ hipError_t go_tiles(const MxProduct &p, hipStream_t s) {
     return go_tile<FP8, BF16, false, X4, 4, 4, 2, 2>(p, 512, s);
 }
 
-// Few rows: the fewest rows a work-group (16, 32 or 64) with which there are at most 256
-// work-groups; us at K = 4096, 16 / 32 / 64 rows / tiles of 64 x 64:
-//   48 x 1024  5.4 6.7 8.3 11.6    48 x 4096  8.8 6.9 8.4 11.8    48 x 8192  12.2 10.7 8.7 12.2
-//   256 x 1024  8.9 6.9 9.2 8.9    96 x 4096  12.0 11.1 9.3 11.9   256 x 4096  28.6 20.5 16.4 12.9
+// Few rows: the smallest tile of a work-group (rows x columns) with which there are at most 256
+// work-groups; us at 16 x 16 / 16 x 32 / 32 x 32 / 64 x 32:
+//   K = 4096    16 x 4096  4.7  5.7    -    -     16 x 8192  7.3  6.5    -    -     32 x 2048  4.7  5.7  6.9   -
+//               32 x 4096  7.0  5.8  7.0    -     64 x 4096 11.6  9.0  7.1  9.4     64 x 8192 20.8 16.3 12.2 10.5
+//   K = 16384   16 x 1024 10.9 15.3    -    -     64 x 1024 11.1 15.3 19.8 28.6     64 x 4096 38.1 29.6 21.3 30.4
+// More rows than 64 of too many columns take tiles (K = 4096, 64 x 32 / tiles of 64 x 64: 96 x 4096
+// 9.3 11.9, 256 x 4096 16.4 12.9).
 template <bool FP8, bool BF16>
 hipError_t go(const MxProduct &p, hipStream_t s) {
-    const int64_t columns = (p.N + 31) / 32;
-    if (columns * ((p.M + 15) / 16) <= 256 || p.M <= 16) return go_few<FP8, BF16, 1, 2, 4, 8>(p, s);
-    if (columns * ((p.M + 31) / 32) <= 256 || p.M <= 32) return go_few<FP8, BF16, 2, 2, 4, 8>(p, s);
-    if (columns * ((p.M + 63) / 64) <= 256 || p.M <= 64) return go_few<FP8, BF16, 4, 2, 4, 8>(p, s);
+    auto fits = [&](int rows, int columns) { return (p.N + columns - 1) / columns * ((p.M + rows - 1) / rows) <= 256; };
+    if (fits(16, 16)) return go_few<FP8, BF16, 1, 1, 4, 8>(p, s);
+    if (fits(16, 32) || p.M <= 16) return go_few<FP8, BF16, 1, 2, 4, 8>(p, s);
+    if (fits(32, 32) || p.M <= 32) return go_few<FP8, BF16, 2, 2, 4, 8>(p, s);
+    if (fits(64, 32) || p.M <= 64) return go_few<FP8, BF16, 4, 2, 4, 8>(p, s);
     return mx_scale_stride(p.K) % 16 == 0 ? go_tiles<FP8, BF16, true>(p, s) : go_tiles<FP8, BF16, false>(p, s);
 }
 
