@@ -246,6 +246,56 @@ def test_calls_on_two_streams_at_once():
     assert all(torch.equal(y, want[i]) for i, y in got)
 
 
+def test_a_layer_s_calls_in_two_graphs():
+    """Norm, product, gated norm, product, captured twice and replayed in turn with eager calls
+    between: nothing of one is the other's."""
+    x, res, z = randn((40, 512), BF16, 50), randn((40, 512), BF16, 51), randn((40, 4, 96), BF16, 52)
+    wn, wg = randn((512,), BF16, 53), randn((4, 96), BF16, 54)
+    w1, s1, _ = mx((384, 512), 55)
+    w2, s2, _ = mx((512, 384), 56)
+
+    def step():
+        a, s, h = lores.lores_block_norm(x, res, None, wn, 1e-6, out_prec=lores.LORES_MXFP4)
+        o = lores.lores_mx_matmul(a, s, w1, s1).view(40, 4, 96)
+        b, t = lores.lores_gated_norm(o, z, wg, 1e-6, out_prec=lores.LORES_MXFP4)
+        y = lores.lores_mx_matmul(b, t, w2, s2)
+        dy = lores.lores_gated_norm_backward(o, z, wg, o, 1e-6)
+        return (h, o, y, *dy, *lores.lores_block_norm_backward(x, h, wn, wn, y, 1e-6, gate=res)[:4])
+
+    step()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step()
+        graphs.append((g, out))
+    for i in range(3):
+        for t, seed in ((x, 60), (res, 61), (z, 62)):
+            t.copy_(randn(t.shape, BF16, seed + 10 * i))
+        for g, out in graphs + graphs[:1]:
+            g.replay()
+            want = step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_calls_from_two_threads():
+    from concurrent.futures import ThreadPoolExecutor
+    w, ws, _ = mx((200, 544), 70)
+    xs = [randn((m, 544), BF16, 71 + m) for m in (3, 90)]
+    want = [lores.lores_mx_matmul(*lores.lores_mx_quant(x), w, ws) for x in xs]
+    torch.cuda.synchronize()
+
+    def run(i):
+        s = torch.cuda.Stream()
+        got = [lores.lores_mx_matmul(*lores.lores_mx_quant(xs[i], stream=s), w, ws, stream=s) for _ in range(20)]
+        s.synchronize()
+        return all(torch.equal(g, want[i]) for g in got)
+
+    with ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(run, range(2)))
+
+
 def test_one_row_for_all():
     """Rows that lie no step apart are read as often as they stand there."""
     x = randn((1, 320), BF16, 45)
@@ -291,3 +341,14 @@ def test_refusals():
             lores.lores_mx_matmul(a, s, a, s, out=out)
     with pytest.raises(TypeError):
         lores.lores_mx_matmul(a, s, a, s, out=torch.empty(4, 4, device=dev()))
+
+    class Elsewhere:                                 # a stream of another GPU
+        device = torch.device("cuda", 1)
+
+    w = torch.ones(64, device=dev())
+    for call in (lambda t: lores.lores_mx_quant(x, stream=t), lambda t: lores.lores_mx_dequant(a, s, stream=t),
+                 lambda t: lores.lores_mx_matmul(a, s, a, s, stream=t),
+                 lambda t: lores.lores_gated_norm(x.view(4, 1, 64), x.view(4, 1, 64), w, 0.1, stream=t),
+                 lambda t: lores.lores_block_norm(x, x, w, w, 0.1, stream=t)):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call(Elsewhere())
