@@ -196,11 +196,14 @@ hipError_t go_few(const MxProduct &p, hipStream_t s) {
 //
 // A work-group goes through several tiles as one stream of stages: while a tile's
 // outputs are written, the next one's first stages are on their way.
-template <bool FP8, int TM, int TN, int NW>
+template <bool FP8, int TM, int TN, int NW, int KS>
 struct Shared {
-    uint8_t w[2][TN * 128], a[2][TM * 128];        // (a place's offset fits a read's own field)
-    uint32_t sc[TN + (FP8 ? 0 : TM)][4];
+    struct Part {
+        uint8_t w[2][TN * 128], a[2][TM * 128];    // (a place's offset fits a read's own field)
+        uint32_t sc[TN + (FP8 ? 0 : TM)][4];
+    } part[KS];
     uint8_t out[NW][2048];
+    f32x4 join[KS > 1 ? TM * TN / 4 : 1];
 };
 
 // The n-th tile of `all`: each of the 8 XCDs (work-groups go to them in turn) takes a
@@ -226,11 +229,15 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *q) {
 // they write again, with the same values), and a lane's place in its rows is the same for
 // all its loads; else rows behind the end are read as the last one.
 //
+// KS: so many sets of wavefronts share a tile's K, each with its own stages; behind the loop
+// their sums are added in order.  For tiles that leave every CU but one work-group, whose
+// loads alone cannot fill it.
+//
 // K goes in groups of 512.  Behind a row's end its first bytes are read,
 // with scales of 0 on both sides: 36 2^-254 is below any fp32, so they add nothing (and
 // an E4M3 NaN there is the row's own).  So the loop has no branch.
-template <bool FP8, bool BF16, bool FULL, bool X4, int MI, int NI, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxProduct p, const uint32_t tiles_m, const uint32_t tiles_n) {
+template <bool FP8, bool BF16, bool FULL, bool X4, int MI, int NI, int WM, int WN, int KS>
+__global__ void __launch_bounds__(64 * WM * WN * KS) lores_mx_tile_kernel(const MxProduct p, const uint32_t tiles_m, const uint32_t tiles_n) {
     constexpr int TM = 16 * MI * WM, TN = 16 * NI * WN, NW = WM * WN;
     constexpr int LW = TN / 8 / NW, LA = TM / 8 / NW;           // a wavefront's loads of 8 rows
     constexpr int SR = TN + (FP8 ? 0 : TM);                     // rows of scales: the columns', the rows'
@@ -241,20 +248,23 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     static_assert(LW * NW * 8 == TN && LA * NW * 8 == TM && SR <= 64 * NW, "every load and scale has its lane");
     static_assert(FULL || NI < 8, "the largest tiles are whole");
     static_assert(TN % 64 == 0 && TM % 64 == 0, "a wavefront has scales of rows or of columns");
-    __shared__ __attribute__((aligned(1024))) Shared<FP8, TM, TN, NW> sh;
-    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    __shared__ __attribute__((aligned(1024))) Shared<FP8, TM, TN, NW, KS> all_sh;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const int ks = KS > 1 ? wave / NW : 0, wv = wave - ks * NW;
+    auto &sh = all_sh.part[ks];
     const int wm = wv % WM, wn = wv / WM;
     // this work-group's tiles: of its XCD's run, every one that lies a round further
     const uint32_t all = tiles_m * tiles_n, x8 = blockIdx.x % 8, each = all / 8, more = all % 8;
     const uint32_t run = x8 * each + min(x8, more), run_end = run + each + (x8 < more), round = gridDim.x / 8;
     uint32_t tile = run + blockIdx.x / 8;
     if (tile >= run_end) return;
-    const int groups = (p.K + 511) / 512, per = mx_scale_stride(p.K);
+    const int groups = ((p.K + 511) / 512 + KS - 1) / KS, b0 = ks * groups;      // of this set: from b0 on
+    const int per = mx_scale_stride(p.K);
     const uint32_t wrow = p.K / 2, arow = FP8 ? p.K : p.K / 2;
     const int piece = (lane & 7) ^ (lane >> 3);      // a lane's of its row, the same in all its loads
 
     // ---- where a tile's operands lie; the tile that is multiplied and the next one
-    const int srow = threadIdx.x % SR;               // (with fewer rows than threads some come twice)
+    const int srow = (threadIdx.x - ks * 64 * NW) % SR;               // (with fewer rows than threads some come twice)
     const bool of_w = FP8 || wv % (SR / 64) < TN / 64;
     struct Aim {
         int64_t m0;
@@ -292,14 +302,16 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     Aim now, then;
     // stage j of a tile's columns, or of its rows, into place j & 1
     auto load_columns = [&](int j, const Aim &x) {
-        const uint32_t k = 256 * j + 32 * piece < p.K ? j * 128 + piece * 16 : 0;
+        const int at = j + 2 * b0;
+        const uint32_t k = 256 * at + 32 * piece < p.K ? at * 128 + piece * 16 : 0;
 #pragma unroll
         for (int i = 0; i < LW; ++i)
             direct16(uniform(x.w + (FULL ? (int64_t)(i * NW * 8) * wrow : 0)), x.wat[FULL ? 0 : i] + k,
                      sh.w[j & 1] + (wv + i * NW) * 1024);
     };
     auto load_rows = [&](int j, const Aim &x) {
-        const uint32_t k = (FP8 ? 128 : 256) * j + (FP8 ? 16 : 32) * piece < p.K ? j * 128 + piece * 16 : 0;
+        const int at = j + (FP8 ? 4 : 2) * b0;
+        const uint32_t k = (FP8 ? 128 : 256) * at + (FP8 ? 16 : 32) * piece < p.K ? at * 128 + piece * 16 : 0;
 #pragma unroll
         for (int i = 0; i < LA; ++i)
             direct16(uniform(x.a + (FULL ? (int64_t)(i * NW * 8) * arow : 0)), x.aat[FULL ? 0 : i] + k,
@@ -309,6 +321,7 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     // made 0 where they are used: used here they would be waited for)
     uint32_t sq[4], sin[4];
     auto fetch_scales = [&](int b, const Aim &x) {
+        b += b0;
         if constexpr (X4) {
             sin[0] = sin[1] = sin[2] = sin[3] = 0u - (uint32_t)(16 * b < per);
             const Words4 v = *(const Global<Words4> *)(x.s + (16 * b & sin[0]) + x.sat);
@@ -335,7 +348,7 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
     int rs[MI], cs[NI];
     auto read_row_scales = [&](int (&x)[MI], int b) {
         // E4M3: 1, but 0 behind K (byte s: block 16 b + 4 s + g)
-        const int none = 16 - min(max(p.K / 32 - 16 * b - g + 3, 0) & ~3, 16);      // 4 bits for each half byte of 0
+        const int none = 16 - min(max(p.K / 32 - 16 * (b0 + b) - g + 3, 0) & ~3, 16);      // 4 bits for each half byte of 0
         const int one = (0x7f7f7f7f >> none) >> none;
 #pragma unroll
         for (int i = 0; i < MI; ++i) x[i] = FP8 ? one : sh.sc[(FP8 ? 0 : TN) + (wm * MI + i) * 16 + r][g];
@@ -469,6 +482,24 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
             step(std::integral_constant<int, 2>(), b);
             step(std::integral_constant<int, 3>(), b);
         }
+        if constexpr (KS > 1) {
+#pragma unroll 1
+            for (int k = 1; k < KS; ++k) {
+                f32x4 *place = all_sh.join + wv * MI * NI * 64 + lane;
+                if (ks == k)
+#pragma unroll
+                    for (int i = 0; i < MI * NI; ++i) place[i * 64] = c[i / NI][i % NI];
+                __syncthreads();
+                if (ks == 0)
+#pragma unroll
+                    for (int i = 0; i < MI * NI; ++i) c[i / NI][i % NI] += place[i * 64];
+                __syncthreads();
+            }
+            if (ks) {
+                now = then;
+                continue;
+            }
+        }
         const int64_t m = now.m0 + wm * MI * 16;
         const int n = now.n0 + wn * NI * 16;
         // outputs in pieces of 16 bytes, if rows of them are whole: 16 rows of 128 bytes at a
@@ -481,7 +512,7 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
         asm volatile("" : "+v"(l));
         const int lr = l & 15, lg = l >> 4, row = l / CH, ch = l % CH;
         if (p.N % E == 0) {
-            uint8_t *own = sh.out[wv];
+            uint8_t *own = all_sh.out[wv];
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const float f = FP8 ? p.a_rows[min(m + lr + 16 * i, p.M - 1)] : 1.0f;
@@ -522,12 +553,12 @@ __global__ void __launch_bounds__(64 * WM * WN) lores_mx_tile_kernel(const MxPro
 }
 
 // `residents`: work-groups that run at once, a multiple of 8
-template <bool FP8, bool BF16, bool FULL, bool X4, int MI, int NI, int WM, int WN>
+template <bool FP8, bool BF16, bool FULL, bool X4, int MI, int NI, int WM, int WN, int KS = 1>
 hipError_t go_tile(const MxProduct &p, int residents, hipStream_t s) {
     constexpr int TM = 16 * MI * WM, TN = 16 * NI * WN;
     const int64_t tm = (p.M + TM - 1) / TM, tn = (p.N + TN - 1) / TN;
     const int64_t groups = (tm * tn + 7) / 8 * 8;
-    lores_mx_tile_kernel<FP8, BF16, FULL, X4, MI, NI, WM, WN><<<dim3((uint32_t)(groups < residents ? groups : residents)), 64 * WM * WN, 0, s>>>(
+    lores_mx_tile_kernel<FP8, BF16, FULL, X4, MI, NI, WM, WN, KS><<<dim3((uint32_t)(groups < residents ? groups : residents)), 64 * WM * WN * KS, 0, s>>>(
         p, (uint32_t)tm, (uint32_t)tn);
     return hipGetLastError();
 }
@@ -538,12 +569,21 @@ hipError_t go_tile(const MxProduct &p, int residents, hipStream_t s) {
 //   outputs           512 x 4096           512 x 8192          1024 x 8192          1536 x 8192
 //   4-bit rows   14.2 15.3 19.6 27.1  24.8 17.6 20.8 27.8  40.2 25.1 25.5 30.7  56.6 38.4 40.4 34.7
 //   E4M3 rows    18.2 21.8 26.5 42.1  31.2 24.2 28.2 42.8  53.7 45.0 34.1 45.9  73.9 63.1 55.7 50.8
+// With at most 256 tiles of 64 x 64 K is shared by two sets of wavefronts, a long one by four; us of
+// 256 x 4096 with one / two / four sets, from weights that no cache holds:
+//   K             1536          2048          4096          8192          16384
+//   4-bit rows   6.2 6.5 8.0   7.2 6.6 7.8  14.0 11.3 11.8  26.6 19.9 19.5  52.4 36.9 34.7
+//   E4M3 rows    8.5 8.3 9.0  10.0 8.3 9.1  17.4 13.4 13.2  39.6 26.6 23.5  70.9 49.6 42.0
 template <bool FP8, bool BF16, bool X4>
 hipError_t go_tiles(const MxProduct &p, hipStream_t s) {
     const int64_t cells = p.M * p.N;
     if (p.M >= 256 && p.N >= 256 && cells > 1 << 23) return go_tile<FP8, BF16, true, X4, 4, 8, 4, 2>(p, 256, s);
     if constexpr (FP8)
         if (p.M >= 256 && p.N >= 256 && cells > 1 << 22) return go_tile<FP8, BF16, true, X4, 4, 4, 2, 4>(p, 256, s);
+    if ((p.M + 63) / 64 * ((p.N + 63) / 64) <= 256) {
+        if (p.K >= 8192) return go_tile<FP8, BF16, false, X4, 2, 2, 2, 2, 4>(p, 256, s);
+        if (p.K >= 2048) return go_tile<FP8, BF16, false, X4, 2, 2, 2, 2, 2>(p, 256, s);
+    }
     if (cells <= 1 << 21) return go_tile<FP8, BF16, false, X4, 2, 2, 2, 2>(p, 768, s);
     return go_tile<FP8, BF16, false, X4, 4, 4, 2, 2>(p, 512, s);
 }

@@ -72,7 +72,8 @@ def test_4_bit_rows_of_more_than_2_21_groups():
         assert (back[at:at + (1 << 25)] == value).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(70001, 32776, 32), (70001, 32771, 64), (3, 40, 1 << 24), (270, 264, 1 << 24)])
+@pytest.mark.parametrize("M,N,K", [(70001, 32776, 32), (70001, 32771, 64), (3, 40, 1 << 24), (270, 264, 1 << 24),
+                                   (270, 1700, 1 << 24)])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_products_beyond_32_bits(M, N, K, fp8):
     """Outputs, or places in the operands, behind 2^31; each sum has three terms, the last

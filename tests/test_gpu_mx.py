@@ -117,7 +117,8 @@ def test_product(M, N, K):
 @pytest.mark.parametrize("M,N,K", [(512, 512, 512), (700, 1000, 1056), (1025, 777, 288), (256, 4096, 256),
                                    (4096, 256, 1024), (2048, 2304, 2080), (40, 3000, 8192), (3001, 4100, 544),
                                    (5000, 2200, 416), (2304, 5000, 384), (12000, 1000, 1536),
-                                   (2304, 2600, 512), (2111, 3001, 2048)])
+                                   (2304, 2600, 512), (2111, 3001, 2048), (250, 3900, 2080),
+                                   (777, 1000, 4096), (300, 3001, 8224), (130, 5000, 9728)])
 def test_larger_products(M, N, K):
     w, ws, wv = mx((N, K), 4)
     a, as_, av = mx((M, K), 5)
