@@ -296,9 +296,10 @@ def _no_graph(what):
 
 def _whole(t, name, dtype, shape, device):
     """The address of a contiguous tensor of this shape (None: NULL)."""
-    import torch
     if t is None:
         return None
+    if torch is None:
+        _bind_torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device != device:
@@ -543,11 +544,19 @@ def lores_rmsnorm_backward(h, weight, dy, eps, dresidual=None, stream=None):
 #
 # For a decode batch these calls cost the host more than the GPU (a launch 3.8 us of
 # some 8), so the checks touch every property once, take the usual shapes first, and
-# enter no context where the current device and stream are the ones to use.
+# enter no context where the current device and stream are the ones to use.  An import
+# statement costs 0.15 us even of what is loaded, hence the module's own name for torch.
+
+torch = None
+
+
+def _bind_torch():
+    global torch
+    import torch
+
 
 def _context(stream, device):
     """What makes `device` and `stream` the current ones; None if they are."""
-    import torch
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
@@ -559,7 +568,6 @@ def _context(stream, device):
 
 def _queue(device):
     """The current stream of `device`."""
-    import torch
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
@@ -596,7 +604,6 @@ def _rows_of(t, name, kept):
 
 def _same(t, name, x):
     """Refuses a tensor that is not of x's device, type and shape."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device != x.device:
@@ -608,7 +615,6 @@ def _same(t, name, x):
 
 
 def _layer_types(x, weight, name):
-    import torch
     if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
         raise TypeError(f"x and {name} must be torch tensors")
     if not x.is_cuda:
@@ -622,7 +628,6 @@ def _layer_types(x, weight, name):
 
 
 def _warn_graph(what, *ts):
-    import torch
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts):
         _no_graph(what)
 
@@ -630,28 +635,29 @@ def _warn_graph(what, *ts):
 def _like(x):
     """An uninitialised contiguous tensor of x's shape and type (empty_like takes the host
     1.1 us, new_empty 1.7)."""
-    import torch
     return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def _rows2(t, lead, n, dtype):
     """An uninitialised contiguous tensor [*lead, n] on t's device (empty_strided: 1.3 us)."""
-    import torch
     if len(lead) == 1:
         return torch.empty_strided((lead[0], n), (n, 1), dtype=dtype, device=t.device)
     return t.new_empty((*lead, n), dtype=dtype)
 
 
+def _flat(t, n, dtype):
+    """An uninitialised tensor of n elements on t's device."""
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=t.device)
+
+
 def _mx_pair(t, lead, n):
     """Tensors for rows of n 4-bit values: codes and scales."""
-    import torch
     u8 = torch.uint8
     return _rows2(t, lead, n // 2, u8), _rows2(t, lead, (n + 127) // 128 * 4, u8)
 
 
 def _out_prec(out_prec, in_bf16, allowed):
     """The output precision, its torch type (None: 4-bit blocks) and whether that is x's."""
-    import torch
     if out_prec is None or out_prec == (LORES_BF16 if in_bf16 else LORES_FP32):
         return (LORES_BF16 if in_bf16 else LORES_FP32), None, True
     if out_prec not in allowed:
@@ -695,6 +701,8 @@ def lores_gated_norm(x, gate, weight, eps, act=LORES_ACT_SILU, gate_first=False,
     LORES_MXFP4: codes [..., heads n / 2] and scales as lores_mx_matmul takes them.
     No autograd graph is recorded (lores_gated_norm_backward has the gradients).
     """
+    if torch is None:
+        _bind_torch()
     d, xp, gp, wp = _gated_dims(x, gate, weight, eps, act, gate_first)
     if x.requires_grad or gate.requires_grad or weight.requires_grad:
         _warn_graph("lores_gated_norm", x, gate, weight)
@@ -719,7 +727,8 @@ def lores_gated_norm_backward(x, gate, weight, dy, eps, act=LORES_ACT_SILU, gate
                               stream=None):
     """Gradients (dx, dgate, dw) of lores_gated_norm's unquantized output: dx, dgate
     of x's shape and type, contiguous; dw of the weight's shape, fp32."""
-    import torch
+    if torch is None:
+        _bind_torch()
     d, xp, gp, wp = _gated_dims(x, gate, weight, eps, act, gate_first)
     dyp = _need(dy, "dy", x.dtype, x.shape, x.device)
     size = ctypes.c_size_t(0)
@@ -727,8 +736,8 @@ def lores_gated_norm_backward(x, gate, weight, dy, eps, act=LORES_ACT_SILU, gate
 
     def call():
         dx, dgate = _like(x), _like(x)
-        dw = x.new_empty(weight.shape, dtype=torch.float32)
-        work = x.new_empty(size.value, dtype=torch.uint8)
+        dw = torch.empty_strided(weight.shape, weight.stride(), dtype=torch.float32, device=x.device)
+        work = _flat(x, size.value, torch.uint8)
         _check(_lib.lib().lores_gated_norm_backward(d, xp, gp, wp, dyp, dx.data_ptr(), dgate.data_ptr(),
                                                     dw.data_ptr(), work.data_ptr(), size.value,
                                                     _queue(x.device)))
@@ -772,9 +781,12 @@ def lores_block_norm(x, residual, weight, weight_next, eps, scale=1.0, gate=None
     lores_mx_matmul takes them.  No autograd graph is recorded
     (lores_block_norm_backward has the gradients).
     """
-    import torch
+    if torch is None:
+        _bind_torch()
     d, xp, rp, gp, w, wn = _block_dims(x, residual, weight, weight_next, eps, scale, gate, act)
-    _warn_graph("lores_block_norm", x, residual, weight, weight_next, gate)
+    if (x.requires_grad or weight_next.requires_grad or (residual is not None and residual.requires_grad)
+            or (weight is not None and weight.requires_grad) or (gate is not None and gate.requires_grad)):
+        _warn_graph("lores_block_norm", x, residual, weight, weight_next, gate)
     prec, dt, same = _out_prec(out_prec, d.in_bf16, _BLOCK_OUT)
 
     def call():
@@ -803,7 +815,8 @@ def lores_block_norm_backward(x, h, weight, weight_next, dy, eps, scale=1.0, gat
     unquantized outputs, from dy and the gradient dh that reaches h otherwise (or
     None).  h is the sum that lores_block_norm returned.  dgate and dw are None
     without a gate or a weight; the weights' gradients are fp32."""
-    import torch
+    if torch is None:
+        _bind_torch()
     d, xp, _, gp, w, wn = _block_dims(x, None, weight, weight_next, eps, scale, gate, act)
     hp = _need(h, "h", x.dtype, x.shape, x.device)
     dyp = _need(dy, "dy", x.dtype, x.shape, x.device)
@@ -814,9 +827,9 @@ def lores_block_norm_backward(x, h, weight, weight_next, dy, eps, scale=1.0, gat
     def call():
         dx, dres = _like(x), _like(x)
         dgate = None if gate is None else _like(x)
-        dwn = x.new_empty(d.n, dtype=torch.float32)
+        dwn = _flat(x, d.n, torch.float32)
         dw = None if weight is None else torch.empty_like(dwn)
-        work = x.new_empty(size.value, dtype=torch.uint8)
+        work = _flat(x, size.value, torch.uint8)
         _check(_lib.lib().lores_block_norm_backward(
             d, xp, hp, gp, w, wn, dyp, dhp, dx.data_ptr(), dres.data_ptr(),
             None if dgate is None else dgate.data_ptr(), None if dw is None else dw.data_ptr(),
@@ -833,7 +846,8 @@ def lores_mx_quant(x, stream=None):
     even column in the low half; scales [..., 4 ceil(n / 128)], the biased power of
     two of each block of 32 (255: a value that is not finite), 0 behind the last.
     """
-    import torch
+    if torch is None:
+        _bind_torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch tensor")
     if not x.is_cuda:
@@ -858,7 +872,6 @@ def lores_mx_quant(x, stream=None):
 
 def _mx_rows(codes, scales, name):
     """Checks a pair of lores_mx_quant's: addresses, rows and their length."""
-    import torch
     if not isinstance(codes, torch.Tensor) or not isinstance(scales, torch.Tensor):
         raise TypeError(f"{name} and its scales must be torch tensors")
     if not codes.is_cuda:
@@ -881,7 +894,8 @@ def _mx_rows(codes, scales, name):
 def lores_mx_dequant(codes, scales, dtype=None, stream=None):
     """The values [..., n] of lores_mx_quant's rows, in dtype (torch.bfloat16, the
     default, or torch.float32)."""
-    import torch
+    if torch is None:
+        _bind_torch()
     dtype = torch.bfloat16 if dtype is None else dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
@@ -905,7 +919,8 @@ def lores_mx_matmul(a, a_scales, w, w_scales, out_prec=LORES_BF16, out=None, str
     out_prec: LORES_BF16, or for 4-bit rows LORES_FP32.  out: a contiguous tensor to
     write to, or None.
     """
-    import torch
+    if torch is None:
+        _bind_torch()
     if out_prec != LORES_BF16 and out_prec != LORES_FP32:
         raise ValueError("out_prec must be LORES_BF16 or LORES_FP32")
     wp, wsp, N, K = _mx_rows(w, w_scales, "w")
