@@ -534,7 +534,8 @@ typedef struct {
  *   gate_first 1: u_j = x_j a(z_j),  y_j = u_j r w_j,  r of u
  *   x, gate    device rows by dims' strides
  *   weight     device [n] or [heads][n]
- *   out_prec   LORES_FP32, LORES_BF16 or LORES_MXFP4 (n a multiple of 32)
+ *   out_prec   LORES_FP32, LORES_BF16 or LORES_MXFP4 (n a multiple of 32; a row whose
+ *              squares leave fp32's range has NaN scales)
  *   y          device out [tokens][heads][n] contiguous; LORES_MXFP4: codes
  *              [tokens][heads n / 2], 16-byte aligned
  *   scales     device out [tokens][4 ceil(heads n / 128)] (LORES_MXFP4: a token's
@@ -644,7 +645,8 @@ int lores_mx_dequant(const uint8_t *codes, const uint8_t *scales, int64_t rows, 
  *   out_prec     LORES_BF16, or with LORES_MXFP4 rows LORES_FP32
  *   out          device out [M][N] contiguous, 16-byte aligned
  * Codes are 16-byte aligned, scales 4-byte aligned; bytes behind the last block of a
- * row's scales must be 0.  Products of 4-bit values are exact and summed in fp32.
+ * row's scales must be 0.  Products of 4-bit values are exact and summed in fp32, in an
+ * order that M, N and K alone decide.
  * With E4M3 rows the matrix instruction adds 8 neighbours of k on a grid of 2^-13 of
  * the power of two of the largest of the 8 (whose own E4M3 rounding is up to 2^-4 of
  * it), and those sums in fp32; outputs are bf16 only for that.
