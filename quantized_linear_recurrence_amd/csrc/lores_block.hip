@@ -39,7 +39,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_kernel(cons
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(e >= own_from<TPR, VEC>(t, i, a.n) ? h[i][e] : 0.0f, h[i][e], sum);
+            for (int e = 0; e < 8; ++e) {
+                const float u = e >= own_from<TPR, VEC>(t, i, a.n) ? h[i][e] : 0.0f;
+                sum = fmaf(u, u, sum);
+            }
         sum = row_sum<TPR>(sum, sm);
         const float r1 = 1.0f / sqrtf(sum / (float)a.n + a.eps);
 #pragma unroll
@@ -66,7 +69,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_kernel(cons
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            sum = fmaf(e >= own_from<TPR, VEC>(t, i, a.n) ? h[i][e] : 0.0f, h[i][e], sum);
+            const float u = e >= own_from<TPR, VEC>(t, i, a.n) ? h[i][e] : 0.0f;
+            sum = fmaf(u, u, sum);
             h[i][e] = h[i][e] * w[i][e];
             bits = max(bits, __float_as_uint(fabsf(h[i][e])));
         }
@@ -131,9 +135,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_ke
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float h = kh[i].at(e);
-                const float hc = e >= own_from<TPR, VEC>(t, i, a.n) ? h : 0.0f;
-                s2 = fmaf(hc, h, s2);
-                dot2 = fmaf(hc, wn[i][e] * ky[i].at(e), dot2);
+                const bool own = e >= own_from<TPR, VEC>(t, i, a.n);
+                const float hc = own ? h : 0.0f;
+                s2 = fmaf(hc, hc, s2);
+                dot2 = fmaf(hc, own ? wn[i][e] * ky[i].at(e) : 0.0f, dot2);
             }
         reduce<TPR, false>(s2, dot2, sm);
         const float r2 = 1.0f / sqrtf(s2 / (float)a.n + a.eps);
@@ -171,9 +176,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_ke
                 gate_of(i, e, value, slope);
                 if constexpr (!LEAN) { ga[i][e] = value; gs[i][e] = slope; }
                 const float x = kx[i].at(e);
-                const float xc = e >= own_from<TPR, VEC>(t, i, a.n) ? x : 0.0f;
-                s1 = fmaf(xc, x, s1);
-                dot1 = fmaf(xc, G[i][e] * value * w[i][e], dot1);
+                const bool own = e >= own_from<TPR, VEC>(t, i, a.n);
+                const float xc = own ? x : 0.0f;
+                s1 = fmaf(xc, xc, s1);
+                dot1 = fmaf(xc, own ? G[i][e] * value * w[i][e] : 0.0f, dot1);
             }
         float r1 = 1.0f, c1 = 0.0f;
         if (a.w) {

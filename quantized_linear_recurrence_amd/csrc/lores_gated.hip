@@ -43,7 +43,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_kernel(cons
         for (int e = 0; e < 8; ++e) {
             const float g = gate_value(a.act, z[i][e], a.act ? sigmoid<T>(z[i][e]) : 0.0f);
             if (a.gate_first) x[i][e] = x[i][e] * g;
-            sum = fmaf(e >= own_from<TPR, VEC>(t, i, a.n) ? x[i][e] : 0.0f, x[i][e], sum);
+            const float u = e >= own_from<TPR, VEC>(t, i, a.n) ? x[i][e] : 0.0f;
+            sum = fmaf(u, u, sum);
             w[i][e] = a.gate_first ? w[i][e] : w[i][e] * g;
         }
     sum = row_sum<TPR>(sum, sm);
@@ -117,9 +118,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_backward_ke
                 if constexpr (!LEAN) s[i][e] = sg;
                 const float g = gate_value(a.act, z, sg), u = a.gate_first ? x * g : x;
                 const float d = kg[i].at(e) * w[i][e];
-                const float uc = e >= own_from<TPR, VEC>(t, i, a.n) ? u : 0.0f;
-                ss = fmaf(uc, u, ss);
-                dot = fmaf(uc, a.gate_first ? d : d * g, dot);
+                const bool own = e >= own_from<TPR, VEC>(t, i, a.n);
+                const float uc = own ? u : 0.0f;
+                ss = fmaf(uc, uc, ss);
+                dot = fmaf(uc, !own ? 0.0f : a.gate_first ? d : d * g, dot);
             }
         reduce<TPR, false>(ss, dot, sm);
         const float rstd = 1.0f / sqrtf(ss / (float)a.n + a.eps);

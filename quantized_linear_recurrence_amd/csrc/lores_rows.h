@@ -92,7 +92,8 @@ template <> struct Elem<uint16_t> {
 // elements of rows at any alignment; 2: the columns of 1 in rows of any length
 // and alignment (of 8 elements or more), by vectors at odd addresses.  A row's last
 // vector then ends with the row, over part of its neighbour's: both compute the same
-// there, and only elements from own_from() on count in sums.
+// there, and only elements from own_from() on count in sums (the others as 0 in every
+// factor: 0 times an infinity is none).
 template <int TPR, int VEC>
 __device__ __forceinline__ int col(int t, int i, int e) {
     return VEC ? (i * TPR + t) * 8 + e : (i * 8 + e) * TPR + t;
