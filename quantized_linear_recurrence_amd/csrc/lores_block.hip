@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_ke
                 const float n1 = kx[i].at(e) * r1, ge = G[i][e] * value;
                 sum(1, i, e) = fmaf(ge, n1, sum(1, i, e));
                 dz[e] = G[i][e] * n1 * w[i][e] * slope;
-                G[i][e] = r1 * fmaf(-n1, c1, ge * w[i][e]);
+                // (without a weight x has no part in it: an infinite x times 0 would be NaN)
+                G[i][e] = a.w ? r1 * fmaf(-n1, c1, ge * w[i][e]) : ge;
             }
             if (a.gate) store_vector<T, TPR, VEC, true>((T *)a.dgate + row * a.n, t, i, a.n, dz);
         }

@@ -84,3 +84,20 @@ def test_one_infinity_in_a_block_s_row(dtype, n):
                 for v, name, tol in zip(got, ("dx", "dres", "dgate", "dw", "dwn"), [TOL[dtype]] * 3 + [DW] * 2):
                     if want[name] is not None:
                         like(v, want[name], tol, f"{name}, {at}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 96, 100, 1030, 16380])
+@pytest.mark.parametrize("value", [INF, -INF, float("nan")])
+def test_a_row_that_is_not_finite_without_a_weight_has_a_gradient(dtype, n, value):
+    """dx = scale a(gate) G has no x in it."""
+    wn, gate, h = weight((n,), dtype, 4), randn((3, n), dtype, 5), randn((3, n), dtype, 8)
+    x, dy, dh = randn((3, n), dtype, 1), randn((3, n), dtype, 6), randn((3, n), dtype, 7)
+    want = lores.lores_block_norm_backward(x, h, None, wn, dy, 0.5, scale=0.5, gate=gate, act=lores.LORES_ACT_SIGMOID, dh=dh)
+    x[1, n // 2] = value
+    got = lores.lores_block_norm_backward(x, h, None, wn, dy, 0.5, scale=0.5, gate=gate, act=lores.LORES_ACT_SIGMOID, dh=dh)
+    assert torch.isfinite(want[0]).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[4], want[4])
+    ref = layer.block_norm_backward(arr(x), arr(h), None, arr(wn), arr(dy), 0.5, 0.5, arr(gate), "sigmoid", arr(dh))
+    like(got[0], ref["dx"], TOL[dtype], "dx")
+    like(got[2], ref["dgate"], TOL[dtype], "dgate")
