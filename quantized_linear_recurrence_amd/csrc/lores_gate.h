@@ -6,14 +6,19 @@
 namespace lores {
 namespace {
 
-// 1 / (1 + e^-z), as 2^(-z log2 e) and a reciprocal (1 ulp each).  The exponent
-// -z log2 e is off by up to 2^-24 |z| log2 e, which bf16 inputs do not see; for fp32
-// the rounded part is carried on as a factor 1 + x ln 2.
+// 1 / (1 + e^-z), as 2^(-z log2 e) and a reciprocal (1 ulp each).  The exponent as one
+// float would be off by up to 2^-24 |z| log2 e (s of z = -80 by 3.4e-6 of itself, which
+// shows in fp32 results).  A bf16 z has 8 bits: its product with the first 15 of log2 e is
+// exact, and the rest goes in as a factor 1 - z 0x1.480fb6p-18 (off by 2^-24 at 70).  For
+// fp32 the rounded part is carried on as a factor 1 + x ln 2.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
     constexpr float log2e = 0x1.715476p+0f;
     if constexpr (sizeof(T) == 2) {
-        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * log2e));
+        // (the factor's z bounded: at an infinity it would meet a 0)
+        const float e = __builtin_amdgcn_exp2f(-z * 0x1.7154p+0f);
+        const float f = fmaf(__builtin_amdgcn_fmed3f(z, -150.0f, 150.0f), -0x1.480fb6p-18f, 1.0f);
+        return __builtin_amdgcn_rcpf(fmaf(e, f, 1.0f));
     } else {
         // beyond +-150 the result is 0 or 1; NaN goes by itself
         const float m = -fminf(fmaxf(z, -150.0f), 150.0f);

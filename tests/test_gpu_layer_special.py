@@ -101,3 +101,53 @@ def test_a_row_that_is_not_finite_without_a_weight_has_a_gradient(dtype, n, valu
     ref = layer.block_norm_backward(arr(x), arr(h), None, arr(wn), arr(dy), 0.5, 0.5, arr(gate), "sigmoid", arr(dh))
     like(got[0], ref["dx"], TOL[dtype], "dx")
     like(got[2], ref["dgate"], TOL[dtype], "dgate")
+
+
+# A gate's element alone: a row of equal values whose r takes 3 roundings of 2^-24; the
+# gate's exponential and reciprocal take 2 each (1 ulp), its factor and sum 3, and the
+# products 4: fewer than 16, 2^-20.  Results down to 2^-126 are not subnormal for |z| <= 80.
+GATE = 2.0 ** -20
+
+
+def far(dtype, n):
+    return torch.linspace(-80.0, 80.0, 24 * n).to(dtype).view(24, 1, n).to("cuda:0")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", ["silu", "sigmoid"])
+def test_gates_in_fp32_results(dtype, kind):
+    """fp32 results of bf16 and fp32 gates alike, element by element: y, and dw of one token."""
+    n = 128
+    z, act = far(dtype, n), {"silu": lores.LORES_ACT_SILU, "sigmoid": lores.LORES_ACT_SIGMOID}[kind]
+    x, w = torch.ones_like(z), torch.full((n,), 0.75, dtype=dtype, device=z.device)
+    y, _ = lores.lores_gated_norm(x, z, w, 1.0, act=act, out_prec=lores.LORES_FP32)
+    want = layer.gated_norm(arr(x), arr(z), arr(w), 1.0, kind, False)
+    assert (np.abs(arr(y) - want) <= GATE * np.abs(want)).all(), np.max(np.abs(arr(y) / want - 1))
+    for t in range(24):
+        _, _, dw = lores.lores_gated_norm_backward(x[t:t + 1], z[t:t + 1], w, x[t:t + 1], 1.0, act=act)
+        want = layer.gated_norm_backward(arr(x[t:t + 1]), arr(z[t:t + 1]), arr(w), arr(x[t:t + 1]), 1.0, kind, False)[2]
+        assert (np.abs(arr(dw) - want) <= GATE * np.abs(want)).all(), np.max(np.abs(arr(dw) / want - 1))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", ["silu", "sigmoid"])
+def test_gates_in_a_block_s_fp32_gradient(dtype, kind):
+    """dw of one row whose G is dh alone (dy 0), of x in equal values: dw = scale dh a(z) r."""
+    n = 128
+    z, act = far(dtype, n)[:, 0], {"silu": lores.LORES_ACT_SILU, "sigmoid": lores.LORES_ACT_SIGMOID}[kind]
+    x, w = torch.ones_like(z), torch.full((n,), 0.75, dtype=dtype, device=z.device)
+    for t in range(24):
+        a, g, zero = x[t:t + 1], z[t:t + 1], torch.zeros_like(x[t:t + 1])
+        dw = lores.lores_block_norm_backward(a, a, w, w, zero, 1.0, scale=0.5, gate=g, act=act, dh=a)[3]
+        want = layer.block_norm_backward(arr(a), arr(a), arr(w), arr(w), arr(zero), 1.0, 0.5, arr(g), kind, arr(a))["dw"]
+        assert (np.abs(arr(dw) - want) <= GATE * np.abs(want)).all(), np.max(np.abs(arr(dw) / want - 1))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_infinite_and_largest_gates(dtype):
+    z = torch.tensor([INF, -INF, float("nan"), 3e38, -3e38, 1e6, -1e6, 160.0, -160.0], device="cuda:0").to(dtype).view(9, 1, 1)
+    x, w = torch.ones_like(z), torch.ones(1, dtype=dtype, device=z.device)
+    s = lores.lores_gated_norm(x, z, w, 0.0, act=lores.LORES_ACT_SIGMOID, out_prec=lores.LORES_FP32)[0].flatten().tolist()
+    assert s[0] == s[3] == s[5] == s[7] == 1.0 and s[1] == s[4] == s[6] == s[8] == 0.0 and s[2] != s[2]
+    y = lores.lores_gated_norm(x, z, w, 0.0, out_prec=lores.LORES_FP32)[0].flatten().tolist()
+    assert y[0] == INF and y[2] != y[2] and y[3:] == [float(z[3]), 0.0, float(z[5]), 0.0, float(z[7]), 0.0]
