@@ -535,7 +535,8 @@ typedef struct {
  *   x, gate    device rows by dims' strides
  *   weight     device [n] or [heads][n]
  *   out_prec   LORES_FP32, LORES_BF16 or LORES_MXFP4 (n a multiple of 32; a row whose
- *              squares leave fp32's range has NaN scales)
+ *              squares' sum is above fp32's range, or at eps = 0 below it without being a
+ *              row of zeros, has NaN scales)
  *   y          device out [tokens][heads][n] contiguous; LORES_MXFP4: codes
  *              [tokens][heads n / 2], 16-byte aligned
  *   scales     device out [tokens][4 ceil(heads n / 128)] (LORES_MXFP4: a token's
@@ -580,7 +581,8 @@ typedef struct {
  *   weight_next device [n], the norm before the next one
  *   out_prec    LORES_FP32, LORES_BF16, LORES_INT8, LORES_FP8 (z_j = fl(h_j wn_j)
  *               coded as by lores_rmsnorm) or LORES_MXFP4 (n a multiple of 32; a row
- *               that is not finite, or whose squares leave fp32's range, has NaN scales)
+ *               that is not finite, or whose squares' sum is above fp32's range, or at
+ *               eps = 0 below it without being a row of zeros, has NaN scales)
  *   y           device out [rows][n] contiguous; LORES_MXFP4: codes [rows][n / 2],
  *               16-byte aligned
  *   scales      device out: 8 bits [rows] fp32; LORES_MXFP4 [rows][4 ceil(n / 128)] bytes

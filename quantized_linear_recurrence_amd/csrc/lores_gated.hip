@@ -49,8 +49,16 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_gated_kernel(cons
         }
     sum = row_sum<TPR>(sum, sm);
     float rstd = 1.0f / sqrtf(sum / (float)a.n + a.eps);
-    // (without an epsilon the r of a row of zeros is an infinity: its codes are 0)
-    if (a.out_prec == LORES_MXFP4 && sum == 0.0f) rstd = 0.0f;
+    // Without an epsilon the r of a row of zeros is an infinity: its codes are 0.  So is that
+    // of other rows whose squares are below fp32: they go on, to scales of NaN.
+    if (a.out_prec == LORES_MXFP4 && rstd == __builtin_inff()) {
+        float some = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) some = x[i][e] == 0.0f ? some : 1.0f;
+        if (row_sum<TPR>(some, sm) == 0.0f) rstd = 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll

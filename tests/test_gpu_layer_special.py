@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import quantized_linear_recurrence_amd as lores
-from tests.layer_common import BF16, DW, EPS, F32, TOL, arr, randn, weight
+from tests.layer_common import BF16, DW, EPS, F32, TOL, arr, blocks_near, randn, weight
 from oracle import layer
 
 pytestmark = pytest.mark.gpu
@@ -151,3 +151,45 @@ def test_infinite_and_largest_gates(dtype):
     assert s[0] == s[3] == s[5] == s[7] == 1.0 and s[1] == s[4] == s[6] == s[8] == 0.0 and s[2] != s[2]
     y = lores.lores_gated_norm(x, z, w, 0.0, out_prec=lores.LORES_FP32)[0].flatten().tolist()
     assert y[0] == INF and y[2] != y[2] and y[3:] == [float(z[3]), 0.0, float(z[5]), 0.0, float(z[7]), 0.0]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [32, 96, 128, 1024, 4096, 16384])
+@pytest.mark.parametrize("eps", [1e-6, 1e-30])
+def test_4_bit_rows_of_tiny_values(dtype, n, eps):
+    """Rows whose squares are below fp32 (or add up to less than eps) but not their values: r is eps^-1/2."""
+    x, z, w = 1e-30 * randn((3, 2, n), F32, 1), randn((3, 2, n), dtype, 2), weight((n,), dtype, 3)
+    x = x.to(dtype)
+    closed = (-60.0 + randn((3, 2, n), F32, 4)).to(dtype)      # a(z) near 1e-26 (sigmoid), -6e-25 (silu)
+    for kind in ("silu", "sigmoid"):
+        for a, g, first in ((x, z, False), (x, z, True), (randn((3, 2, n), dtype, 5), closed, True),
+                            (randn((3, 2, n), dtype, 5), closed, False)):
+            act = {"silu": lores.LORES_ACT_SILU, "sigmoid": lores.LORES_ACT_SIGMOID}[kind]
+            c, s = lores.lores_gated_norm(a, g, w, eps, act=act, gate_first=first, out_prec=lores.LORES_MXFP4)
+            want = layer.gated_norm(arr(a), arr(g), arr(w), eps, kind, first).reshape(3, -1)
+            assert (np.abs(want) > 0).all()
+            blocks_near(c, s, want, f"{kind}, {first}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [32, 128, 1024, 4096, 16384])
+def test_4_bit_rows_without_an_epsilon(dtype, n):
+    """Zeros have codes and scales of 0; rows whose squares are below fp32 have no r and NaN scales, as fp32
+    outputs there are not finite.  The block norm's answers are the same."""
+    x, z, w = torch.zeros(5, 1, n, dtype=dtype, device="cuda:0"), randn((5, 1, n), dtype, 2), weight((n,), dtype, 3)
+    x[1] = 1e-30
+    x[2, 0, n // 2] = -1e-30
+    x[3] = randn((1, n), dtype, 4)
+    x[4] = -0.0
+    c, s = lores.lores_gated_norm(x, z, w, 0.0, out_prec=lores.LORES_MXFP4)
+    y, _ = lores.lores_gated_norm(x, z, w, 0.0, out_prec=lores.LORES_FP32)
+    assert not torch.isfinite(y[1:3]).any() and torch.isfinite(y[3]).all()
+    blocks = n // 32
+    for c, s in ((c, s), lores.lores_block_norm(x[:, 0], None, None, w, 0.0, out_prec=lores.LORES_MXFP4)[:2]):
+        assert (c[[0, 4]] & 0x77 == 0).all() and (s[[0, 4]] == 0).all()
+        assert (s[1:3, :blocks] == 255).all() and (c[1:3] == 0).all() and (s[3, :blocks] < 255).all()
+    z[1, 0, 1] = float("nan")                        # 0 times NaN stays
+    c, s = lores.lores_gated_norm(torch.zeros_like(x), z, w, 0.0, out_prec=lores.LORES_MXFP4)
+    assert s[1, 0] == 255 and (s[1, 1:] == 0).all() and (s[[0, 2, 3, 4]] == 0).all()
+    c, s = lores.lores_gated_norm(x, z, w, 0.0, gate_first=True, out_prec=lores.LORES_MXFP4)
+    assert (s[1, :blocks] == 255).all() and (s[0] == 0).all()
