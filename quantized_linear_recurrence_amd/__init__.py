@@ -645,6 +645,13 @@ def _rows2(t, lead, n, dtype):
     return t.new_empty((*lead, n), dtype=dtype)
 
 
+def _warn_coded(what, *ts):
+    """Of the 4-bit operators, which have no backward pass."""
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in ts):
+        warnings.warn(f"{what} records no autograd graph: no gradient will reach its inputs, and 4-bit rows have "
+                      "none. Call it on detached tensors or under torch.no_grad()", stacklevel=3)
+
+
 def _flat(t, n, dtype):
     """An uninitialised tensor of n elements on t's device."""
     return torch.empty_strided((n,), (1,), dtype=dtype, device=t.device)
@@ -845,6 +852,7 @@ def lores_mx_quant(x, stream=None):
     Returns (codes, scales), uint8: codes [..., n / 2], two E2M1 values a byte, the
     even column in the low half; scales [..., 4 ceil(n / 128)], the biased power of
     two of each block of 32 (255: a value that is not finite), 0 behind the last.
+    No autograd graph is recorded, and there is no backward operator.
     """
     if torch is None:
         _bind_torch()
@@ -859,6 +867,8 @@ def lores_mx_quant(x, stream=None):
         raise ValueError(f"x must be [..., n] with n a multiple of 32, got {list(shape)}")
     n = shape[-1]
     step = _rows_of(x, "x", 1)[0]
+    if x.requires_grad:
+        _warn_coded("lores_mx_quant", x)
 
     def call():
         codes, scales = _mx_pair(x, shape[:-1], n)
@@ -917,7 +927,8 @@ def lores_mx_matmul(a, a_scales, w, w_scales, out_prec=LORES_BF16, out=None, str
     (lores_mx_quant, or a norm with LORES_MXFP4), or torch.float8_e4m3fn [..., K] with
     one fp32 factor per row [...] (lores_rmsnorm, lores_block_norm with LORES_FP8).
     out_prec: LORES_BF16, or for 4-bit rows LORES_FP32.  out: a contiguous tensor to
-    write to, or None.
+    write to, or None.  No autograd graph is recorded, and there is no backward
+    operator.
     """
     if torch is None:
         _bind_torch()
@@ -941,6 +952,8 @@ def lores_mx_matmul(a, a_scales, w, w_scales, out_prec=LORES_BF16, out=None, str
         ap = _need(a, "a", a.dtype, a.shape, device)
         asp = _need(a_scales, "a_scales", torch.float32, lead, device)
         M = a.numel() // K
+        if a.requires_grad or a_scales.requires_grad:
+            _warn_coded("lores_mx_matmul", a, a_scales)
     else:
         prec = LORES_MXFP4
         ap, asp, M, ka = _mx_rows(a, a_scales, "a")
