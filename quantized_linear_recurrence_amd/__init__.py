@@ -289,9 +289,10 @@ def _raw_stream(stream, device):
     return (torch.cuda.current_stream(device.index) if stream is None else stream).cuda_stream
 
 
-def _no_graph(what):
+def _no_graph(what, depth=3):
+    """Warns at the caller of the operator, `depth` calls up from here."""
     warnings.warn(f"{what} records no autograd graph: no gradient will reach its inputs. Call it and "
-                  f"{what}_backward from a torch.autograd.Function, or under torch.no_grad()", stacklevel=3)
+                  f"{what}_backward from a torch.autograd.Function, or under torch.no_grad()", stacklevel=depth)
 
 
 def _whole(t, name, dtype, shape, device):
@@ -629,7 +630,7 @@ def _layer_types(x, weight, name):
 
 def _warn_graph(what, *ts):
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts):
-        _no_graph(what)
+        _no_graph(what, 4)
 
 
 def _like(x):
