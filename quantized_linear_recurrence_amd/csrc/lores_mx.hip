@@ -19,25 +19,19 @@ struct Shape {
     int32_t chunks;                    // work-groups along a row
 };
 
-// The widest of 4 .. 256 threads whose idle share is at most an eighth, else the least idle one.
+// The widest of 4 .. 256 threads whose idle share is at most an eighth (4, a block's, leave none idle).
 Shape shape_of(int32_t n) {
     const int32_t pieces = n / 8;
-    int32_t best = 2;
-    int64_t least = INT64_MAX;
-    for (int32_t l = 8; l >= 2; --l) {
-        const int64_t took = (((int64_t)pieces + (1 << l) - 1) >> l) << l;
-        if (took * 7 <= (int64_t)pieces * 8) return {l, (int32_t)(took >> l)};
-        if (took < least) { least = took; best = l; }
-    }
-    return {best, (int32_t)(least >> best)};
+    int32_t l = 8;
+    while ((((int64_t)pieces + (1 << l) - 1) >> l << l) * 7 > (int64_t)pieces * 8) --l;
+    return {l, (pieces + (1 << l) - 1) >> l};
 }
 
-__device__ __forceinline__ bool place(const MxRows &a, const Shape &sh, int64_t &row, int &c) {
+__device__ __forceinline__ void place(const MxRows &a, const Shape &sh, int64_t &row, int &c) {
     const int64_t b = block_at(blockIdx.x, blockIdx.y), rb = b / sh.chunks;
     const int chunk = (int)(b - rb * sh.chunks);
     row = rb * (kRows << (8 - sh.log_threads)) + (threadIdx.x >> sh.log_threads);
     c = ((chunk << sh.log_threads) + (threadIdx.x & ((1 << sh.log_threads) - 1))) * 8;
-    return row < a.rows;
 }
 
 template <typename T, bool VEC>
