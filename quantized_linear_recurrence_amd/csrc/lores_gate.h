@@ -15,9 +15,9 @@ template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
     constexpr float log2e = 0x1.715476p+0f;
     if constexpr (sizeof(T) == 2) {
-        // (the factor's z bounded: at an infinity it would meet a 0)
+        // (the factor's z is at most 150, by its bits: an infinity there would meet e = 0)
         const float e = __builtin_amdgcn_exp2f(-z * 0x1.7154p+0f);
-        const float f = fmaf(__builtin_amdgcn_fmed3f(z, -150.0f, 150.0f), -0x1.480fb6p-18f, 1.0f);
+        const float f = fmaf(__int_as_float(min(__float_as_int(z), 0x43160000)), -0x1.480fb6p-18f, 1.0f);
         return __builtin_amdgcn_rcpf(fmaf(e, f, 1.0f));
     } else {
         // beyond +-150 the result is 0 or 1; NaN goes by itself
