@@ -927,8 +927,9 @@ def lores_mx_matmul(a, a_scales, w, w_scales, out_prec=LORES_BF16, out=None, str
     w, w_scales: lores_mx_quant's of the weights.  a, a_scales: 4-bit rows
     (lores_mx_quant, or a norm with LORES_MXFP4), or torch.float8_e4m3fn [..., K] with
     one fp32 factor per row [...] (lores_rmsnorm, lores_block_norm with LORES_FP8).
-    out_prec: LORES_BF16, or for 4-bit rows LORES_FP32.  out: a contiguous tensor to
-    write to, or None.  No autograd graph is recorded, and there is no backward
+    out_prec: LORES_BF16, or for 4-bit rows LORES_FP32.  Sums are fp32; of E4M3 rows 8
+    neighbours of k are first added on a grid of 2^-13 of the largest product, which
+    shows where sums cancel.  out: a contiguous tensor to write to, or None.  No autograd graph is recorded, and there is no backward
     operator.
     """
     if torch is None:

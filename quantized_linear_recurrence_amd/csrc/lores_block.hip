@@ -9,7 +9,8 @@
 // Bound by memory: a row is read once, kept in registers through both norms
 // and written once, past the caches' recent lines (16384 x 4096 with a gate: forward
 // 128 -> 117 us, backward 206 -> 202; followed by a read of y, 1024 to 32768 rows take as
-// long or less).  16384 x 4096 with a gate: forward 118 us, 5.7 TB/s, backward 202, 5.3 TB/s.
+// long or less).  16384 x 4096 with a gate: forward 118 us, 5.7 TB/s, backward 205, 5.2 TB/s;
+// 8192 x 4096 of fp32 124, 5.4 TB/s, and 215, 5.0 TB/s.
 #include "lores_gate.h"
 #include "lores_layer.h"
 
@@ -86,7 +87,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_kernel(cons
 //
 // 1024 threads leave a thread 128 registers, which two vectors of five rows, two
 // weights and their sums do not fit (4096 x 16384 with all kept: 630 us).  LEAN
-// keeps the sums in LDS and reads the weights and the gate's row where they are used.
+// keeps the sums in LDS and reads the weights and the gate's row where they are used (271 us; 92 to
+// 124 bytes of scratch a lane are left, and of odd rows 550 to 600).
 template <typename T, int TPR, int VPT, int VEC>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) lores_block_backward_kernel(const BlockArgs a) {
     constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;

@@ -6,9 +6,10 @@
 //   gate first: e = dy w,  du = r (e - n mean(e n)),  dx = du a,  dz = du x s,  dw = sum dy n
 //
 // Bound by memory: a row is read once, kept in registers and written once.  8192 x 32 x 128
-// bf16: forward 39 us, 5.2 TB/s, backward 74, 4.5 TB/s (with 33 M elements of fp32 35 and 74);
-// heads of 100: 38 and 69.  A row takes the fewest threads that hold it in two vectors each
-// (heads of 64 with 16 threads instead of 8: forward 62 instead of 38).
+// bf16, rows that no cache holds: forward 40 us, 5.0 TB/s (to 4-bit rows 41), backward 67 and
+// 5 for the groups' sums, 5.0 TB/s; fp32 73 us, 5.5 TB/s, and 131, 5.1 TB/s; heads of 100 bf16 44
+// and 68.  A row of up to 512 elements takes 8, 16, 32 or 64 threads, one vector each, longer ones
+// 64, 256 or 1024 with one or two (16384 x 32 x 64, 8 threads a row: forward 40 us; 16: 62).
 #include "lores_gate.h"
 #include "lores_layer.h"
 
