@@ -929,8 +929,8 @@ def lores_mx_matmul(a, a_scales, w, w_scales, out_prec=LORES_BF16, out=None, str
     one fp32 factor per row [...] (lores_rmsnorm, lores_block_norm with LORES_FP8).
     out_prec: LORES_BF16, or for 4-bit rows LORES_FP32.  Sums are fp32; of E4M3 rows 8
     neighbours of k are first added on a grid of 2^-13 of the largest product, which
-    shows where sums cancel.  out: a contiguous tensor to write to, or None.  No autograd graph is recorded, and there is no backward
-    operator.
+    shows where sums cancel.  out: a contiguous tensor to write to, or None.  No
+    autograd graph is recorded, and there is no backward operator.
     """
     if torch is None:
         _bind_torch()

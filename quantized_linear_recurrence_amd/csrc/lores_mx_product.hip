@@ -577,7 +577,8 @@ hipError_t go_tile(const MxProduct &p, int residents, hipStream_t s) {
 // 128 x 256 up to 2^23 (256 whole ones), else 256 x 256.  Tiles that a last row or column leaves nearly
 // empty count as whole (sizes just past a multiple are not measured), and with fewer than 256 rows or
 // columns 128 x 128 takes any number.  Of E4M3 rows with K in whole 512 that tile needs 275
-// registers, so one work-group of the two that are launched for a CU runs at a time.  us at K = 4096, 64 x 64 / 128 x 128 / 128 x 256 / 256 x 256:
+// registers, so one work-group of the two that are launched for a CU runs at a time.
+// us at K = 4096, 64 x 64 / 128 x 128 / 128 x 256 / 256 x 256:
 //   outputs           512 x 4096           512 x 8192          1024 x 8192          1536 x 8192
 //   4-bit rows   14.2 15.3 19.6 27.1  24.8 17.6 20.8 27.8  40.2 25.1 25.5 30.7  56.6 38.4 40.4 34.7
 //   E4M3 rows    18.2 21.8 26.5 42.1  31.2 24.2 28.2 42.8  53.7 45.0 34.1 45.9  73.9 63.1 55.7 50.8
